@@ -308,6 +308,115 @@ sv_status spec_kd_loss(int n_seq, int t_len, int V, sv_dtype dtype, const void *
 sv_status spec_kd_launch_shape(int V, sv_dtype dtype, int with_grad, int *cluster, int *buffers,
                                int *grid_ctas);
 
+/* Penalties for repeated tokens, biases and grammar masks on logit rows: what
+ * a rollout applies to the target's (and the drafter's) rows before
+ * spec_verify, so that verification runs on the distribution that is sampled.
+ * No page defines these; the rule is the usual one.  Row i of sequence b
+ * follows its history and its drafts x_{b,0..i-1}.  With n(v) the times v was
+ * generated (the history after the prompt, and those drafts) and seen(v)
+ * whether v was generated or stands in the prompt, in this order:
+ *   z <- z > 0 ? z / r_b : z r_b     where seen(v)     (repetition)
+ *   z <- z - f_b n(v) - p_b          where n(v) > 0    (frequency, presence)
+ *   z <- z + bias_b(v)
+ *   z <- -inf                        where the row's mask has bit v clear
+ * in fp32, rounded once to dtype; a logit to which none of it applies keeps
+ * its bits.
+ *   logits, out   [B, R, V] dtype device; out == logits works in place,
+ *                 otherwise the two may not overlap
+ *   history       [B, .] int32 device, rows history_stride apart, of which
+ *                 the first history_max entries may be read; sequence b's
+ *                 history is its first history_len[b] tokens (NULL:
+ *                 history_max), the first prompt_len[b] of them (NULL: 0)
+ *                 the prompt.  history_max = 0: none
+ *   tokens        [B, k] int32 device, the drafts, or NULL: none counted
+ *   draft_len     [B] int32 device or NULL.  With it R is k + 1 (target
+ *                 rows, i <= k_b) or k (draft rows, i < k_b), and the rows
+ *                 past these are neither read nor written; a length outside
+ *                 [0, k] leaves its whole sequence so (spec_verify reports
+ *                 it).  NULL: every row
+ *   repetition, presence, frequency   [B] fp32 device or NULL (1, 0, 0);
+ *                 repetition > 0
+ *   bias_ids, bias_values   [B, n_bias] int32 / fp32 device; of entries with
+ *                 the same token the last counts.  n_bias = 0: none
+ *   mask          [B, R, ceil(V / 32)] int32 device or NULL: bit v % 32 of
+ *                 word v / 32 set allows token v.  A row that allows nothing
+ *                 becomes all -inf, which spec_verify reports
+ * Token ids outside [0, V) (history, drafts, biases) are passed over.  NaN
+ * and infinities go through the arithmetic above; what the mask forbids is
+ * -inf whatever it held.  k < 32.  Asynchronous on `stream`; no context, no
+ * workspace, no allocation; deterministic.  Host-checkable errors (sizes,
+ * NULL pointers, overlap, pointers not aligned to dtype) return
+ * SV_ERR_INVALID_ARG and launch nothing.  Any V; rows of more than 1 GiB are
+ * SV_ERR_INVALID_ARG. */
+sv_status sv_process_logits(int B, int R, int V, sv_dtype dtype, const void *logits, void *out,
+                            int history_max, long long history_stride, const int32_t *history,
+                            const int32_t *prompt_len, const int32_t *history_len, int k,
+                            const int32_t *tokens, const int32_t *draft_len, const float *repetition,
+                            const float *presence, const float *frequency, int n_bias,
+                            const int32_t *bias_ids, const float *bias_values, const int32_t *mask,
+                            sv_stream_t stream);
+
+/* A teacher's top log-probabilities: of every row the K tokens with the
+ * largest logits (largest first, ties to the lower id) with their
+ * log-probabilities, and the row's log-sum-exp.  Kept in place of the row
+ * (8 K bytes for V logits), they are what spec_kd_top_loss distils from.
+ *   target_logits [n_seq, t_len, V] dtype device, contiguous
+ *   n_rows        [n_seq] int32 device or NULL: only the first n_rows[b] rows
+ *                 of sequence b are taken (spec_verify's out_len: the rows
+ *                 whose tokens were emitted); the others are not read and get
+ *                 ids -1, logp -inf, lse -inf
+ *   K             1 .. SV_KD_TOP_MAX
+ *   temperature   > 0: logp = log softmax(z / T)
+ *   ids, logp     [n_seq, t_len, K] int32 / fp32 device, out
+ *   lse           [n_seq, t_len] fp32 device, out: log sum exp(z / T)
+ * A token with z = -inf is never listed: a row with fewer than K others ends
+ * with ids -1, logp -inf.  A row holding NaN or +inf gets ids -1, logp NaN
+ * and lse NaN, a row that is all -inf ids -1, logp NaN and lse -inf.
+ * Asynchronous on `stream`; no context, no workspace, no allocation;
+ * deterministic.  Errors and limits as for spec_kd_loss. */
+#define SV_KD_TOP_MAX 256
+
+sv_status spec_kd_top(int n_seq, int t_len, int V, sv_dtype dtype, const void *target_logits,
+                      const int32_t *n_rows, int K, float temperature, int32_t *ids, float *logp,
+                      float *lse, sv_stream_t stream);
+
+/* Reward-weighted distillation from such lists, and its gradient in the draft
+ * logits: spec_kd_loss where the teacher's rows are no longer at hand.  With
+ * p_j = exp(logp_j), P = sum p_j, q = softmax(z / T) of the draft row and
+ * Q = sum_j q(id_j):
+ *   SV_KD_TOP_TAIL    the other tokens as one event of probability r = 1 - P
+ *     (below 2^-20, what fp32 log-probabilities cannot tell from rounding, it
+ *     is taken as 0, the list as complete):
+ *     KL = sum_j p_j (log p_j - log q(id_j)) + r (log r - log(1 - Q)),
+ *     grad(x) = w (q(x) - p_j) / T for a listed x, w q(x) (1 - r / (1 - Q)) / T
+ *     for the others;
+ *   SV_KD_TOP_RENORM  the list scaled to sum to one, p_j / P in place of p_j:
+ *     KL = sum_j p_j (log p_j - log q(id_j)),
+ *     grad(x) = w (q(x) - p_j) / T for a listed x, w q(x) / T for the others.
+ *   ids, logp     [n_seq, t_len, K] int32 / fp32 device; entries with id < 0
+ *                 are passed over (whatever their logp, NaN apart)
+ *   draft_logits  [n_seq, t_len, V] dtype device, contiguous
+ *   weights       [n_seq] fp32 device
+ *   row_kl, loss  [n_seq, t_len], [n_seq] fp32 device, out:
+ *                 loss[b] = w_b sum_t row_kl[b, t]
+ *   grad          [n_seq, t_len, V] dtype device, out (bf16: rounded to
+ *                 nearest even), or NULL for the loss alone; may not overlap
+ *                 the logits
+ * A row without a list (every id < 0) has KL 0 and gradient 0 and is not
+ * read.  NaN or +inf in the draft row or the list, a draft row that is all
+ * -inf, an id >= V or one listed twice give a NaN KL, NaN gradient and NaN
+ * loss for the rollout; a listed token with p_j > 0 (or, with r > 0, all
+ * others) at draft logit -inf gives KL = +inf.  K as for spec_kd_top,
+ * V <= 524288.  Asynchronous on `stream`; no context, no workspace, no
+ * allocation; every sum is taken in a fixed order.  Host-checkable errors
+ * return SV_ERR_INVALID_ARG and launch nothing. */
+typedef enum { SV_KD_TOP_TAIL = 0, SV_KD_TOP_RENORM = 1 } sv_kd_top_mode;
+
+sv_status spec_kd_top_loss(int n_seq, int t_len, int V, sv_dtype dtype, int K, const int32_t *ids,
+                           const float *logp, const void *draft_logits, const float *weights,
+                           float temperature, int mode, float *row_kl, float *loss, void *grad,
+                           sv_stream_t stream);
+
 /* Test hook: the limit, in nanoseconds, of each bounded wait for staged logits
  * (default 1 s).  0 makes every wait report expiry, so every sequence that
  * reads a row ends with SV_ERR_TIMEOUT; the copies are still drained (with a

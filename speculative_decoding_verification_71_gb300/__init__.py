@@ -25,7 +25,7 @@ __all__ = [
     "SV_OK", "SV_ERR_INVALID_ARG", "SV_ERR_BAD_DRAFT_LEN", "SV_ERR_BAD_TOKEN",
     "SV_ERR_NONFINITE", "SV_ERR_TIMEOUT", "SV_ERR_CUDA", "SV_ERR_UNSUPPORTED",
     "SV_F32", "SV_BF16", "EXPORTED_SYMBOLS", "DraftController", "verify_tree", "SV_CTRL_BATCH", "SV_CTRL_PER_SEQUENCE",
-    "measure_ex2",
+    "measure_ex2", "process_logits", "kd_top", "kd_top_loss", "SV_KD_TOP_MAX",
 ]
 
 SV_OK, SV_ERR_INVALID_ARG, SV_ERR_BAD_DRAFT_LEN, SV_ERR_BAD_TOKEN = 0, 1, 2, 3
@@ -34,6 +34,8 @@ SV_F32, SV_BF16 = 0, 1
 SV_CTRL_BATCH, SV_CTRL_PER_SEQUENCE = 0, 1
 SV_KERNEL_AUTO, SV_KERNEL_CLUSTER, SV_KERNEL_PIECES = 0, 1, 2
 SV_CTRL_MAX_POINTS = 12
+SV_KD_TOP_TAIL, SV_KD_TOP_RENORM = 0, 1
+SV_KD_TOP_MAX = 256
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_PKG, "libspecverify.so")
@@ -47,7 +49,7 @@ EXPORTED_SYMBOLS = (
     "spec_verify_noalloc", "spec_kd_loss", "spec_kd_launch_shape",
     "spec_ctrl_create", "spec_ctrl_destroy", "spec_ctrl_set_cost", "spec_ctrl_set_params", "spec_ctrl_reset",
     "spec_ctrl_observe", "spec_ctrl_choose", "spec_ctrl_alpha", "spec_ctrl_status",
-    "spec_verify_tree",
+    "spec_verify_tree", "sv_process_logits", "spec_kd_top", "spec_kd_top_loss",
 )
 
 
@@ -156,6 +158,14 @@ def load_library(path: str | None = None):
     lib.spec_verify_tree.restype = c.c_int
     lib.spec_verify_tree.argtypes = [c.c_int, c.c_int, c.c_int, c.c_int, P, P, P, P, P, P, c.c_float,
                                      P, P, P, P, P, P]
+    lib.sv_process_logits.restype = c.c_int
+    lib.sv_process_logits.argtypes = [c.c_int, c.c_int, c.c_int, c.c_int, P, P, c.c_int, c.c_longlong, P, P, P,
+                                      c.c_int, P, P, P, P, P, c.c_int, P, P, P, P]
+    lib.spec_kd_top.restype = c.c_int
+    lib.spec_kd_top.argtypes = [c.c_int, c.c_int, c.c_int, c.c_int, P, P, c.c_int, c.c_float, P, P, P, P]
+    lib.spec_kd_top_loss.restype = c.c_int
+    lib.spec_kd_top_loss.argtypes = [c.c_int, c.c_int, c.c_int, c.c_int, c.c_int, P, P, P, P, c.c_float, c.c_int,
+                                     P, P, P, P]
     lib.spec_verify_noalloc.restype = c.c_int
     lib.spec_verify_noalloc.argtypes = [c.c_int, c.c_int, c.c_int, c.c_int, P, P, P, P, P, c.c_float, P, P, P]
     if path is None:
@@ -457,6 +467,166 @@ def kd_loss(target, draft, weights, temperature=1.0, grad=True, stream=None):
                           _stream_handle(stream))
     if st != SV_OK:
         raise SpecVerifyError(st, "spec_kd_loss")
+    return row_kl, loss, g
+
+
+def _dtype_code(t):
+    if t.dtype == torch.bfloat16:
+        return SV_BF16
+    if t.dtype == torch.float32:
+        return SV_F32
+    raise TypeError("logits must be float32 or bfloat16")
+
+
+def _logit_rows(name, t):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() != 3:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected three dimensions")
+    _check_dev(name, t, t.dtype, t.shape, t.device)
+    return t.shape, t.device, _dtype_code(t)
+
+
+class _on_stream:
+    """The call's device and stream: ``handle`` is what the library launches
+    on.  Tensors allocated inside belong to the stream, so memory that another
+    stream still uses is not handed out."""
+
+    def __init__(self, device, stream):
+        self.device, self.stream = device, stream
+        self.ctx = None
+
+    def __enter__(self):
+        if self.stream is not None:
+            self.ctx = torch.cuda.stream(self.stream)
+        elif self.device.index != torch.cuda.current_device():
+            self.ctx = torch.cuda.device(self.device)
+        if self.ctx is not None:
+            self.ctx.__enter__()
+        self.handle = torch.cuda.current_stream().cuda_stream
+        return self
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+
+
+def process_logits(logits, history=None, prompt_len=None, history_len=None, tokens=None, draft_len=None,
+                   repetition=None, presence=None, frequency=None, bias_ids=None, bias_values=None, mask=None,
+                   out=None, stream=None):
+    """Penalties, biases and grammar masks on logit rows (``sv_process_logits``
+    in include/specverify.h): what a rollout applies to target or draft rows
+    before ``SpecVerifier.verify``.
+
+    logits [B, R, V] float32 or bfloat16; row i of a sequence follows its
+    history and its first i drafts.  history [B, H] int32 (rows may be
+    strided), of which the first history_len [B] tokens count and the first
+    prompt_len [B] of those are the prompt; tokens [B, k] int32 and draft_len
+    [B] int32 with R = k + 1 (target rows) or R = k (draft rows), rows past
+    the drafts left alone; repetition, presence, frequency [B] float32;
+    bias_ids [B, M] int32 with bias_values [B, M] float32; mask
+    [B, R, ceil(V / 32)] int32, a set bit allows its token.  ``out=logits``
+    works in place; without ``out`` the result is a new tensor (whose rows
+    past the drafts are not set).  Returns the result."""
+    lib = load_library()
+    (B, R, V), dev, code = _logit_rows("logits", logits)
+    i32, f32 = torch.int32, torch.float32
+    H = stride = k = M = 0
+    if history is not None:
+        if not isinstance(history, torch.Tensor):
+            raise TypeError("history must be a torch.Tensor")
+        if history.device != dev:
+            raise ValueError(f"history is on {history.device}, expected {dev}")
+        if history.dtype != i32:
+            raise TypeError(f"history has dtype {history.dtype}, expected {i32}")
+        if history.dim() != 2 or history.shape[0] != B:
+            raise ValueError(f"history has shape {tuple(history.shape)}, expected ({B}, H)")
+        H = history.shape[1]
+        stride = history.stride(0) if B > 1 else H
+        if H > 1 and history.stride(1) != 1 or stride < H:
+            raise ValueError("history must have contiguous rows that do not overlap")
+    elif prompt_len is not None or history_len is not None:
+        raise ValueError("prompt_len and history_len describe a history")
+    _check_dev("prompt_len", prompt_len, i32, (B,), dev)
+    _check_dev("history_len", history_len, i32, (B,), dev)
+    if tokens is not None:
+        k = tokens.shape[1] if isinstance(tokens, torch.Tensor) and tokens.dim() == 2 else R - 1
+        _check_dev("tokens", tokens, i32, (B, k), dev)
+        if R not in (k, k + 1):
+            raise ValueError(f"{R} rows for {k} drafts: expected {k} or {k + 1}")
+    elif draft_len is not None:
+        k = R - 1
+    _check_dev("draft_len", draft_len, i32, (B,), dev)
+    _check_dev("repetition", repetition, f32, (B,), dev)
+    _check_dev("presence", presence, f32, (B,), dev)
+    _check_dev("frequency", frequency, f32, (B,), dev)
+    if (bias_ids is None) != (bias_values is None):
+        raise ValueError("bias_ids and bias_values go together")
+    if bias_ids is not None:
+        M = bias_ids.shape[1] if isinstance(bias_ids, torch.Tensor) and bias_ids.dim() == 2 else 0
+        _check_dev("bias_ids", bias_ids, i32, (B, M), dev)
+        _check_dev("bias_values", bias_values, f32, (B, M), dev)
+    _check_dev("mask", mask, i32, (B, R, (V + 31) // 32), dev)
+    _check_dev("out", out, logits.dtype, (B, R, V), dev)
+    with _on_stream(dev, stream) as on:
+        if out is None:
+            out = torch.empty_like(logits)
+        st = lib.sv_process_logits(B, R, V, code, _ptr(logits), _ptr(out), H, stride, _ptr(history),
+                                   _ptr(prompt_len), _ptr(history_len), k, _ptr(tokens), _ptr(draft_len),
+                                   _ptr(repetition), _ptr(presence), _ptr(frequency), M, _ptr(bias_ids),
+                                   _ptr(bias_values), _ptr(mask), on.handle)
+    if st != SV_OK:
+        raise SpecVerifyError(st, "sv_process_logits")
+    return out
+
+
+def kd_top(target, k, temperature=1.0, n_rows=None, stream=None):
+    """The k most likely tokens of each teacher row (``spec_kd_top`` in
+    include/specverify.h).  target [n_seq, t_len, V] float32 or bfloat16;
+    n_rows [n_seq] int32: only a sequence's first rows are taken (pass
+    ``verify``'s out_len).  Returns (ids [n_seq, t_len, k] int32, logp
+    [n_seq, t_len, k] float32, lse [n_seq, t_len] float32), likeliest first;
+    entries without a token have id -1 and logp -inf."""
+    lib = load_library()
+    (n_seq, t_len, V), dev, code = _logit_rows("target", target)
+    k = int(k)
+    if not 1 <= k <= SV_KD_TOP_MAX:
+        raise ValueError(f"k is {k}, expected 1..{SV_KD_TOP_MAX}")
+    _check_dev("n_rows", n_rows, torch.int32, (n_seq,), dev)
+    with _on_stream(dev, stream) as on:
+        ids = torch.empty((n_seq, t_len, k), dtype=torch.int32, device=dev)
+        logp = torch.empty((n_seq, t_len, k), dtype=torch.float32, device=dev)
+        lse = torch.empty((n_seq, t_len), dtype=torch.float32, device=dev)
+        st = lib.spec_kd_top(n_seq, t_len, V, code, _ptr(target), _ptr(n_rows), k, float(temperature), _ptr(ids),
+                             _ptr(logp), _ptr(lse), on.handle)
+    if st != SV_OK:
+        raise SpecVerifyError(st, "spec_kd_top")
+    return ids, logp, lse
+
+
+def kd_top_loss(ids, logp, draft, weights, temperature=1.0, tail=True, grad=True, stream=None):
+    """Distillation loss of the draft from ``kd_top``'s lists and its gradient
+    in the draft logits (``spec_kd_top_loss`` in include/specverify.h).  ids,
+    logp [n_seq, t_len, K] int32 / float32; draft [n_seq, t_len, V] float32 or
+    bfloat16; weights [n_seq] float32.  ``tail``: the unlisted tokens are one
+    event with the rest of the probability; otherwise the list is scaled to
+    sum to one.  Returns (row_kl [n_seq, t_len] float32, loss [n_seq] float32,
+    grad [n_seq, t_len, V] in the logits' dtype or None)."""
+    lib = load_library()
+    (n_seq, t_len, V), dev, code = _logit_rows("draft", draft)
+    K = ids.shape[2] if isinstance(ids, torch.Tensor) and ids.dim() == 3 else 0
+    _check_dev("ids", ids, torch.int32, (n_seq, t_len, K), dev)
+    _check_dev("logp", logp, torch.float32, (n_seq, t_len, K), dev)
+    _check_dev("weights", weights, torch.float32, (n_seq,), dev)
+    with _on_stream(dev, stream) as on:
+        row_kl = torch.empty((n_seq, t_len), dtype=torch.float32, device=dev)
+        loss = torch.empty((n_seq,), dtype=torch.float32, device=dev)
+        g = torch.empty_like(draft) if grad else None
+        st = lib.spec_kd_top_loss(n_seq, t_len, V, code, K, _ptr(ids), _ptr(logp), _ptr(draft), _ptr(weights),
+                                  float(temperature), SV_KD_TOP_TAIL if tail else SV_KD_TOP_RENORM, _ptr(row_kl),
+                                  _ptr(loss), _ptr(g), on.handle)
+    if st != SV_OK:
+        raise SpecVerifyError(st, "spec_kd_top_loss")
     return row_kl, loss, g
 
 
