@@ -331,7 +331,7 @@ sv_status spec_kd_launch_shape(int V, sv_dtype dtype, int with_grad, int *cluste
  *   tokens        [B, k] int32 device, the drafts, or NULL: none counted
  *   draft_len     [B] int32 device or NULL.  With it R is k + 1 (target
  *                 rows, i <= k_b) or k (draft rows, i < k_b), and the rows
- *                 past these are neither read nor written; a length outside
+ *                 past these are neither used nor written; a length outside
  *                 [0, k] leaves its whole sequence so (spec_verify reports
  *                 it).  NULL: every row
  *   repetition, presence, frequency   [B] fp32 device or NULL (1, 0, 0);
@@ -343,11 +343,14 @@ sv_status spec_kd_launch_shape(int V, sv_dtype dtype, int with_grad, int *cluste
  *                 becomes all -inf, which spec_verify reports
  * Token ids outside [0, V) (history, drafts, biases) are passed over.  NaN
  * and infinities go through the arithmetic above; what the mask forbids is
- * -inf whatever it held.  k < 32.  Asynchronous on `stream`; no context, no
+ * -inf whatever it held.  k < 32, n_bias <= SV_MAX_BIASES, history_max <
+ * 2^20.  Asynchronous on `stream`; no context, no
  * workspace, no allocation; deterministic.  Host-checkable errors (sizes,
  * NULL pointers, overlap, pointers not aligned to dtype) return
  * SV_ERR_INVALID_ARG and launch nothing.  Any V; rows of more than 1 GiB are
  * SV_ERR_INVALID_ARG. */
+#define SV_MAX_BIASES 1023
+
 sv_status sv_process_logits(int B, int R, int V, sv_dtype dtype, const void *logits, void *out,
                             int history_max, long long history_stride, const int32_t *history,
                             const int32_t *prompt_len, const int32_t *history_len, int k,

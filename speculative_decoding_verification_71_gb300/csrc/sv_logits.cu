@@ -43,10 +43,12 @@ namespace {
 constexpr int kLgThreads = 256;
 constexpr int kLgCtas = 4;                // resident per SM
 constexpr int kLgMaxDrafts = 32;
-constexpr uint32_t kLgPrompt = 1u << 31;  // table word: in the prompt
-constexpr uint32_t kLgDraft = 1u << 30;   // ... among the drafts
-constexpr uint32_t kLgBias = 1u << 29;    // ... has a bias
-constexpr uint32_t kLgCount = kLgBias - 1;    // ... times generated in the history
+// A table word: in the prompt, among the drafts, the last bias's entry + 1
+// and the times generated in the history.
+constexpr uint32_t kLgPrompt = 1u << 31, kLgDraft = 1u << 30;
+constexpr int kLgBiasShift = 20;
+constexpr uint32_t kLgBias = (kLgDraft - 1) >> kLgBiasShift << kLgBiasShift;   // 10 bits
+constexpr uint32_t kLgCount = (1u << kLgBiasShift) - 1;
 constexpr int kLgPad = 8;                 // tokens before the slice that a shifted row's vectors reach
 
 struct LogitsParams {
@@ -66,12 +68,15 @@ struct LogitsParams {
   long long history_stride;
   int history_max;
   int B, R, V, k, n_bias;
+  int parts;                     // passes of 256 U vectors that a slice takes per row
+  int list_max;                  // tokens that a table can hold at most
+  int history_vec;               // history rows lie on 16 bytes
   int table;                     // there is something to look up: history, drafts or biases
   int same_shift;                // logits and out lie alike: rows go as 16-byte vectors
 };
 
 // Words of the bitmap over a table of `span` tokens: whole 16-byte units.
-#define SV_LG_BITMAP_WORDS(span) (((span) + 127) / 128 * 4)
+__host__ __device__ constexpr int lg_bitmap_words(int span) { return (span + 127) / 128 * 4; }
 
 // Element by element a where the bit is set, else b: bit copies, so that a
 // value that stays keeps its bits (a conversion would not keep a NaN's).
@@ -103,159 +108,234 @@ __device__ __noinline__ void edge_vector(const unsigned char* in, unsigned char*
   }
 }
 
-// A thread's vectors of one row's slice: what the mask says of them and, where
-// they have to be read, their values.
-template <int ELT, int U>
+// A thread's vectors of one pass over a row: what the mask says of them and,
+// where they have to be read, their values.
+template <int ELT, int U, bool MASK>
 struct RowPart {
   uint4 w[U];
-  uint32_t allowed[U];
+  uint32_t allowed[MASK ? U : 1];
 
   static constexpr int N = Vec<ELT>::N;
+  static constexpr int kTokens = kLgThreads * U * N;
   static constexpr uint32_t kAll = (1u << N) - 1u;
 
-  __device__ __forceinline__ static int token(int q, int s0, int shift) {
-    return s0 - shift + (static_cast<int>(threadIdx.x) + q * kLgThreads) * N;
+  // Token of vector q of a pass from token s on.
+  __device__ __forceinline__ static int token(int q, int s) {
+    return s + (static_cast<int>(threadIdx.x) + q * kLgThreads) * N;
   }
+  // s: first token of the pass less the row's shift.  A pass inside its row
+  // needs no look at the row's ends.
+  __device__ __forceinline__ static bool inside(const LogitsParams& P, int s) {
+    return P.same_shift && s >= 0 && s <= P.V - kTokens;
+  }
+  __device__ __forceinline__ static bool whole(const LogitsParams& P, int t0) {
+    return P.same_shift && t0 >= 0 && t0 <= P.V - N;
+  }
+
   __device__ __forceinline__ void load(const LogitsParams& P, long long r, int s0, bool in_place) {
     const unsigned char* in = P.logits + r * P.V * ELT;
-    const int* mask = P.mask ? P.mask + r * ((P.V + 31) / 32) : nullptr;
-    const int shift = row_shift<ELT>(in);
+    const int s = s0 - row_shift<ELT>(in);
+    const unsigned char* at = in + static_cast<long long>(token(0, s)) * ELT;
+    const bool all = inside(P, s);
+    if (MASK) {
+      const int* mask = P.mask + r * ((P.V + 31) / 32);
 #pragma unroll
-    for (int q = 0; q < U; ++q) {
-      const int t0 = token(q, s0, shift);
-      const bool whole = P.same_shift && t0 >= 0 && t0 <= P.V - N;
-      allowed[q] = mask && whole ? bits_at<N>(mask, t0) : kAll;
-    }
+      for (int q = 0; q < U; ++q)
+        allowed[q] = all || whole(P, token(q, s)) ? bits_at<N>(mask, token(q, s)) : 0u;
 #pragma unroll
-    for (int q = 0; q < U; ++q) {
-      const int t0 = token(q, s0, shift);
-      const bool whole = P.same_shift && t0 >= 0 && t0 <= P.V - N;
-      if (whole && allowed[q] && !(in_place && allowed[q] == kAll)) w[q] = load_vec16(in + static_cast<long long>(t0) * ELT);
+      for (int q = 0; q < U; ++q)
+        if (allowed[q] && !(in_place && allowed[q] == kAll)) w[q] = load_vec16(at + q * kLgThreads * 16);
+    } else if (all) {
+#pragma unroll
+      for (int q = 0; q < U; ++q) w[q] = load_vec16(at + q * kLgThreads * 16);
+    } else {
+#pragma unroll
+      for (int q = 0; q < U; ++q)
+        if (whole(P, token(q, s))) w[q] = load_vec16(at + q * kLgThreads * 16);
     }
   }
   __device__ __forceinline__ void store(const LogitsParams& P, long long r, int s0, bool in_place) const {
     const unsigned char* in = P.logits + r * P.V * ELT;
     unsigned char* out = P.out + r * P.V * ELT;
-    const int shift = row_shift<ELT>(in);
+    const int s = s0 - row_shift<ELT>(in);
+    unsigned char* at = out + static_cast<long long>(token(0, s)) * ELT;
+    if (inside(P, s)) {
+#pragma unroll
+      for (int q = 0; q < U; ++q)
+        if (!(MASK && in_place && allowed[q] == kAll)) store_vec16(at + q * kLgThreads * 16, masked(q));
+      return;
+    }
 #pragma unroll
     for (int q = 0; q < U; ++q) {
-      const int t0 = token(q, s0, shift);
-      if (P.same_shift && t0 >= 0 && t0 <= P.V - N) {
-        if (in_place && allowed[q] == kAll) continue;
-        uint4 res = w[q];
-        if (allowed[q] != kAll)
-          res = allowed[q] ? select<ELT>(allowed[q], res, Vec<ELT>::neg_inf()) : Vec<ELT>::neg_inf();
-        store_vec16(out + static_cast<long long>(t0) * ELT, res);
-      } else if (t0 < P.V) {
-        edge_vector<ELT>(in, out, P.mask ? P.mask + r * ((P.V + 31) / 32) : nullptr, t0, P.V);
+      if (whole(P, token(q, s))) {
+        if (!(MASK && in_place && allowed[q] == kAll)) store_vec16(at + q * kLgThreads * 16, masked(q));
+      } else if (token(q, s) < P.V) {
+        edge_vector<ELT>(in, out, MASK ? P.mask + r * ((P.V + 31) / 32) : nullptr, token(q, s), P.V);
       }
     }
   }
+  __device__ __forceinline__ uint4 masked(int q) const {
+    if (!MASK || allowed[MASK ? q : 0] == kAll) return w[q];
+    if (!allowed[MASK ? q : 0]) return Vec<ELT>::neg_inf();
+    return select<ELT>(allowed[MASK ? q : 0], w[q], Vec<ELT>::neg_inf());
+  }
 };
 
-// A batch of history tokens, kLgAhead per thread from entry j0 + thread on;
-// -1 past history_max.
-constexpr int kLgAhead = 8;
-__device__ __forceinline__ void load_history(const int* h, int j0, int end, int (&t)[kLgAhead]) {
+// A batch of history tokens, 4 kLgAhead per thread: entries
+// lg_entry(j0, q) .. + 3; -1 from `end` on.
+constexpr int kLgAhead = 4;
+constexpr int kLgBatch = kLgThreads * 4 * kLgAhead;
+__device__ __forceinline__ int lg_entry(int j0, int q) { return j0 + (static_cast<int>(threadIdx.x) + q * kLgThreads) * 4; }
+__device__ __forceinline__ void load_history(const int* h, int j0, int end, int vec, int4 (&t)[kLgAhead]) {
 #pragma unroll
   for (int q = 0; q < kLgAhead; ++q) {
-    const int j = j0 + static_cast<int>(threadIdx.x) + q * kLgThreads;
-    t[q] = j < end ? h[j] : -1;
+    const int j = lg_entry(j0, q);
+    if (j >= end) {
+      t[q] = make_int4(-1, -1, -1, -1);
+    } else if (vec && j + 3 < end) {
+      t[q] = *reinterpret_cast<const int4*>(h + j);
+    } else {
+      t[q].x = j < end ? h[j] : -1;
+      t[q].y = j + 1 < end ? h[j + 1] : -1;
+      t[q].z = j + 2 < end ? h[j + 2] : -1;
+      t[q].w = j + 3 < end ? h[j + 3] : -1;
+    }
   }
 }
 
-// U vectors of a row per thread: slices of 256 U vectors.
-template <int ELT, int U>
+// A token of the table in one row: what its correction reads.
+struct LogitsFix {
+  uint32_t word;     // the table's
+  float z, bias;
+  bool mine;
+
+  template <int ELT>
+  __device__ __forceinline__ void load(const LogitsParams& P, long long r, int s0, int n_slice, uint32_t w, int u, int b) {
+    const unsigned char* row = P.logits + r * P.V * ELT;
+    const int t = s0 - kLgPad + u;
+    word = w;
+    // the copy of the row's tokens from s0 - shift on is this CTA's; its
+    // neighbour marks the few before s0 too
+    mine = static_cast<unsigned>(u - kLgPad + row_shift<ELT>(row)) < static_cast<unsigned>(n_slice) &&
+           mask_allows(P.mask ? P.mask + r * ((P.V + 31) / 32) : nullptr, t);
+    z = load_elem<ELT>(row, t);
+    if (word & kLgBias) bias = P.bias_values[static_cast<long long>(b) * P.n_bias + ((word & kLgBias) >> kLgBiasShift) - 1];
+  }
+};
+
+// U vectors of a row per thread and pass.
+template <int ELT, int U, bool MASK>
 __global__ void __launch_bounds__(kLgThreads, kLgCtas) logits_kernel(const __grid_constant__ LogitsParams P) {
   using VT = Vec<ELT>;
-  constexpr int kSlice = kLgThreads * U * VT::N;   // tokens
-  constexpr int span = kSlice + kLgPad;            // tokens the table covers
-  constexpr int kBitmap = SV_LG_BITMAP_WORDS(span);
+  constexpr int kPart = kLgThreads * U * VT::N;    // tokens of a pass
+  const int n_slice = kPart * P.parts;             // ... of the slice
+  const int span = n_slice + kLgPad;               // ... of the table
+  const int n_bitmap = lg_bitmap_words(span);
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ int drafts[kLgMaxDrafts];
   __shared__ int n_listed;
+  __shared__ float numbers[3];                     // repetition, presence, frequency
   uint32_t* tab = reinterpret_cast<uint32_t*>(smem);
   uint32_t* touched = tab + span;                                  // bitmap over the table
-  int* slot = reinterpret_cast<int*>(touched + kBitmap);           // biases: last entry + 1, with biases only
-  uint16_t* list = reinterpret_cast<uint16_t*>(slot + (P.n_bias ? span : 0));
+  uint16_t* list = reinterpret_cast<uint16_t*>(touched + n_bitmap);   // [list_max]
   const int tid = threadIdx.x;
   // slice-major: a vocabulary's first tokens are its most frequent, so the
   // slices with the most to look up go first
-  const int b = blockIdx.x % P.B, s0 = blockIdx.x / P.B * kSlice, first = s0 - kLgPad;
+  const int b = blockIdx.x % P.B, s0 = blockIdx.x / P.B * n_slice, first = s0 - kLgPad;
   const long long r0 = static_cast<long long>(b) * P.R;
   const bool in_place = P.logits == P.out;
-  const bool copies = !in_place || P.mask;
+  const bool copies = MASK || !in_place;
 
   // ---- every load whose address is known goes out at once
   const int kb = P.draft_len ? P.draft_len[b] : P.k;
   const int* h = P.history + b * P.history_stride;
-  int t[kLgAhead];
+  int4 t[kLgAhead];
   int len = 0, plen = 0;
   if (P.history) {
     len = P.history_len ? P.history_len[b] : P.history_max;
     plen = P.prompt_len ? P.prompt_len[b] : 0;
-    load_history(h, 0, P.history_max, t);
+    load_history(h, 0, P.history_max, P.history_vec, t);
   }
-  RowPart<ELT, U> part;
+  RowPart<ELT, U, MASK> part;
   if (copies) part.load(P, r0, s0, in_place);
 
   // ---- the table of the slice's tokens
   int n_fixes = 0;
   if (P.table) {
     uint4* zero = reinterpret_cast<uint4*>(smem);
-    for (int w = tid; w < (span + kBitmap + (P.n_bias ? span : 0)) / 4; w += kLgThreads) zero[w] = make_uint4(0, 0, 0, 0);
-    if (tid == 0) n_listed = 0;
+    for (int w = tid; w < (span + n_bitmap) / 4; w += kLgThreads) zero[w] = make_uint4(0, 0, 0, 0);
+    if (tid == 0) {
+      n_listed = 0;
+      numbers[0] = P.repetition ? P.repetition[b] : 1.f;
+    }
+    if (tid == 1) numbers[1] = P.presence ? P.presence[b] : 0.f;
+    if (tid == 2) numbers[2] = P.frequency ? P.frequency[b] : 0.f;
   }
   if (kb < 0 || kb > P.k) return;                // the verifier reports it
   const int rows = P.draft_len ? min(P.R, kb + (P.R - P.k)) : P.R;
   const int n_drafts = P.tokens ? kb : 0;
-  int fix_u = -1;                                // this thread's first (token, row) pair
-  float fix_z = 0.f;
+  LogitsFix fix;                                 // this thread's first (token, row) pair
   if (P.table) {
     if (tid < n_drafts) drafts[tid] = P.tokens[static_cast<long long>(b) * P.k + tid];
     __syncthreads();
     auto touch = [&](int u) { atomicOr(&touched[u >> 5], 1u << (u & 31)); };
-    if (P.history) {
-      len = min(len, P.history_max);
-      const int end = min(span, P.V - first);    // places of tokens in [0, V)
-      const int start = max(0, -first);
-      for (int j0 = 0; j0 < len; j0 += kLgThreads * kLgAhead) {
-        int ahead[kLgAhead];
-        load_history(h, j0 + kLgThreads * kLgAhead, len, ahead);
-#pragma unroll
-        for (int q = 0; q < kLgAhead; ++q) {
-          const int j = j0 + tid + q * kLgThreads;
-          const int u = t[q] < 0 ? -1 : t[q] - first;
-          const bool in = u >= start && u < end && j < len;
-          if (in && j >= plen) atomicAdd(&tab[u], 1u);
-          if (in && j < plen) atomicOr(&tab[u], kLgPrompt);
-          if (in) touch(u);
-          t[q] = ahead[q];
-        }
-      }
-    }
     // a token's place in this CTA's table, or -1
     auto place = [&](int x) {
       const int u = x - first;
       return x >= 0 && x < P.V && static_cast<unsigned>(u) < static_cast<unsigned>(span) ? u : -1;
     };
-    auto mark = [&](int u, uint32_t flag) {
-      atomicOr(&tab[u], flag);
-      touch(u);
-    };
+    if (P.n_bias) {   // the largest entry wins a token's word, before anything is added to it
+      const int* ids = P.bias_ids + static_cast<long long>(b) * P.n_bias;
+      for (int j = tid; j < P.n_bias; j += kLgThreads) {
+        const int u = place(ids[j]);
+        if (u >= 0) atomicMax(&tab[u], static_cast<uint32_t>(j + 1) << kLgBiasShift), touch(u);
+      }
+      __syncthreads();
+    }
     if (tid < n_drafts) {
       const int u = place(drafts[tid]);
-      if (u >= 0) mark(u, kLgDraft);
+      if (u >= 0) atomicOr(&tab[u], kLgDraft), touch(u);
     }
-    // the last bias of a token counts: the largest entry wins the token's word
-    const int* ids = P.bias_ids + static_cast<long long>(b) * P.n_bias;
-    for (int j = tid; j < P.n_bias; j += kLgThreads) {
-      const int u = place(ids[j]);
-      if (u >= 0) atomicMax(&slot[u], j + 1), mark(u, kLgBias);
+    if (P.history) {
+      len = min(len, P.history_max);
+      // places of the tokens in [0, V) from `base` on: unsigned, so that what
+      // lies before the slice, a -1 or any other id out of range is past them
+      const int base = max(0, first), skipped = base - first;
+      const uint32_t count = static_cast<uint32_t>(max(0, min(span - skipped, P.V - base)));
+      uint32_t* const words = tab + skipped;
+      auto add = [&](int x) {
+        const uint32_t u = static_cast<uint32_t>(x) - static_cast<uint32_t>(base);
+        if (u < count) atomicAdd(&words[u], 1u);
+        if (u < count) touch(static_cast<int>(u) + skipped);
+      };
+      auto add_prompt = [&](int x) {
+        const uint32_t u = static_cast<uint32_t>(x) - static_cast<uint32_t>(base);
+        if (u < count) atomicOr(&words[u], kLgPrompt);
+        if (u < count) touch(static_cast<int>(u) + skipped);
+      };
+      for (int j0 = 0; j0 < len; j0 += kLgBatch) {
+        if (j0 > 0) load_history(h, j0, len, P.history_vec, t);
+#pragma unroll
+        for (int q = 0; q < kLgAhead; ++q) {
+          const int j = lg_entry(j0, q);
+          if (j >= len) break;
+          if (j >= plen && j + 3 < len) {
+            add(t[q].x); add(t[q].y); add(t[q].z); add(t[q].w);
+          } else if (j + 3 < plen && j + 3 < len) {
+            add_prompt(t[q].x); add_prompt(t[q].y); add_prompt(t[q].z); add_prompt(t[q].w);
+          } else {
+            for (int e = 0; e < 4 && j + e < len; ++e) {
+              const int x = e == 0 ? t[q].x : e == 1 ? t[q].y : e == 2 ? t[q].z : t[q].w;
+              if (j + e < plen) add_prompt(x);
+              else add(x);
+            }
+          }
+        }
+      }
     }
     __syncthreads();
     // the list of the tokens that the table holds
-    for (int w = tid; w < kBitmap; w += kLgThreads) {
+    for (int w = tid; w < n_bitmap; w += kLgThreads) {
       uint32_t bits = touched[w];
       if (!bits) continue;
       int at = atomicAdd(&n_listed, __popc(bits));
@@ -263,18 +343,19 @@ __global__ void __launch_bounds__(kLgThreads, kLgCtas) logits_kernel(const __gri
     }
     __syncthreads();
     n_fixes = n_listed * rows;
-    if (tid < n_fixes) {   // its logit arrives during the copy
-      fix_u = list[tid / rows];
-      const int x = min(max(first + fix_u, 0), P.V - 1);
-      fix_z = load_elem<ELT>(P.logits + (r0 + tid % rows) * P.V * ELT, x);
+    if (tid < n_fixes) {   // what it reads arrives during the copy
+      const int i = tid % rows;
+      fix.load<ELT>(P, r0 + i, s0, n_slice, tab[list[tid / rows]], list[tid / rows], b);
     }
   }
 
-  // ---- the mask and the copy, a row ahead
-  for (int i = 0; copies && i < rows; ++i) {
-    RowPart<ELT, U> ahead;
-    if (i + 1 < rows) ahead.load(P, r0 + i + 1, s0, in_place);
-    part.store(P, r0 + i, s0, in_place);
+  // ---- the mask and the copy, a pass ahead
+  for (int i = 0, q = 0; copies && i < rows;) {
+    const int at = i, of = q;
+    if (++q == P.parts) q = 0, ++i;
+    RowPart<ELT, U, MASK> ahead;
+    if (i < rows) ahead.load(P, r0 + i, s0 + q * kPart, in_place);
+    part.store(P, r0 + at, s0 + of * kPart, in_place);
     part = ahead;
   }
   if (n_fixes == 0) return;
@@ -282,35 +363,26 @@ __global__ void __launch_bounds__(kLgThreads, kLgCtas) logits_kernel(const __gri
   // ---- the tokens of the table, their stores after the copy's: a thread for
   // each token of each row
   __syncthreads();
-  const float rep = P.repetition ? P.repetition[b] : 1.f, pres = P.presence ? P.presence[b] : 0.f,
-              freq = P.frequency ? P.frequency[b] : 0.f;
-  const int mask_words = (P.V + 31) / 32;
   for (int j = tid; j < n_fixes; j += kLgThreads) {
-    const bool have = j == tid;
-    const int i = j % rows, u = have ? fix_u : list[j / rows], x = first + u;
-    const uint32_t c = tab[u];
-    int n = static_cast<int>(c & kLgCount);
-    if (c & kLgDraft)
-      for (int d = 0; d < min(i, n_drafts); ++d) n += drafts[d] == x;
-    const bool seen = n > 0 || (c & kLgPrompt);
-    if (!seen && !(c & kLgBias)) continue;   // drafted only later
-    // the copy of the row's tokens from s0 - shift on is this CTA's; its
-    // neighbour marks the few before s0 too
-    const long long r = r0 + i;
-    const unsigned char* rowp = P.logits + r * P.V * ELT;
-    if (static_cast<unsigned>(u - kLgPad + row_shift<ELT>(rowp)) >= static_cast<unsigned>(kSlice)) continue;
-    if (!mask_allows(P.mask ? P.mask + r * mask_words : nullptr, x)) continue;
-    float z = have ? fix_z : load_elem<ELT>(rowp, x);
-    if (seen) z = z > 0.f ? __fdiv_rn(z, rep) : __fmul_rn(z, rep);
-    if (n > 0) z = __fsub_rn(__fsub_rn(z, __fmul_rn(freq, static_cast<float>(n))), pres);
-    if (c & kLgBias) z = __fadd_rn(z, P.bias_values[static_cast<long long>(b) * P.n_bias + slot[u] - 1]);
-    VT::store_rounded(P.out + (r * P.V + x) * ELT, 0, z);
+    const int i = j % rows, u = list[j / rows];
+    if (j != tid) fix.load<ELT>(P, r0 + i, s0, n_slice, tab[u], u, b);
+    if (!fix.mine) continue;
+    int n = static_cast<int>(fix.word & kLgCount);
+    if (fix.word & kLgDraft)
+      for (int d = 0; d < min(i, n_drafts); ++d) n += drafts[d] == first + u;
+    const bool seen = n > 0 || (fix.word & kLgPrompt);
+    if (!seen && !(fix.word & kLgBias)) continue;   // drafted only later
+    float z = fix.z;
+    if (seen) z = z > 0.f ? __fdiv_rn(z, numbers[0]) : __fmul_rn(z, numbers[0]);
+    if (n > 0) z = __fsub_rn(__fsub_rn(z, __fmul_rn(numbers[2], static_cast<float>(n))), numbers[1]);
+    if (fix.word & kLgBias) z = __fadd_rn(z, fix.bias);
+    VT::store_rounded(P.out + ((r0 + i) * P.V + first + u) * ELT, 0, z);
   }
 }
 
-int logits_smem(int n_tokens, bool table, bool with_bias) {
+int logits_smem(int n_tokens, int list_max) {
   const int span = n_tokens + kLgPad;
-  return table ? span * (with_bias ? 10 : 6) + 4 * SV_LG_BITMAP_WORDS(span) : 0;
+  return 4 * (span + lg_bitmap_words(span)) + (list_max + 1) / 2 * 4;
 }
 
 }  // namespace
@@ -324,11 +396,11 @@ extern "C" sv_status sv_process_logits(int B, int R, int V, sv_dtype dtype, cons
                                        const int32_t* bias_ids, const float* bias_values, const int32_t* mask,
                                        sv_stream_t stream) {
   using namespace sv;
-  if (B < 1 || R < 1 || V < 1 || k < 0 || k >= kLgMaxDrafts || n_bias < 0 || history_max < 0) return SV_ERR_INVALID_ARG;
+  if (B < 1 || R < 1 || V < 1 || k < 0 || k >= kLgMaxDrafts || n_bias < 0 || n_bias > SV_MAX_BIASES || history_max < 0) return SV_ERR_INVALID_ARG;
   if (dtype != SV_F32 && dtype != SV_BF16) return SV_ERR_INVALID_ARG;
   if (!logits || !out || (n_bias && (!bias_ids || !bias_values)) || (history_max && !history)) return SV_ERR_INVALID_ARG;
   if ((tokens || draft_len) && R != k && R != k + 1) return SV_ERR_INVALID_ARG;
-  if (history_max >= (1 << 29) || (history_max && history_stride < history_max)) return SV_ERR_INVALID_ARG;
+  if (history_max > static_cast<int>(kLgCount) || (history_max && history_stride < history_max)) return SV_ERR_INVALID_ARG;
   if (static_cast<long long>(B) * R > (1LL << 30)) return SV_ERR_INVALID_ARG;
   const int elt = dtype == SV_F32 ? 4 : 2;
   if (static_cast<long long>(V) * elt > (1LL << 30)) return SV_ERR_INVALID_ARG;
@@ -363,11 +435,16 @@ extern "C" sv_status sv_process_logits(int B, int R, int V, sv_dtype dtype, cons
   const int n = elt == 2 ? 8 : 4;
   int unroll = 1;
   auto slices = [&](int u) { return (V + n - 1 + kLgThreads * u * n - 1) / (kLgThreads * u * n); };
-  const int most = n_bias ? 2 : 4;   // with biases the table is twice as large (34 KB at most)
-  while (unroll < most && static_cast<long long>(B) * slices(2 * unroll) >= 1216) unroll *= 2;
-  const long long ctas = static_cast<long long>(B) * slices(unroll);
+  while (unroll < 4 && static_cast<long long>(B) * slices(2 * unroll) >= 1216) unroll *= 2;
+  // fp32 slices of as many tokens as bf16's: the history is read once a slice
+  p.parts = elt == 4 && unroll == 4 && p.history && static_cast<long long>(B) * slices(8) >= 608 ? 2 : 1;
+  const long long ctas = static_cast<long long>(B) * slices(unroll * p.parts);
   if (ctas > 0x7fffffffLL) return SV_ERR_INVALID_ARG;
-  const int smem = logits_smem(kLgThreads * unroll * n, p.table, n_bias > 0);
+  const int n_tokens = kLgThreads * unroll * n * p.parts;
+  const long long held = (p.history ? history_max : 0LL) + (p.tokens ? k : 0) + n_bias;
+  p.list_max = static_cast<int>(held < n_tokens + kLgPad ? held : n_tokens + kLgPad);
+  p.history_vec = reinterpret_cast<uintptr_t>(history) % 16 == 0 && (history_stride % 4 == 0 || B == 1);
+  const int smem = p.table ? logits_smem(n_tokens, p.list_max) : 0;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   NvtxRange range("sv_process_logits");
   auto launch = [&](auto kernel) {
@@ -378,7 +455,8 @@ extern "C" sv_status sv_process_logits(int B, int R, int V, sv_dtype dtype, cons
     kernel<<<static_cast<unsigned>(ctas), kLgThreads, smem, s>>>(p);
     return cudaGetLastError() == cudaSuccess ? SV_OK : SV_ERR_CUDA;
   };
-  if (elt == 2)
-    return unroll == 4 ? launch(logits_kernel<2, 4>) : unroll == 2 ? launch(logits_kernel<2, 2>) : launch(logits_kernel<2, 1>);
-  return unroll == 4 ? launch(logits_kernel<4, 4>) : unroll == 2 ? launch(logits_kernel<4, 2>) : launch(logits_kernel<4, 1>);
+#define SV_LAUNCH(ELT, U) (mask ? launch(logits_kernel<ELT, U, true>) : launch(logits_kernel<ELT, U, false>))
+  if (elt == 2) return unroll == 4 ? SV_LAUNCH(2, 4) : unroll == 2 ? SV_LAUNCH(2, 2) : SV_LAUNCH(2, 1);
+  return unroll == 4 ? SV_LAUNCH(4, 4) : unroll == 2 ? SV_LAUNCH(4, 2) : SV_LAUNCH(4, 1);
+#undef SV_LAUNCH
 }
