@@ -376,7 +376,7 @@ sv_status sv_process_logits(int B, int R, int V, sv_dtype dtype, const void *log
  * with ids -1, logp -inf.  A row holding NaN or +inf gets ids -1, logp NaN
  * and lse NaN, a row that is all -inf ids -1, logp NaN and lse -inf.
  * Asynchronous on `stream`; no context, no workspace, no allocation;
- * deterministic.  Errors and limits as for spec_kd_loss. */
+ * deterministic.  Errors and limits as for spec_kd_loss, with at most 2^28 rows. */
 #define SV_KD_TOP_MAX 256
 
 sv_status spec_kd_top(int n_seq, int t_len, int V, sv_dtype dtype, const void *target_logits,

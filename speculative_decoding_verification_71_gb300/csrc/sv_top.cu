@@ -9,12 +9,24 @@
 // does not overflow.  The K tokens are those with the largest z, ties
 // to the lower id; a token of probability 0 (z = -inf) is never listed.
 //
-// A CTA takes a row.  The list comes from a radix selection on the values'
-// order-preserving 32-bit keys, eight bits a pass, then of the tokens that
-// tie with the last one those of the lowest ids.
+// A row goes to a cluster of 1 to 8 CTAs, each streaming its part of it once:
+// running maxima and sums per thread for (M, S), and beside them the tokens
+// that can still be in the list.  A token can be left out as soon as K others
+// at or above some t are known and it is below t; t comes from the threads'
+// running maxima: if q = K / 16 lanes of each of the 16 warps have seen a
+// value of at least t, K tokens have.  So t is the least of the warps' q-th
+// largest lane maxima, and a row's candidates are a few times K (some 600 for
+// K = 64 of 152k).  The warps publish their parts of t without a barrier but
+// one, after the first tile (an older part is smaller and lets more through).
+// The cluster's first CTA gathers the candidates at or above the largest of
+// the CTAs' t from their shared memory, selects the K by radix and ranks
+// them.  Candidates that outgrow their buffer (rows of few distinct values,
+// or masked with a finite value) are left, and the first CTA selects from the
+// row itself.
 
 #include <cuda_runtime.h>
 
+#include <cfloat>
 #include <cmath>
 #include <cstdint>
 
@@ -28,6 +40,11 @@ namespace {
 constexpr int kTopThreads = 512;
 constexpr int kTopWarps = kTopThreads / 32;
 constexpr int kTopMaxK = SV_KD_TOP_MAX;
+constexpr int kTopUnroll = 4;             // 16-byte vectors of a tile per thread
+constexpr int kTopTile = kTopThreads * kTopUnroll;
+constexpr int kTopFewRows = 1216;         // CTAs below which a row is split
+constexpr int kTopCap = 4096;             // candidates a CTA can hold: no fewer than the
+                                          // tokens of a part that leaves threads idle
 
 struct TopParams {
   const unsigned char* rows;   // [n_seq, t_len, V]
@@ -38,6 +55,7 @@ struct TopParams {
   int t_len, V, K;
   float c2;                    // log2(e) / T
   float T;
+  int quota;                   // ceil(K / warps)
 };
 
 constexpr uint32_t kKeyNegInf = 0x007fffffu;   // top_key(-inf)
@@ -51,101 +69,148 @@ __device__ __forceinline__ float key_value(uint32_t k) {
   return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xffffffffu));
 }
 
+typedef unsigned long long key64;   // key and id: larger for a larger value, then a lower id
+__device__ __forceinline__ key64 top_entry(uint32_t key, uint32_t id) { return (static_cast<key64>(key) << 32) | ~id; }
+
 struct TopShared {
-  float wm[kTopWarps], ws[kTopWarps];
+  float wm[kTopWarps], ws[kTopWarps];     // the warps' maxima and sums
+  volatile float wt[kTopWarps];           // the warps' parts of t
   unsigned int hist[256];
   unsigned int warp_n[kTopWarps];
-  unsigned int n_found;
-  uint32_t prefix;
-  int remaining;
-  unsigned long long list[kTopMaxK];
+  unsigned int n_found;                   // candidates seen (may pass kTopCap)
+  unsigned int n_list;
+  float M, S, t;                          // this CTA's part
+  int digit, left;
+  key64 list[kTopMaxK];
 };
 
+constexpr int kTopListAt = (static_cast<int>(sizeof(TopShared)) + 15) / 16 * 16;
+constexpr int kTopSmem = kTopListAt + kTopCap * static_cast<int>(sizeof(key64));
+
+// Shared variables of CTA `rank` of the cluster.
+__device__ __forceinline__ float peer_float(const volatile float* p, int rank) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(peer(p, rank)) : "memory");
+  return v;
+}
+__device__ __forceinline__ unsigned int peer_uint(const unsigned int* p, int rank) {
+  unsigned int v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(peer(p, rank)) : "memory");
+  return v;
+}
+__device__ __forceinline__ key64 peer_key(const key64* p, int rank) {
+  key64 v;
+  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(peer(p, rank)) : "memory");
+  return v;
+}
+
+// The warp's lanes' values in descending order.
+__device__ __forceinline__ float warp_sort(float v, int lane) {
+#pragma unroll
+  for (int size = 2; size <= 32; size <<= 1)
+#pragma unroll
+    for (int o = size >> 1; o > 0; o >>= 1) {
+      const float x = __shfl_xor_sync(0xffffffffu, v, o);
+      const bool keep_max = ((lane & o) == 0) == ((lane & size) == 0);
+      v = keep_max ? fmaxf(v, x) : fminf(v, x);
+    }
+  return v;
+}
+
+// Appends the elements of vector v that are at least t.
 template <int ELT>
-__global__ void __launch_bounds__(kTopThreads) top_kernel(const TopParams P) {
+__device__ __noinline__ void append(uint4 w, int t0, float t, key64* cand, unsigned int* n_found) {
+  constexpr int N = Vec<ELT>::N;
+  float z[N];
+  Vec<ELT>::unpack(w, z);
+#pragma unroll
+  for (int e = 0; e < N; ++e)
+    if (z[e] >= t) {
+      const unsigned int at = atomicAdd(n_found, 1u);
+      if (at < kTopCap) cand[at] = top_entry(top_key(z[e]), static_cast<uint32_t>(t0 + e));
+    }
+}
+
+// The bin, from the top, in which the running count of hist reaches `left`
+// (1 <= left <= total), and what is left of `left` in it: by warp 0.
+__device__ __forceinline__ void find_bin(TopShared& sh, int left) {
+  const int lane = threadIdx.x;
+  if (lane < 32) {
+    unsigned int h[8], sum = 0;    // lane 0 has the eight highest bins
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum += h[i] = sh.hist[255 - (lane * 8 + i)];
+    unsigned int before = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned int up = __shfl_up_sync(0xffffffffu, before, o);
+      if (lane >= o) before += up;
+    }
+    before -= sum;
+    if (before < static_cast<unsigned>(left) && before + sum >= static_cast<unsigned>(left)) {
+      int i = 0;
+      for (; i < 7 && before + h[i] < static_cast<unsigned>(left); ++i) before += h[i];
+      sh.digit = 255 - (lane * 8 + i);
+      sh.left = left - static_cast<int>(before);
+    }
+  }
+}
+
+// The n_list largest of n distinct entries (n_list <= n), into sh.list in any
+// order.
+__device__ __forceinline__ void select_entries(TopShared& sh, const key64* cand, int n, int n_list) {
+  const int tid = threadIdx.x;
+  key64 prefix = 0;     // the digits of the n_list-th largest so far, the rest zero
+  if (n > n_list) {
+    int left = n_list;
+    for (int shift = 56; shift >= 0; shift -= 8) {
+      if (tid < 256) sh.hist[tid] = 0;
+      __syncthreads();
+      for (int i = tid; i < n; i += kTopThreads) {
+        const key64 k = cand[i];
+        if (shift == 56 || (k >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&sh.hist[(k >> shift) & 255u], 1u);
+      }
+      __syncthreads();
+      find_bin(sh, left);
+      __syncthreads();
+      prefix |= static_cast<key64>(sh.digit) << shift;
+      left = sh.left;
+      if (static_cast<unsigned>(left) == sh.hist[sh.digit]) break;   // the whole bin
+    }
+  }
+  for (int i = tid; i < n; i += kTopThreads)
+    if (cand[i] >= prefix) sh.list[atomicAdd(&sh.n_list, 1u)] = cand[i];
+  __syncthreads();
+}
+
+// The n_list largest tokens of a row (of which at least n_list are above
+// -inf) from the row itself, into sh.list in any order: a radix selection on
+// the values, then of the tokens that tie with the last one the lowest ids.
+template <int ELT>
+__device__ __noinline__ void select_from_row(TopShared& sh, const unsigned char* row, int V, int n_list) {
   using VT = Vec<ELT>;
   constexpr int N = VT::N;
-  __shared__ TopShared sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const long long r = blockIdx.x;
-  const unsigned char* row = P.rows + r * P.V * ELT;
-  int* ids = P.ids + r * P.K;
-  float* logp = P.logp + r * P.K;
-  if (P.n_rows && static_cast<int>(r % P.t_len) >= P.n_rows[r / P.t_len]) {
-    for (int j = tid; j < P.K; j += kTopThreads) ids[j] = -1, logp[j] = -INFINITY;
-    if (tid == 0) P.lse[r] = -INFINITY;
-    return;
-  }
-  const int shift = row_shift<ELT>(row), nvec = row_vecs<ELT>(P.V, shift);
-
-  // ---- M and S: per thread a running maximum and the sum against it
-  float m = -INFINITY, base = 0.f, s = 0.f;
-  unsigned finite = 0;
-  for (int v = tid; v < nvec; v += kTopThreads) {
-    float z[N];
-    VT::unpack(load_row_vec<ELT>(row, P.V, shift, v), z);
-    float vm = z[0];
-#pragma unroll
-    for (int e = 1; e < N; ++e) vm = fmaxf(vm, z[e]);
-    if (vm > m) {
-      s = m == -INFINITY ? 0.f : s * fast_exp2(__fmul_rn(__fsub_rn(m, vm), P.c2));
-      m = base = vm;
-    }
-#pragma unroll
-    for (int e = 0; e < N; ++e) {
-      s += fast_exp2(__fmul_rn(__fsub_rn(z[e], base), P.c2));
-      finite += z[e] > -INFINITY;
-    }
-  }
-  if (s != s) m = NAN;   // a NaN is carried by the maximum
-  float wm = m;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) wm = fmax_nan(wm, __shfl_xor_sync(0xffffffffu, wm, o));
-  float ws = m > -INFINITY ? s * fast_exp2(__fmul_rn(__fsub_rn(m, wm), P.c2)) : 0.f;
-  ws = warp_sum(ws);
-  finite = __reduce_add_sync(0xffffffffu, finite);
-  if (lane == 0) sh.wm[warp] = wm, sh.ws[warp] = ws, sh.warp_n[warp] = finite;
-  if (tid == 0) sh.n_found = 0, sh.prefix = 0;
-  __syncthreads();
-  float M = -INFINITY, S = 0.f;
-  unsigned n_finite = 0;
-  for (int w = 0; w < kTopWarps; ++w) M = fmax_nan(M, sh.wm[w]), n_finite += sh.warp_n[w];
-  for (int w = 0; w < kTopWarps; ++w)
-    if (sh.wm[w] > -INFINITY) S += sh.ws[w] * fast_exp2(__fmul_rn(__fsub_rn(sh.wm[w], M), P.c2));
-  if (!(S > 0.f) || !isfinite(S) || !isfinite(M)) {   // NaN, +inf, or nothing but -inf
-    for (int j = tid; j < P.K; j += kTopThreads) ids[j] = -1, logp[j] = NAN;
-    if (tid == 0) P.lse[r] = M == -INFINITY ? -INFINITY : NAN;
-    return;
-  }
-
-  // ---- the K-th largest key, most significant byte first
-  int need = min(static_cast<unsigned>(P.K), n_finite);
-  const int listed = need;
+  const int shift = row_shift<ELT>(row), nvec = row_vecs<ELT>(V, shift);
+  int need = n_list;
   uint32_t prefix = 0;
-  for (int shift_bits = 24; shift_bits >= 0; shift_bits -= 8) {
-    for (int i = tid; i < 256; i += kTopThreads) sh.hist[i] = 0;
+  for (int bits = 24; bits >= 0; bits -= 8) {
+    if (tid < 256) sh.hist[tid] = 0;
     __syncthreads();
     for (int v = tid; v < nvec; v += kTopThreads) {
       float z[N];
-      VT::unpack(load_row_vec<ELT>(row, P.V, shift, v), z);
+      VT::unpack(load_row_vec<ELT>(row, V, shift, v), z);
 #pragma unroll
       for (int e = 0; e < N; ++e) {
         const uint32_t key = top_key(z[e]);
-        if (key > kKeyNegInf && (shift_bits == 24 || (key >> (shift_bits + 8)) == (prefix >> (shift_bits + 8))))
-          atomicAdd(&sh.hist[(key >> shift_bits) & 255u], 1u);
+        if (key > kKeyNegInf && (bits == 24 || (key >> (bits + 8)) == (prefix >> (bits + 8))))
+          atomicAdd(&sh.hist[(key >> bits) & 255u], 1u);
       }
     }
     __syncthreads();
-    if (tid == 0) {
-      int left = need;
-      int d = 255;
-      for (; d > 0 && static_cast<int>(sh.hist[d]) < left; --d) left -= sh.hist[d];
-      sh.prefix = prefix | (static_cast<uint32_t>(d) << shift_bits);
-      sh.remaining = left;
-    }
+    find_bin(sh, need);
     __syncthreads();
-    prefix = sh.prefix;
-    need = sh.remaining;
+    prefix |= static_cast<uint32_t>(sh.digit) << bits;
+    need = sh.left;
   }
   // `need` of the tokens that tie with key `prefix`, and every larger one
   unsigned ties_before = 0;
@@ -154,12 +219,11 @@ __global__ void __launch_bounds__(kTopThreads) top_kernel(const TopParams P) {
     float z[N];
     unsigned tie = 0;
     if (v < nvec) {
-      VT::unpack(load_row_vec<ELT>(row, P.V, shift, v), z);
+      VT::unpack(load_row_vec<ELT>(row, V, shift, v), z);
 #pragma unroll
       for (int e = 0; e < N; ++e) {
         const uint32_t key = top_key(z[e]);
-        const uint32_t id = static_cast<uint32_t>(v * N - shift + e);
-        if (key > prefix) sh.list[atomicAdd(&sh.n_found, 1u)] = (static_cast<unsigned long long>(key) << 32) | ~id;
+        if (key > prefix) sh.list[atomicAdd(&sh.n_list, 1u)] = top_entry(key, static_cast<uint32_t>(v * N - shift + e));
         else if (key == prefix && key > kKeyNegInf) tie |= 1u << e;
       }
     }
@@ -181,31 +245,186 @@ __global__ void __launch_bounds__(kTopThreads) top_kernel(const TopParams P) {
     }
     for (int e = 0; e < N; ++e)
       if ((tie >> e) & 1u) {
-        const uint32_t id = static_cast<uint32_t>(v * N - shift + e);
         if (at < static_cast<unsigned>(need))
-          sh.list[listed - need + at] = (static_cast<unsigned long long>(prefix) << 32) | ~id;
+          sh.list[n_list - need + at] = top_entry(prefix, static_cast<uint32_t>(v * N - shift + e));
         ++at;
       }
     ties_before += all;
   }
   __syncthreads();
+}
 
-  // ---- in order: each entry's place is the number of larger ones
-  const float L = logf(S);
-  for (int j = tid; j < P.K; j += kTopThreads) {
-    if (j >= listed) {
-      ids[j] = -1;
-      logp[j] = -INFINITY;
-      continue;
+template <int ELT>
+__global__ void __launch_bounds__(kTopThreads, 2) top_kernel(const TopParams P) {
+  using VT = Vec<ELT>;
+  constexpr int N = VT::N;
+  extern __shared__ __align__(16) unsigned char smem[];
+  TopShared& sh = *reinterpret_cast<TopShared*>(smem);
+  key64* cand = reinterpret_cast<key64*>(smem + kTopListAt);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int ctas = cluster_ctas(), rank = cluster_rank();
+  const long long r = blockIdx.x / ctas;
+  const unsigned char* row = P.rows + r * P.V * ELT;
+  int* ids = P.ids + r * P.K;
+  float* logp = P.logp + r * P.K;
+  if (P.n_rows && static_cast<int>(r % P.t_len) >= P.n_rows[r / P.t_len]) {   // the whole cluster
+    if (rank == 0) {
+      for (int j = tid; j < P.K; j += kTopThreads) ids[j] = -1, logp[j] = -INFINITY;
+      if (tid == 0) P.lse[r] = -INFINITY;
     }
-    const unsigned long long mine = sh.list[j];
-    int place = 0;
-    for (int i = 0; i < listed; ++i) place += sh.list[i] > mine;
-    const float z = key_value(static_cast<uint32_t>(mine >> 32));
-    ids[place] = static_cast<int>(~static_cast<uint32_t>(mine));
-    logp[place] = __fsub_rn(__fdiv_rn(__fsub_rn(z, M), P.T), L);
+    return;
   }
-  if (tid == 0) P.lse[r] = __fadd_rn(__fdiv_rn(M, P.T), L);
+  const int shift = row_shift<ELT>(row), nvec = row_vecs<ELT>(P.V, shift);
+  const int part = (nvec + ctas - 1) / ctas;
+  const int v0 = min(nvec, rank * part), v1 = min(nvec, v0 + part);
+  if (tid == 0) sh.n_found = sh.n_list = 0;
+
+  auto load = [&](uint4 (&w)[kTopUnroll], int base) {
+    // inside the part and away from the row's first and last vector
+    if (base >= v0 + 1 && base + kTopTile < v1) {
+      const unsigned char* at = row + (static_cast<long long>(base + tid) * N - shift) * ELT;
+#pragma unroll
+      for (int q = 0; q < kTopUnroll; ++q) w[q] = load_vec16(at + q * kTopThreads * 16);
+    } else {
+#pragma unroll
+      for (int q = 0; q < kTopUnroll; ++q) {
+        const int v = base + q * kTopThreads + tid;
+        w[q] = v < v1 ? load_row_vec<ELT>(row, P.V, shift, v) : VT::neg_inf();
+      }
+    }
+  };
+
+  float m = -INFINITY, t = -FLT_MAX;   // below t nothing is a candidate, nor is -inf
+  f2 s2 = 0ull;
+  const f2 cc = pack2(P.c2, P.c2);
+  uint4 w[kTopUnroll];
+  load(w, v0);
+  int tile = 0;
+  for (int base = v0; base < v1; base += kTopTile, ++tile) {
+    uint4 next[kTopUnroll];
+    if (base + kTopTile < v1) load(next, base + kTopTile);
+    const float vm = VT::vmax(w);        // NaN is passed over here and kept by the sum
+    if (vm > m) {
+      if (m > -INFINITY) {
+        const float f = fast_exp2(__fmul_rn(__fsub_rn(m, vm), P.c2));
+        s2 = mul2(s2, pack2(f, f));
+      }
+      m = vm;
+    }
+    const float mb = m > -INFINITY ? m : 0.f;
+    const f2 mm = pack2(mb, mb);
+#pragma unroll
+    for (int q = 0; q < kTopUnroll; ++q) {
+      f2 z[N / 2];
+      VT::pairs(w[q], z);
+#pragma unroll
+      for (int i = 0; i < N / 2; ++i) s2 = add2(s2, exp2_2(mul2(sub2(z[i], mm), cc)));
+    }
+    // ---- t: after the first tile, and each time the tiles seen have doubled
+    if ((tile & (tile + 1)) == 0) {
+      const float part_t = __shfl_sync(0xffffffffu, warp_sort(m, lane), P.quota - 1);
+      if (lane == 0) sh.wt[warp] = part_t;
+      if (tile == 0) __syncthreads();
+    }
+    const float seen = sh.wt[lane & (kTopWarps - 1)];
+    t = fmaxf(from_ordered_key(__reduce_min_sync(0xffffffffu, ordered_key(seen))), -FLT_MAX);
+    if (vm >= t) {
+#pragma unroll
+      for (int q = 0; q < kTopUnroll; ++q) {
+        const uint4 one[1] = {w[q]};
+        if (VT::vmax(one) >= t) append<ELT>(w[q], (base + q * kTopThreads + tid) * N - shift, t, cand, &sh.n_found);
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < kTopUnroll; ++q) w[q] = next[q];
+  }
+
+  // ---- this CTA's M, S and t
+  float s, s_hi;
+  unpack2(s2, s, s_hi);
+  s += s_hi;
+  const float part_t = __shfl_sync(0xffffffffu, warp_sort(m, lane), P.quota - 1);
+  if (s != s) m = NAN;   // a NaN is carried by the maximum
+  float wm = m;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) wm = fmax_nan(wm, __shfl_xor_sync(0xffffffffu, wm, o));
+  float ws = m > -INFINITY ? s * fast_exp2(__fmul_rn(__fsub_rn(m, wm), P.c2)) : 0.f;
+  ws = warp_sum(ws);
+  if (lane == 0) sh.wm[warp] = wm, sh.ws[warp] = ws, sh.wt[warp] = part_t;
+  __syncthreads();
+  if (warp == 0) {
+    const bool in = lane < kTopWarps;
+    const float lm = in ? sh.wm[lane] : -INFINITY;
+    float M = lm;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmax_nan(M, __shfl_xor_sync(0xffffffffu, M, o));
+    const float S = warp_sum(lm > -INFINITY ? sh.ws[lane] * fast_exp2(__fmul_rn(__fsub_rn(lm, M), P.c2)) : 0.f);
+    const float tt = from_ordered_key(__reduce_min_sync(0xffffffffu, ordered_key(in ? sh.wt[lane] : INFINITY)));
+    if (lane == 0) sh.M = M, sh.S = S, sh.t = tt;
+  }
+  if (ctas > 1) cluster_sync();
+  else __syncthreads();
+
+  if (rank == 0) {
+    // ---- the row's M, S and t
+    float M = sh.M, tt = sh.t;
+    for (int c = 1; c < ctas; ++c) M = fmax_nan(M, peer_float(&sh.M, c)), tt = fmaxf(tt, peer_float(&sh.t, c));
+    float S = 0.f;
+    bool fits = true;
+    for (int c = 0; c < ctas; ++c) {
+      const float cm = peer_float(&sh.M, c), cs = peer_float(&sh.S, c);
+      if (cm > -INFINITY) S += cs * fast_exp2(__fmul_rn(__fsub_rn(cm, M), P.c2));
+      const unsigned n = peer_uint(&sh.n_found, c);
+      fits &= n <= kTopCap;
+    }
+    const bool valid = S > 0.f && isfinite(S) && isfinite(M);   // not NaN, +inf, or nothing but -inf
+    int listed = 0;
+    if (valid) {
+      // ---- the candidates at or above t, all in this CTA's buffer
+      if (fits && ctas > 1) {
+        const uint32_t least = top_key(fmaxf(tt, -FLT_MAX));
+        __syncthreads();
+        for (int c = 1; c < ctas; ++c) {
+          const unsigned n = peer_uint(&sh.n_found, c);
+          for (unsigned i = tid; i < n; i += kTopThreads) {
+            const key64 k = peer_key(&cand[i], c);
+            if (static_cast<uint32_t>(k >> 32) >= least) {
+              const unsigned at = atomicAdd(&sh.n_found, 1u);
+              if (at < kTopCap) cand[at] = k;
+            }
+          }
+        }
+        __syncthreads();
+        fits = sh.n_found <= kTopCap;
+      }
+      if (fits) {
+        const int n = static_cast<int>(sh.n_found);
+        listed = min(P.K, n);
+        select_entries(sh, cand, n, listed);
+      } else {
+        // more candidates than the buffer holds: K of them at least
+        listed = P.K;
+        select_from_row<ELT>(sh, row, P.V, listed);
+      }
+    }
+    // ---- in order: each entry's place is the number of larger ones
+    const float L = logf(S);
+    for (int j = tid; j < P.K; j += kTopThreads) {
+      if (j >= listed) {
+        ids[j] = -1;
+        logp[j] = valid ? -INFINITY : NAN;
+        continue;
+      }
+      const key64 mine = sh.list[j];
+      int place = 0;
+      for (int i = 0; i < listed; ++i) place += sh.list[i] > mine;
+      const float z = key_value(static_cast<uint32_t>(mine >> 32));
+      ids[place] = static_cast<int>(~static_cast<uint32_t>(mine));
+      logp[place] = __fsub_rn(__fdiv_rn(__fsub_rn(z, M), P.T), L);
+    }
+    if (tid == 0) P.lse[r] = valid ? __fadd_rn(__fdiv_rn(M, P.T), L) : M == -INFINITY ? -INFINITY : NAN;
+  }
+  if (ctas > 1) cluster_sync();   // the other CTAs' memory is read no more
 }
 
 }  // namespace
@@ -216,7 +435,7 @@ extern "C" sv_status spec_kd_top(int n_seq, int t_len, int V, sv_dtype dtype, co
                                  float* lse, sv_stream_t stream) {
   using namespace sv;
   if (n_seq < 1 || t_len < 1 || V < 1 || K < 1 || K > SV_KD_TOP_MAX) return SV_ERR_INVALID_ARG;
-  if (static_cast<long long>(n_seq) * t_len > (1LL << 30)) return SV_ERR_INVALID_ARG;
+  if (static_cast<long long>(n_seq) * t_len > (1LL << 28)) return SV_ERR_INVALID_ARG;
   if (dtype != SV_F32 && dtype != SV_BF16) return SV_ERR_INVALID_ARG;
   if (!(temperature > 0.f) || !std::isfinite(temperature)) return SV_ERR_INVALID_ARG;
   if (!target_logits || !ids || !logp || !lse) return SV_ERR_INVALID_ARG;
@@ -226,11 +445,23 @@ extern "C" sv_status spec_kd_top(int n_seq, int t_len, int V, sv_dtype dtype, co
   const double c2 = 1.4426950408889634 / static_cast<double>(temperature);
   if (!(c2 < 1e30)) return SV_ERR_INVALID_ARG;
   TopParams p{static_cast<const unsigned char*>(target_logits), n_rows, ids, logp, lse, t_len, V, K,
-              static_cast<float>(c2), temperature};
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+              static_cast<float>(c2), temperature, (K + kTopWarps - 1) / kTopWarps};
+  // as many CTAs to a row as leave each two tiles, until there are enough of them
+  const int rows = n_seq * t_len, nvec = V / (16 / elt);
+  int cluster = 1;
+  while (cluster < 8 && static_cast<long long>(rows) * cluster < kTopFewRows && nvec / (2 * cluster) >= 2 * kTopTile) cluster *= 2;
   NvtxRange range("spec_kd_top");
-  const int ctas = n_seq * t_len;
-  if (elt == 2) top_kernel<2><<<ctas, kTopThreads, 0, s>>>(p);
-  else top_kernel<4><<<ctas, kTopThreads, 0, s>>>(p);
-  return cudaGetLastError() == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = cluster;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(rows) * cluster);
+  cfg.blockDim = dim3(kTopThreads);
+  cfg.dynamicSmemBytes = kTopSmem;
+  cfg.stream = reinterpret_cast<cudaStream_t>(stream);
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = elt == 2 ? cudaLaunchKernelEx(&cfg, top_kernel<2>, p) : cudaLaunchKernelEx(&cfg, top_kernel<4>, p);
+  return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? SV_OK : SV_ERR_CUDA;
 }
