@@ -10,19 +10,24 @@
 // to the lower id; a token of probability 0 (z = -inf) is never listed.
 //
 // A row goes to a cluster of 1 to 8 CTAs, each streaming its part of it once:
-// running maxima and sums per thread for (M, S), and beside them the tokens
-// that can still be in the list.  A token can be left out as soon as K others
-// at or above some t are known and it is below t; t comes from the threads'
-// running maxima: if q = K / 16 lanes of each of the 16 warps have seen a
-// value of at least t, K tokens have.  So t is the least of the warps' q-th
-// largest lane maxima, and a row's candidates are a few times K (some 600 for
-// K = 64 of 152k).  The warps publish their parts of t without a barrier but
-// one, after the first tile (an older part is smaller and lets more through).
-// The cluster's first CTA gathers the candidates at or above the largest of
-// the CTAs' t from their shared memory, selects the K by radix and ranks
-// them.  Candidates that outgrow their buffer (rows of few distinct values,
-// or masked with a finite value) are left, and the first CTA selects from the
-// row itself.
+// running maxima and sums per thread for (M, S), and beside them the 16-byte
+// vectors that can still hold a token of the list.  A token can be left out
+// as soon as K others at or above some t are known and it is below t; t comes
+// from the threads' running maxima: if q = K / 16 lanes of each of the 16
+// warps have seen a value of at least t, K tokens have.  So t is the least of
+// the warps' q-th largest lane maxima, and what passes is a few times K.  The
+// warps publish their parts of t without a barrier but one, after the first
+// tile (an older part is smaller and lets more through).  A vector whose
+// maximum passes is kept whole, a ballot and one addition for a warp; its
+// tokens are looked at once t is final (appending token by token while
+// streaming: 116 us against @@ on 1024 ragged rows of 128256 bf16 logits,
+// K = 64).
+//
+// The CTAs hand their tokens at or above t, and their M and S, to the
+// cluster's first one and leave; it selects the K by radix and ranks them.
+// Vectors that outgrow their buffer (rows of few distinct values, or masked
+// with a finite value) are dropped, and the first CTA selects from the row
+// itself.
 
 #include <cuda_runtime.h>
 
@@ -43,8 +48,10 @@ constexpr int kTopMaxK = SV_KD_TOP_MAX;
 constexpr int kTopUnroll = 4;             // 16-byte vectors of a tile per thread
 constexpr int kTopTile = kTopThreads * kTopUnroll;
 constexpr int kTopFewRows = 1216;         // CTAs below which a row is split
-constexpr int kTopCap = 4096;             // candidates a CTA can hold: no fewer than the
-                                          // tokens of a part that leaves threads idle
+constexpr int kTopVecs = 2048;            // vectors a CTA can hold: more than a part that
+                                          // leaves threads idle has
+constexpr int kTopPush = 512;             // tokens that a CTA hands on at most
+constexpr int kTopCap = 8 * kTopPush;     // tokens to select from
 
 struct TopParams {
   const unsigned char* rows;   // [n_seq, t_len, V]
@@ -77,31 +84,35 @@ struct TopShared {
   volatile float wt[kTopWarps];           // the warps' parts of t
   unsigned int hist[256];
   unsigned int warp_n[kTopWarps];
-  unsigned int n_found;                   // candidates seen (may pass kTopCap)
+  unsigned int n_vecs;                    // vectors kept (may pass kTopVecs)
+  unsigned int n_tokens;                  // tokens to select from (may pass kTopCap)
   unsigned int n_list;
-  float M, S, t;                          // this CTA's part
+  unsigned int base;                      // where this CTA's tokens go in the first one's
+  unsigned int lost;                      // (first CTA) some CTA's vectors outgrew its buffer
+  float M[8], S[8];                       // (first CTA) the CTAs' parts
   int digit, left;
   key64 list[kTopMaxK];
 };
+constexpr int kTopVecsAt = (static_cast<int>(sizeof(TopShared)) + 15) / 16 * 16;
+constexpr int kTopIdsAt = kTopVecsAt + kTopVecs * 16;
+constexpr int kTopTokensAt = kTopIdsAt + kTopVecs * 4;
+constexpr int kTopSmem = kTopTokensAt + kTopCap * static_cast<int>(sizeof(key64));
 
-constexpr int kTopListAt = (static_cast<int>(sizeof(TopShared)) + 15) / 16 * 16;
-constexpr int kTopSmem = kTopListAt + kTopCap * static_cast<int>(sizeof(key64));
-
-// Shared variables of CTA `rank` of the cluster.
-__device__ __forceinline__ float peer_float(const volatile float* p, int rank) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(peer(p, rank)) : "memory");
-  return v;
+// All threads of the cluster: arrive (what they wrote before is visible to
+// those that wait after), and wait.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
+// Shared variables of the cluster's first CTA.
+__device__ __forceinline__ unsigned int first_add(unsigned int* p, unsigned int v) {
+  unsigned int old;
+  asm volatile("atom.relaxed.cluster.shared::cluster.add.u32 %0, [%1], %2;" : "=r"(old) : "r"(peer(p, 0)), "r"(v) : "memory");
+  return old;
 }
-__device__ __forceinline__ unsigned int peer_uint(const unsigned int* p, int rank) {
-  unsigned int v;
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(peer(p, rank)) : "memory");
-  return v;
+__device__ __forceinline__ void first_store(float* p, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" :: "r"(peer(p, 0)), "f"(v) : "memory");
 }
-__device__ __forceinline__ key64 peer_key(const key64* p, int rank) {
-  key64 v;
-  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(peer(p, rank)) : "memory");
-  return v;
+__device__ __forceinline__ void first_store(key64* p, key64 v) {
+  asm volatile("st.shared::cluster.u64 [%0], %1;" :: "r"(peer(p, 0)), "l"(v) : "memory");
 }
 
 // The warp's lanes' values in descending order.
@@ -115,20 +126,6 @@ __device__ __forceinline__ float warp_sort(float v, int lane) {
       v = keep_max ? fmaxf(v, x) : fminf(v, x);
     }
   return v;
-}
-
-// Appends the elements of vector v that are at least t.
-template <int ELT>
-__device__ __noinline__ void append(uint4 w, int t0, float t, key64* cand, unsigned int* n_found) {
-  constexpr int N = Vec<ELT>::N;
-  float z[N];
-  Vec<ELT>::unpack(w, z);
-#pragma unroll
-  for (int e = 0; e < N; ++e)
-    if (z[e] >= t) {
-      const unsigned int at = atomicAdd(n_found, 1u);
-      if (at < kTopCap) cand[at] = top_entry(top_key(z[e]), static_cast<uint32_t>(t0 + e));
-    }
 }
 
 // The bin, from the top, in which the running count of hist reaches `left`
@@ -260,7 +257,9 @@ __global__ void __launch_bounds__(kTopThreads, 2) top_kernel(const TopParams P) 
   constexpr int N = VT::N;
   extern __shared__ __align__(16) unsigned char smem[];
   TopShared& sh = *reinterpret_cast<TopShared*>(smem);
-  key64* cand = reinterpret_cast<key64*>(smem + kTopListAt);
+  uint4* vecs = reinterpret_cast<uint4*>(smem + kTopVecsAt);
+  int* vec_at = reinterpret_cast<int*>(smem + kTopIdsAt);
+  key64* tokens = reinterpret_cast<key64*>(smem + kTopTokensAt);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int ctas = cluster_ctas(), rank = cluster_rank();
   const long long r = blockIdx.x / ctas;
@@ -277,7 +276,6 @@ __global__ void __launch_bounds__(kTopThreads, 2) top_kernel(const TopParams P) 
   const int shift = row_shift<ELT>(row), nvec = row_vecs<ELT>(P.V, shift);
   const int part = (nvec + ctas - 1) / ctas;
   const int v0 = min(nvec, rank * part), v1 = min(nvec, v0 + part);
-  if (tid == 0) sh.n_found = sh.n_list = 0;
 
   auto load = [&](uint4 (&w)[kTopUnroll], int base) {
     // inside the part and away from the row's first and last vector
@@ -299,6 +297,11 @@ __global__ void __launch_bounds__(kTopThreads, 2) top_kernel(const TopParams P) 
   const f2 cc = pack2(P.c2, P.c2);
   uint4 w[kTopUnroll];
   load(w, v0);
+  if (tid == 0) sh.n_vecs = sh.n_tokens = sh.n_list = sh.lost = 0;
+  if (ctas > 1) {
+    __syncthreads();
+    cluster_arrive();                  // the counters are set
+  }
   int tile = 0;
   for (int base = v0; base < v1; base += kTopTile, ++tile) {
     uint4 next[kTopUnroll];
@@ -328,11 +331,20 @@ __global__ void __launch_bounds__(kTopThreads, 2) top_kernel(const TopParams P) 
     }
     const float seen = sh.wt[lane & (kTopWarps - 1)];
     t = fmaxf(from_ordered_key(__reduce_min_sync(0xffffffffu, ordered_key(seen))), -FLT_MAX);
-    if (vm >= t) {
+    if (__any_sync(0xffffffffu, vm >= t)) {
 #pragma unroll
       for (int q = 0; q < kTopUnroll; ++q) {
         const uint4 one[1] = {w[q]};
-        if (VT::vmax(one) >= t) append<ELT>(w[q], (base + q * kTopThreads + tid) * N - shift, t, cand, &sh.n_found);
+        const bool keep = VT::vmax(one) >= t;
+        const unsigned who = __ballot_sync(0xffffffffu, keep);
+        if (!who) continue;
+        unsigned at = 0;
+        if (lane == 0) at = atomicAdd(&sh.n_vecs, __popc(who));
+        at = __shfl_sync(0xffffffffu, at, 0) + __popc(who & ((1u << lane) - 1u));
+        if (keep && at < kTopVecs) {
+          vecs[at] = w[q];
+          vec_at[at] = base + q * kTopThreads + tid;
+        }
       }
     }
 #pragma unroll
@@ -352,6 +364,7 @@ __global__ void __launch_bounds__(kTopThreads, 2) top_kernel(const TopParams P) 
   ws = warp_sum(ws);
   if (lane == 0) sh.wm[warp] = wm, sh.ws[warp] = ws, sh.wt[warp] = part_t;
   __syncthreads();
+  if (ctas > 1) cluster_wait();        // the first CTA's counters are set
   if (warp == 0) {
     const bool in = lane < kTopWarps;
     const float lm = in ? sh.wm[lane] : -INFINITY;
@@ -359,72 +372,94 @@ __global__ void __launch_bounds__(kTopThreads, 2) top_kernel(const TopParams P) 
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) M = fmax_nan(M, __shfl_xor_sync(0xffffffffu, M, o));
     const float S = warp_sum(lm > -INFINITY ? sh.ws[lane] * fast_exp2(__fmul_rn(__fsub_rn(lm, M), P.c2)) : 0.f);
-    const float tt = from_ordered_key(__reduce_min_sync(0xffffffffu, ordered_key(in ? sh.wt[lane] : INFINITY)));
-    if (lane == 0) sh.M = M, sh.S = S, sh.t = tt;
+    if (lane == 0) {
+      first_store(&sh.M[rank], M);
+      first_store(&sh.S[rank], S);
+    }
   }
-  if (ctas > 1) cluster_sync();
-  else __syncthreads();
+  {
+    const float seen = sh.wt[lane & (kTopWarps - 1)];
+    t = fmaxf(from_ordered_key(__reduce_min_sync(0xffffffffu, ordered_key(seen))), -FLT_MAX);
+  }
+  // ---- the kept vectors' tokens at or above t
+  const bool whole = sh.n_vecs <= kTopVecs;
+  const int n_vecs = static_cast<int>(whole ? sh.n_vecs : 0u);
+  for (int i = tid; i < n_vecs; i += kTopThreads) {
+    float z[N];
+    VT::unpack(vecs[i], z);
+    const int t0 = vec_at[i] * N - shift;
+#pragma unroll
+    for (int e = 0; e < N; ++e)
+      if (z[e] >= t) {
+        const unsigned at = atomicAdd(&sh.n_tokens, 1u);
+        if (at < kTopCap) tokens[at] = top_entry(top_key(z[e]), static_cast<uint32_t>(t0 + e));
+      }
+  }
+  if (rank != 0) {
+    __syncthreads();
+    // at most kTopPush: where there are more, the K largest
+    unsigned n = sh.n_tokens;
+    const key64* from = tokens;
+    if (n > kTopPush && n <= kTopCap) {
+      select_entries(sh, tokens, static_cast<int>(n), P.K);
+      from = sh.list;
+      n = P.K;
+    }
+    if (tid == 0) {
+      const bool lost = !whole || n > kTopCap;
+      if (lost) first_add(&sh.lost, 1u);
+      sh.base = first_add(&sh.n_tokens, lost ? 0u : n);
+      if (lost) sh.n_tokens = 0;
+    }
+    __syncthreads();
+    if (sh.n_tokens)
+      for (unsigned i = tid; i < n; i += kTopThreads)
+        if (sh.base + i < kTopCap) first_store(&tokens[sh.base + i], from[i]);
+    cluster_arrive();                  // and leave
+    return;
+  }
+  if (tid == 0 && !whole) atomicAdd(&sh.lost, 1u);
+  if (ctas > 1) {
+    cluster_arrive();
+    cluster_wait();
+  } else {
+    __syncthreads();
+  }
 
-  if (rank == 0) {
-    // ---- the row's M, S and t
-    float M = sh.M, tt = sh.t;
-    for (int c = 1; c < ctas; ++c) M = fmax_nan(M, peer_float(&sh.M, c)), tt = fmaxf(tt, peer_float(&sh.t, c));
-    float S = 0.f;
-    bool fits = true;
-    for (int c = 0; c < ctas; ++c) {
-      const float cm = peer_float(&sh.M, c), cs = peer_float(&sh.S, c);
-      if (cm > -INFINITY) S += cs * fast_exp2(__fmul_rn(__fsub_rn(cm, M), P.c2));
-      const unsigned n = peer_uint(&sh.n_found, c);
-      fits &= n <= kTopCap;
+  // ---- the row's M and S
+  float M = -INFINITY, S = 0.f;
+  for (int c = 0; c < ctas; ++c) M = fmax_nan(M, sh.M[c]);
+  for (int c = 0; c < ctas; ++c)
+    if (sh.M[c] > -INFINITY) S += sh.S[c] * fast_exp2(__fmul_rn(__fsub_rn(sh.M[c], M), P.c2));
+  const bool valid = S > 0.f && isfinite(S) && isfinite(M);   // not NaN, +inf, or nothing but -inf
+  int listed = 0;
+  if (valid) {
+    if (!sh.lost && sh.n_tokens <= kTopCap) {
+      const int n = static_cast<int>(sh.n_tokens);
+      listed = min(P.K, n);
+      select_entries(sh, tokens, n, listed);
+    } else {
+      // more candidates than the buffers hold: K of them at least
+      listed = P.K;
+      select_from_row<ELT>(sh, row, P.V, listed);
     }
-    const bool valid = S > 0.f && isfinite(S) && isfinite(M);   // not NaN, +inf, or nothing but -inf
-    int listed = 0;
-    if (valid) {
-      // ---- the candidates at or above t, all in this CTA's buffer
-      if (fits && ctas > 1) {
-        const uint32_t least = top_key(fmaxf(tt, -FLT_MAX));
-        __syncthreads();
-        for (int c = 1; c < ctas; ++c) {
-          const unsigned n = peer_uint(&sh.n_found, c);
-          for (unsigned i = tid; i < n; i += kTopThreads) {
-            const key64 k = peer_key(&cand[i], c);
-            if (static_cast<uint32_t>(k >> 32) >= least) {
-              const unsigned at = atomicAdd(&sh.n_found, 1u);
-              if (at < kTopCap) cand[at] = k;
-            }
-          }
-        }
-        __syncthreads();
-        fits = sh.n_found <= kTopCap;
-      }
-      if (fits) {
-        const int n = static_cast<int>(sh.n_found);
-        listed = min(P.K, n);
-        select_entries(sh, cand, n, listed);
-      } else {
-        // more candidates than the buffer holds: K of them at least
-        listed = P.K;
-        select_from_row<ELT>(sh, row, P.V, listed);
-      }
-    }
-    // ---- in order: each entry's place is the number of larger ones
-    const float L = logf(S);
-    for (int j = tid; j < P.K; j += kTopThreads) {
-      if (j >= listed) {
-        ids[j] = -1;
-        logp[j] = valid ? -INFINITY : NAN;
-        continue;
-      }
-      const key64 mine = sh.list[j];
-      int place = 0;
-      for (int i = 0; i < listed; ++i) place += sh.list[i] > mine;
-      const float z = key_value(static_cast<uint32_t>(mine >> 32));
-      ids[place] = static_cast<int>(~static_cast<uint32_t>(mine));
-      logp[place] = __fsub_rn(__fdiv_rn(__fsub_rn(z, M), P.T), L);
-    }
-    if (tid == 0) P.lse[r] = valid ? __fadd_rn(__fdiv_rn(M, P.T), L) : M == -INFINITY ? -INFINITY : NAN;
   }
-  if (ctas > 1) cluster_sync();   // the other CTAs' memory is read no more
+  // ---- in order: each entry's place is the number of larger ones
+  const float L = logf(S);
+  for (int j = tid; j < P.K; j += kTopThreads) {
+    if (j >= listed) {
+      ids[j] = -1;
+      logp[j] = valid ? -INFINITY : NAN;
+      continue;
+    }
+    const key64 mine = sh.list[j];
+    int place = 0;
+    for (int i = 0; i < listed; ++i) place += sh.list[i] > mine;
+    const float z = key_value(static_cast<uint32_t>(mine >> 32));
+    ids[place] = static_cast<int>(~static_cast<uint32_t>(mine));
+    logp[place] = __fsub_rn(__fdiv_rn(__fsub_rn(z, M), P.T), L);
+  }
+  if (tid == 0) P.lse[r] = valid ? __fadd_rn(__fdiv_rn(M, P.T), L) : M == -INFINITY ? -INFINITY : NAN;
 }
 
 }  // namespace
@@ -462,6 +497,9 @@ extern "C" sv_status spec_kd_top(int n_seq, int t_len, int V, sv_dtype dtype, co
   cfg.stream = reinterpret_cast<cudaStream_t>(stream);
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
+  // 105 KB a CTA: more than the 48 KB that need no asking
+  const void* fn = elt == 2 ? reinterpret_cast<const void*>(&top_kernel<2>) : reinterpret_cast<const void*>(&top_kernel<4>);
+  if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kTopSmem) != cudaSuccess) return SV_ERR_CUDA;
   const cudaError_t e = elt == 2 ? cudaLaunchKernelEx(&cfg, top_kernel<2>, p) : cudaLaunchKernelEx(&cfg, top_kernel<4>, p);
   return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? SV_OK : SV_ERR_CUDA;
 }
