@@ -1,33 +1,36 @@
 // The K most likely tokens of teacher rows as log-probabilities, with the
 // row's log-sum-exp, for sm_103a.
 //
-// For a row z and a temperature T, with c = log2(e) / T, M = max z and
-// S = sum_x 2^((z(x) - M) c):
-//   lse = M / T + ln S,  logp(x) = (z(x) - M) / T - ln S.
-// Differences are taken before the scale: a likely token's logp keeps its
-// digits whatever the row's level, and a row of the type's lowest values
-// does not overflow.  The K tokens are those with the largest z, ties
+// For a row z and a temperature T, with c = log2(e) / T, M = max z,
+// K0 = fl(M c) and S = sum_x 2^(z(x) c - K0) (one fused multiply-add a term):
+//   L = ln S + ln 2 (K0 - M c) = ln sum_x e^((z(x) - M) / T),
+//   lse = M / T + L,  logp(x) = (z(x) - M) / T - L,
+// K0 - M c exactly (a fused multiply-add again), so that a likely token's logp
+// keeps its digits whatever the row's level.  Where M c overflows (a row of
+// nothing but the type's lowest values) the sum is taken of 2^((z - M) c)
+// instead.  The K tokens are those with the largest z, ties
 // to the lower id; a token of probability 0 (z = -inf) is never listed.
 //
 // A row goes to a cluster of 1 to 8 CTAs, each streaming its part of it once:
-// running maxima and sums per thread for (M, S), and beside them the 16-byte
-// vectors that can still hold a token of the list.  A token can be left out
-// as soon as K others at or above some t are known and it is below t; t comes
-// from the threads' running maxima: if q = K / 16 lanes of each of the 16
-// warps have seen a value of at least t, K tokens have.  So t is the least of
-// the warps' q-th largest lane maxima, and what passes is a few times K.  The
-// warps publish their parts of t without a barrier but one, after the first
-// tile (an older part is smaller and lets more through).  A vector whose
-// maximum passes is kept whole, a ballot and one addition for a warp; its
-// tokens are looked at once t is final (appending token by token while
-// streaming: 116 us against @@ on 1024 ragged rows of 128256 bf16 logits,
-// K = 64).
+// running maxima and sums per thread for (M, S), and beside them what can
+// still hold a token of the list.  A token can be left out as soon as K others
+// at or above some t are known and it is below t; t comes from the threads'
+// maxima: if q = K / 8 values of at least t are among the largest that the lanes
+// of each of the 8 warps have seen in a tile, K tokens have.  So t is the least
+// of the warps' q-th largest, and what passes is a few times K.  The warps publish
+// their parts of t without a barrier but one, after the first tile (an older
+// part is smaller and lets more through).  A thread whose four vectors of a
+// tile hold a value of at least t notes them, with one ballot and one addition
+// a warp (their values in shared memory while there is room; the others are
+// read again, from L2); once t is final, their tokens at or above t are kept.
+// On 1024 ragged rows of 128256 bf16 logits, K = 64: 50 us; appending token by
+// token while streaming 116 us.
 //
 // The CTAs hand their tokens at or above t, and their M and S, to the
-// cluster's first one and leave; it selects the K by radix and ranks them.
-// Vectors that outgrow their buffer (rows of few distinct values, or masked
-// with a finite value) are dropped, and the first CTA selects from the row
-// itself.
+// cluster's first one and leave; it ranks them by counting the larger ones of
+// each.  Notes or tokens that outgrow their buffer (rows of few distinct
+// values, or masked with a finite value) are dropped, and the first CTA
+// selects from the row itself.
 
 #include <cuda_runtime.h>
 
@@ -42,16 +45,17 @@
 namespace sv {
 namespace {
 
-constexpr int kTopThreads = 512;
+constexpr int kTopThreads = 256;
 constexpr int kTopWarps = kTopThreads / 32;
 constexpr int kTopMaxK = SV_KD_TOP_MAX;
 constexpr int kTopUnroll = 4;             // 16-byte vectors of a tile per thread
 constexpr int kTopTile = kTopThreads * kTopUnroll;
-constexpr int kTopFewRows = 1216;         // CTAs below which a row is split
-constexpr int kTopVecs = 2048;            // vectors a CTA can hold: more than a part that
-                                          // leaves threads idle has
-constexpr int kTopPush = 512;             // tokens that a CTA hands on at most
-constexpr int kTopCap = 8 * kTopPush;     // tokens to select from
+constexpr int kTopPlaces = 2048;          // (thread, tile) places a CTA can note: more than a part
+                                          // that leaves threads idle has
+constexpr int kTopHeld = 256;             // ... with their values
+constexpr int kTopCap = 1792;             // tokens to rank or to select from
+constexpr int kTopEdge = 128;             // entries that share the last one's bin, told apart by counting
+constexpr int kTopCount = 256;            // tokens ranked by counting; of more the K are selected first
 
 struct TopParams {
   const unsigned char* rows;   // [n_seq, t_len, V]
@@ -63,8 +67,10 @@ struct TopParams {
   float c2;                    // log2(e) / T
   float T;
   int quota;                   // ceil(K / warps)
+  int push;                    // tokens that a CTA hands on at most (>= K)
 };
 
+typedef unsigned long long key64;   // key and id: larger for a larger value, then a lower id
 constexpr uint32_t kKeyNegInf = 0x007fffffu;   // top_key(-inf)
 
 // Larger for a larger value; -0 and 0 are one value.
@@ -76,27 +82,30 @@ __device__ __forceinline__ float key_value(uint32_t k) {
   return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xffffffffu));
 }
 
-typedef unsigned long long key64;   // key and id: larger for a larger value, then a lower id
 __device__ __forceinline__ key64 top_entry(uint32_t key, uint32_t id) { return (static_cast<key64>(key) << 32) | ~id; }
 
+// What a CTA keeps in shared memory: no more than it needs, for what that
+// leaves is L1, and loads in flight need its lines (54 KB a CTA in place of
+// 43: 215 us against 207 on 4096 rows of 128256 bf16 logits, K = 64).
 struct TopShared {
-  float wm[kTopWarps], ws[kTopWarps];     // the warps' maxima and sums
-  volatile float wt[kTopWarps];           // the warps' parts of t
+  float wm[kTopWarps], ws[kTopWarps];   // the warps' maxima and sums
+  volatile int wt[kTopWarps];           // the warps' parts of t, as ordered keys
   unsigned int hist[256];
   unsigned int warp_n[kTopWarps];
-  unsigned int n_vecs;                    // vectors kept (may pass kTopVecs)
-  unsigned int n_tokens;                  // tokens to select from (may pass kTopCap)
+  unsigned int n_places;                // places noted (may pass kTopPlaces)
+  unsigned int n_tokens;                // tokens to select from (may pass kTopCap)
   unsigned int n_list;
-  unsigned int base;                      // where this CTA's tokens go in the first one's
-  unsigned int lost;                      // (first CTA) some CTA's vectors outgrew its buffer
-  float M[8], S[8];                       // (first CTA) the CTAs' parts
+  unsigned int base;                    // where this CTA's tokens go in the first one's
+  unsigned int lost;                    // (first CTA) some CTA's tokens outgrew its buffers
+  float M[8], S[8], t[8];               // (first CTA) the CTAs' parts
   int digit, left;
+  unsigned int n_edge;
+  key64 edge[kTopEdge];
   key64 list[kTopMaxK];
+  int places[kTopPlaces];               // a thread's first vector of a tile
+  uint4 held[kTopUnroll][kTopHeld];
+  key64 tokens[kTopCap];
 };
-constexpr int kTopVecsAt = (static_cast<int>(sizeof(TopShared)) + 15) / 16 * 16;
-constexpr int kTopIdsAt = kTopVecsAt + kTopVecs * 16;
-constexpr int kTopTokensAt = kTopIdsAt + kTopVecs * 4;
-constexpr int kTopSmem = kTopTokensAt + kTopCap * static_cast<int>(sizeof(key64));
 
 // All threads of the cluster: arrive (what they wrote before is visible to
 // those that wait after), and wait.
@@ -128,6 +137,31 @@ __device__ __forceinline__ float warp_sort(float v, int lane) {
   return v;
 }
 
+// A value that at least `quota` tokens seen by the warp's lanes reach, from the
+// lanes' largest tile maxima m1 and, where half the lanes would not be enough
+// to tell, their second largest m2.
+__device__ __forceinline__ float quota_of(float m1, float m2, int quota, int lane) {
+  if (quota <= 4) {
+    int key = ordered_key(m1), top = 0;
+    for (int i = 0; i < quota; ++i) {   // the largest leaves, one lane at a time
+      top = __reduce_max_sync(0xffffffffu, key);
+      const unsigned who = __ballot_sync(0xffffffffu, key == top);
+      if (lane == __ffs(who) - 1) key = static_cast<int>(0x80000000u);
+    }
+    return from_ordered_key(top);
+  }
+  float v = warp_sort(m1, lane);
+  if (quota > 16) {   // the upper half of both, in order again
+    v = fmaxf(v, __shfl_sync(0xffffffffu, warp_sort(m2, lane), 31 - lane));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const float x = __shfl_xor_sync(0xffffffffu, v, o);
+      v = lane & o ? fminf(v, x) : fmaxf(v, x);
+    }
+  }
+  return __shfl_sync(0xffffffffu, v, quota - 1);
+}
+
 // The bin, from the top, in which the running count of hist reaches `left`
 // (1 <= left <= total), and what is left of `left` in it: by warp 0.
 __device__ __forceinline__ void find_bin(TopShared& sh, int left) {
@@ -152,27 +186,64 @@ __device__ __forceinline__ void find_bin(TopShared& sh, int left) {
   }
 }
 
-// The n_list largest of n distinct entries (n_list <= n), into sh.list in any
-// order.
-__device__ __forceinline__ void select_entries(TopShared& sh, const key64* cand, int n, int n_list) {
+// The n_list largest of n distinct entries (n_list <= n <= kTopCap), all of
+// keys from `least` on, into sh.list in any order.  One histogram of 256 bins
+// spread over the keys' own range; then what falls into the bin of the
+// n_list-th largest is told apart by counting.  Where that bin is too full to
+// count (values that tie), radix passes from the entries' most significant
+// byte on.
+__device__ __noinline__ void select_entries(TopShared& sh, const key64* cand, int n, int n_list, uint32_t least,
+                                               uint32_t most) {
   const int tid = threadIdx.x;
-  key64 prefix = 0;     // the digits of the n_list-th largest so far, the rest zero
-  if (n > n_list) {
-    int left = n_list;
-    for (int shift = 56; shift >= 0; shift -= 8) {
-      if (tid < 256) sh.hist[tid] = 0;
-      __syncthreads();
-      for (int i = tid; i < n; i += kTopThreads) {
-        const key64 k = cand[i];
-        if (shift == 56 || (k >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&sh.hist[(k >> shift) & 255u], 1u);
-      }
-      __syncthreads();
-      find_bin(sh, left);
-      __syncthreads();
-      prefix |= static_cast<key64>(sh.digit) << shift;
-      left = sh.left;
-      if (static_cast<unsigned>(left) == sh.hist[sh.digit]) break;   // the whole bin
+  if (n == n_list) {
+    for (int i = tid; i < n; i += kTopThreads) sh.list[i] = cand[i];
+    __syncthreads();
+    return;
+  }
+  const int coarse = max(0, 24 - __clz(most - least));   // (most - least) >> coarse < 256
+  auto bin = [&](key64 k) { return (static_cast<uint32_t>(k >> 32) - least) >> coarse; };
+  if (tid < 256) sh.hist[tid] = 0;
+  if (tid == 0) sh.n_list = sh.n_edge = 0;
+  __syncthreads();
+  for (int i = tid; i < n; i += kTopThreads) atomicAdd(&sh.hist[bin(cand[i])], 1u);
+  __syncthreads();
+  find_bin(sh, n_list);
+  __syncthreads();
+  const uint32_t edge = sh.digit;
+  int left = sh.left;
+  if (sh.hist[edge] <= kTopEdge) {
+    for (int i = tid; i < n; i += kTopThreads) {
+      const key64 k = cand[i];
+      if (bin(k) > edge) sh.list[atomicAdd(&sh.n_list, 1u)] = k;
+      if (bin(k) == edge) sh.edge[atomicAdd(&sh.n_edge, 1u)] = k;
     }
+    __syncthreads();
+    const int n_edge = static_cast<int>(sh.n_edge);
+    if (tid < n_edge) {
+      const key64 mine = sh.edge[tid];
+      int larger = 0;
+      for (int i = 0; i < n_edge; ++i) larger += sh.edge[i] > mine;
+      if (larger < left) sh.list[n_list - left + larger] = mine;
+    }
+    __syncthreads();
+    return;
+  }
+  key64 prefix = 0;     // the digits of the n_list-th largest so far, the rest zero
+  left = n_list;
+  for (int shift = 56; shift >= 0; shift -= 8) {
+    __syncthreads();
+    if (tid < 256) sh.hist[tid] = 0;
+    __syncthreads();
+    for (int i = tid; i < n; i += kTopThreads) {
+      const key64 k = cand[i];
+      if (shift == 56 || (k >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&sh.hist[(k >> shift) & 255u], 1u);
+    }
+    __syncthreads();
+    find_bin(sh, left);
+    __syncthreads();
+    prefix |= static_cast<key64>(sh.digit) << shift;
+    left = sh.left;
+    if (static_cast<unsigned>(left) == sh.hist[sh.digit]) break;   // the whole bin
   }
   for (int i = tid; i < n; i += kTopThreads)
     if (cand[i] >= prefix) sh.list[atomicAdd(&sh.n_list, 1u)] = cand[i];
@@ -251,15 +322,40 @@ __device__ __noinline__ void select_from_row(TopShared& sh, const unsigned char*
   __syncthreads();
 }
 
+// fl(m c), kept in range, and how far it lies above m c (0 where it does not
+// stand for m c: see sum_again).
+__device__ __forceinline__ float top_scale(float m, float c) { return fmaxf(__fmul_rn(m, c), -FLT_MAX); }
+__device__ __forceinline__ float top_residue(float m, float c) {
+  const float k = __fmul_rn(m, c);
+  return k > -FLT_MAX ? -__fmaf_rn(m, c, -k) : 0.f;
+}
+
+// S of a row whose M c is below the range, as 2^((z - M) c).
 template <int ELT>
-__global__ void __launch_bounds__(kTopThreads, 2) top_kernel(const TopParams P) {
+__device__ __noinline__ float sum_again(TopShared& sh, const unsigned char* row, int V, float M, float c) {
+  const int shift = row_shift<ELT>(row), nvec = row_vecs<ELT>(V, shift);
+  float s = 0.f;
+  for (int v = threadIdx.x; v < nvec; v += kTopThreads) {
+    float z[Vec<ELT>::N];
+    Vec<ELT>::unpack(load_row_vec<ELT>(row, V, shift, v), z);
+    for (int e = 0; e < Vec<ELT>::N; ++e) s += fast_exp2(__fmul_rn(__fsub_rn(z[e], M), c));
+  }
+  s = warp_sum(s);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) sh.ws[threadIdx.x >> 5] = s;
+  __syncthreads();
+  s = 0.f;
+  for (int w = 0; w < kTopWarps; ++w) s += sh.ws[w];
+  return s;
+}
+
+template <int ELT>
+__global__ void __launch_bounds__(kTopThreads, 4) top_kernel(const __grid_constant__ TopParams P) {
   using VT = Vec<ELT>;
   constexpr int N = VT::N;
   extern __shared__ __align__(16) unsigned char smem[];
   TopShared& sh = *reinterpret_cast<TopShared*>(smem);
-  uint4* vecs = reinterpret_cast<uint4*>(smem + kTopVecsAt);
-  int* vec_at = reinterpret_cast<int*>(smem + kTopIdsAt);
-  key64* tokens = reinterpret_cast<key64*>(smem + kTopTokensAt);
+  key64* tokens = sh.tokens;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int ctas = cluster_ctas(), rank = cluster_rank();
   const long long r = blockIdx.x / ctas;
@@ -275,133 +371,181 @@ __global__ void __launch_bounds__(kTopThreads, 2) top_kernel(const TopParams P) 
   }
   const int shift = row_shift<ELT>(row), nvec = row_vecs<ELT>(P.V, shift);
   const int part = (nvec + ctas - 1) / ctas;
-  const int v0 = min(nvec, rank * part), v1 = min(nvec, v0 + part);
+  int v0 = min(nvec, rank * part), v1 = min(nvec, v0 + part);
+  if (tid == 0) sh.n_places = sh.n_tokens = sh.n_list = sh.lost = 0;
+  if (tid < kTopWarps) sh.wt[tid] = ordered_key(-FLT_MAX);
+  __syncthreads();
+  if (ctas > 1) cluster_arrive();      // the counters are set
 
-  auto load = [&](uint4 (&w)[kTopUnroll], int base) {
-    // inside the part and away from the row's first and last vector
-    if (base >= v0 + 1 && base + kTopTile < v1) {
-      const unsigned char* at = row + (static_cast<long long>(base + tid) * N - shift) * ELT;
-#pragma unroll
-      for (int q = 0; q < kTopUnroll; ++q) w[q] = load_vec16(at + q * kTopThreads * 16);
-    } else {
-#pragma unroll
-      for (int q = 0; q < kTopUnroll; ++q) {
-        const int v = base + q * kTopThreads + tid;
-        w[q] = v < v1 ? load_row_vec<ELT>(row, P.V, shift, v) : VT::neg_inf();
-      }
-    }
-  };
-
-  float m = -INFINITY, t = -FLT_MAX;   // below t nothing is a candidate, nor is -inf
+  float m = -INFINITY, m2 = -INFINITY, k0 = 0.f;
+  float t = -FLT_MAX;                  // below t nothing is a candidate, nor is -inf
   f2 s2 = 0ull;
   const f2 cc = pack2(P.c2, P.c2);
-  uint4 w[kTopUnroll];
-  load(w, v0);
-  if (tid == 0) sh.n_vecs = sh.n_tokens = sh.n_list = sh.lost = 0;
-  if (ctas > 1) {
-    __syncthreads();
-    cluster_arrive();                  // the counters are set
-  }
-  int tile = 0;
-  for (int base = v0; base < v1; base += kTopTile, ++tile) {
-    uint4 next[kTopUnroll];
-    if (base + kTopTile < v1) load(next, base + kTopTile);
+  const unsigned below = (1u << lane) - 1u;
+  // A thread's vectors of a tile, the first of them vector `at`.
+  auto take = [&](const uint4 (&w)[kTopUnroll], int at, bool publish, bool barrier) {
     const float vm = VT::vmax(w);        // NaN is passed over here and kept by the sum
+    m2 = fmaxf(m2, fminf(m, vm));
     if (vm > m) {
-      if (m > -INFINITY) {
-        const float f = fast_exp2(__fmul_rn(__fsub_rn(m, vm), P.c2));
-        s2 = mul2(s2, pack2(f, f));
-      }
+      const float kn = fmaxf(__fmul_rn(vm, P.c2), -FLT_MAX);
+      const float f = m > -INFINITY ? fast_exp2(__fsub_rn(k0, kn)) : 0.f;
+      s2 = mul2(s2, pack2(f, f));
       m = vm;
+      k0 = kn;
     }
-    const float mb = m > -INFINITY ? m : 0.f;
-    const f2 mm = pack2(mb, mb);
+    const f2 nk = pack2(-k0, -k0);
 #pragma unroll
     for (int q = 0; q < kTopUnroll; ++q) {
       f2 z[N / 2];
       VT::pairs(w[q], z);
 #pragma unroll
-      for (int i = 0; i < N / 2; ++i) s2 = add2(s2, exp2_2(mul2(sub2(z[i], mm), cc)));
+      for (int i = 0; i < N / 2; ++i) s2 = add2(s2, exp2_2(fma2(z[i], cc, nk)));
     }
-    // ---- t: after the first tile, and each time the tiles seen have doubled
-    if ((tile & (tile + 1)) == 0) {
-      const float part_t = __shfl_sync(0xffffffffu, warp_sort(m, lane), P.quota - 1);
-      if (lane == 0) sh.wt[warp] = part_t;
-      if (tile == 0) __syncthreads();
+    if (publish) {
+      const float part_t = quota_of(m, m2, P.quota, lane);
+      if (lane == 0) sh.wt[warp] = ordered_key(fmaxf(part_t, -FLT_MAX));
+      if (barrier) __syncthreads();
     }
-    const float seen = sh.wt[lane & (kTopWarps - 1)];
-    t = fmaxf(from_ordered_key(__reduce_min_sync(0xffffffffu, ordered_key(seen))), -FLT_MAX);
-    if (__any_sync(0xffffffffu, vm >= t)) {
+    t = from_ordered_key(__reduce_min_sync(0xffffffffu, sh.wt[lane & (kTopWarps - 1)]));
+    const unsigned who = __ballot_sync(0xffffffffu, vm >= t);
+    if (who) {
+      unsigned note = 0;
+      if (lane == 0) note = atomicAdd(&sh.n_places, __popc(who));
+      note = __shfl_sync(0xffffffffu, note, 0) + __popc(who & below);
+      if (vm >= t) {
+        if (note < kTopPlaces) sh.places[note] = at;
+        if (note < kTopHeld) {
 #pragma unroll
-      for (int q = 0; q < kTopUnroll; ++q) {
-        const uint4 one[1] = {w[q]};
-        const bool keep = VT::vmax(one) >= t;
-        const unsigned who = __ballot_sync(0xffffffffu, keep);
-        if (!who) continue;
-        unsigned at = 0;
-        if (lane == 0) at = atomicAdd(&sh.n_vecs, __popc(who));
-        at = __shfl_sync(0xffffffffu, at, 0) + __popc(who & ((1u << lane) - 1u));
-        if (keep && at < kTopVecs) {
-          vecs[at] = w[q];
-          vec_at[at] = base + q * kTopThreads + tid;
+          for (int q = 0; q < kTopUnroll; ++q) sh.held[q][note] = w[q];
         }
       }
     }
+  };
+
+  // ---- a first tile of the row's ends where they are not whole vectors (two
+  // threads, in the CTAs that have them, padded with -inf; nothing is known of
+  // t then, so they are noted whatever they hold, and first), then full tiles,
+  // the next one's loads ahead, then the rest
+  const bool head = shift != 0 && v0 == 0, tail = v1 == nvec && (P.V + shift) % N != 0 && v1 > v0;
+  const int ends = head || tail;
+  int place = v0 + head + tid;
+  uint4 a[kTopUnroll], b[kTopUnroll];
+  if (ends) {
 #pragma unroll
-    for (int q = 0; q < kTopUnroll; ++q) w[q] = next[q];
+    for (int q = 0; q < kTopUnroll; ++q) a[q] = VT::neg_inf();
+    if (tid == 0 && head) a[0] = load_row_vec<ELT>(row, P.V, shift, place = 0);
+    if (tid == 1 && tail && nvec > head) a[0] = load_row_vec<ELT>(row, P.V, shift, place = nvec - 1);
+    v0 += head;
+    v1 -= tail;
+  }
+  const unsigned char* at = row + (static_cast<long long>(v0 + tid) * N - shift) * ELT;
+  int left = v1 - v0;                    // vectors not yet loaded
+  auto load = [&](uint4 (&w)[kTopUnroll]) {
+    if (left >= kTopTile) {
+#pragma unroll
+      for (int q = 0; q < kTopUnroll; ++q) w[q] = load_vec16(at + q * kTopThreads * 16);
+    } else {
+#pragma unroll
+      for (int q = 0; q < kTopUnroll; ++q)
+        w[q] = tid + q * kTopThreads < left ? load_vec16(at + q * kTopThreads * 16) : VT::neg_inf();
+    }
+    at += kTopTile * 16;
+    left -= kTopTile;
+  };
+  // t is published after the first full tile (with a barrier) and each time
+  // the tiles taken have doubled
+  int tiles = -ends;                     // taken, not counting the ends
+  if (!ends) load(a);
+  for (;;) {
+    const bool more = left > 0;
+    if (more) load(b);
+    take(a, place, tiles >= 0 && (tiles & (tiles + 1)) == 0, tiles == 0);
+    if (++tiles == 0) place = v0 + tid;
+    else place += kTopTile;
+    if (!more) break;
+    const bool again = left > 0;
+    if (again) load(a);
+    take(b, place, (tiles & (tiles + 1)) == 0, tiles == 0);
+    ++tiles;
+    place += kTopTile;
+    if (!again) break;
   }
 
-  // ---- this CTA's M, S and t
+  // ---- this CTA's t, M and S
   float s, s_hi;
   unpack2(s2, s, s_hi);
   s += s_hi;
-  const float part_t = __shfl_sync(0xffffffffu, warp_sort(m, lane), P.quota - 1);
-  if (s != s) m = NAN;   // a NaN is carried by the maximum
-  float wm = m;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) wm = fmax_nan(wm, __shfl_xor_sync(0xffffffffu, wm, o));
-  float ws = m > -INFINITY ? s * fast_exp2(__fmul_rn(__fsub_rn(m, wm), P.c2)) : 0.f;
-  ws = warp_sum(ws);
-  if (lane == 0) sh.wm[warp] = wm, sh.ws[warp] = ws, sh.wt[warp] = part_t;
+  if (tiles & (tiles - 1)) {             // tiles taken since t was published
+    const float part_t = quota_of(m, m2, P.quota, lane);
+    if (lane == 0) sh.wt[warp] = ordered_key(fmaxf(part_t, -FLT_MAX));
+  }
+  // a NaN is carried by the maximum
+  float wm = from_ordered_key(__reduce_max_sync(0xffffffffu, ordered_key(m)));
+  if (__any_sync(0xffffffffu, s != s)) wm = NAN;
+  const float ws = warp_sum(m > -INFINITY ? s * fast_exp2(__fsub_rn(k0, top_scale(wm, P.c2))) : 0.f);
+  if (lane == 0) sh.wm[warp] = wm, sh.ws[warp] = ws;
   __syncthreads();
   if (ctas > 1) cluster_wait();        // the first CTA's counters are set
-  if (warp == 0) {
+  t = from_ordered_key(__reduce_min_sync(0xffffffffu, sh.wt[lane & (kTopWarps - 1)]));
+  if (warp == kTopWarps - 1) {         // the warp with the fewest notes to look at
     const bool in = lane < kTopWarps;
     const float lm = in ? sh.wm[lane] : -INFINITY;
     float M = lm;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) M = fmax_nan(M, __shfl_xor_sync(0xffffffffu, M, o));
-    const float S = warp_sum(lm > -INFINITY ? sh.ws[lane] * fast_exp2(__fmul_rn(__fsub_rn(lm, M), P.c2)) : 0.f);
+    const float S = warp_sum(lm > -INFINITY ? sh.ws[lane] * fast_exp2(__fsub_rn(top_scale(lm, P.c2), top_scale(M, P.c2))) : 0.f);
     if (lane == 0) {
       first_store(&sh.M[rank], M);
       first_store(&sh.S[rank], S);
+      first_store(&sh.t[rank], t);
     }
   }
-  {
-    const float seen = sh.wt[lane & (kTopWarps - 1)];
-    t = fmaxf(from_ordered_key(__reduce_min_sync(0xffffffffu, ordered_key(seen))), -FLT_MAX);
-  }
-  // ---- the kept vectors' tokens at or above t
-  const bool whole = sh.n_vecs <= kTopVecs;
-  const int n_vecs = static_cast<int>(whole ? sh.n_vecs : 0u);
-  for (int i = tid; i < n_vecs; i += kTopThreads) {
-    float z[N];
-    VT::unpack(vecs[i], z);
-    const int t0 = vec_at[i] * N - shift;
+  // ---- the noted vectors' tokens at or above t
+  const bool whole = sh.n_places <= kTopPlaces;
+  const int n_places = static_cast<int>(whole ? sh.n_places : 0u);
+  for (int i0 = warp * 32; i0 < n_places; i0 += kTopThreads) {
+    const int i = i0 + lane;
+    if (i >= n_places) break;
+    const int first = sh.places[i];
+    uint4 w[kTopUnroll];
+    if (i < kTopHeld) {
 #pragma unroll
-    for (int e = 0; e < N; ++e)
-      if (z[e] >= t) {
-        const unsigned at = atomicAdd(&sh.n_tokens, 1u);
-        if (at < kTopCap) tokens[at] = top_entry(top_key(z[e]), static_cast<uint32_t>(t0 + e));
+      for (int q = 0; q < kTopUnroll; ++q) w[q] = sh.held[q][i];
+    } else {
+      // (never a row's end: those are noted first)
+#pragma unroll
+      for (int q = 0; q < kTopUnroll; ++q) {
+        const int v = first + q * kTopThreads;
+        w[q] = v < v1 ? load_vec16(row + (static_cast<long long>(v) * N - shift) * ELT) : VT::neg_inf();
       }
+    }
+    unsigned in = 0;                     // the vectors with a token at or above t
+#pragma unroll
+    for (int q = 0; q < kTopUnroll; ++q) {
+      const uint4 one[1] = {w[q]};
+      in |= static_cast<unsigned>(VT::vmax(one) >= t) << q;
+    }
+    for (; in; in &= in - 1) {
+      const int q = __ffs(in) - 1;
+      const uint4 one = q == 0 ? w[0] : q == 1 ? w[1] : q == 2 ? w[2] : w[3];
+      float z[N];
+      VT::unpack(one, z);
+      const int t0 = (first + q * kTopThreads) * N - shift;
+#pragma unroll
+      for (int e = 0; e < N; ++e)
+        if (z[e] >= t) {
+          const unsigned at = atomicAdd(&sh.n_tokens, 1u);
+          if (at < kTopCap) tokens[at] = top_entry(top_key(z[e]), static_cast<uint32_t>(t0 + e));
+        }
+    }
   }
   if (rank != 0) {
     __syncthreads();
-    // at most kTopPush: where there are more, the K largest
+    // at most P.push: where there are more, the K largest
     unsigned n = sh.n_tokens;
     const key64* from = tokens;
-    if (n > kTopPush && n <= kTopCap) {
-      select_entries(sh, tokens, static_cast<int>(n), P.K);
+    if (n > P.push && n <= kTopCap) {
+      select_entries(sh, tokens, static_cast<int>(n), P.K, top_key(t), 0xffffffffu);
       from = sh.list;
       n = P.K;
     }
@@ -427,40 +571,73 @@ __global__ void __launch_bounds__(kTopThreads, 2) top_kernel(const TopParams P) 
   }
 
   // ---- the row's M and S
-  float M = -INFINITY, S = 0.f;
+  float M = -INFINITY, S = 0.f, t_min = INFINITY;
+  for (int c = 0; c < ctas; ++c) t_min = fminf(t_min, sh.t[c]);
   for (int c = 0; c < ctas; ++c) M = fmax_nan(M, sh.M[c]);
   for (int c = 0; c < ctas; ++c)
-    if (sh.M[c] > -INFINITY) S += sh.S[c] * fast_exp2(__fmul_rn(__fsub_rn(sh.M[c], M), P.c2));
+    if (sh.M[c] > -INFINITY) S += sh.S[c] * fast_exp2(__fsub_rn(top_scale(sh.M[c], P.c2), top_scale(M, P.c2)));
+  if (S == 0.f && isfinite(M)) S = sum_again<ELT>(sh, row, P.V, M, P.c2);
   const bool valid = S > 0.f && isfinite(S) && isfinite(M);   // not NaN, +inf, or nothing but -inf
-  int listed = 0;
+  const float L = __fmaf_rn(0.6931471805599453f, top_residue(M, P.c2), logf(S));
+  int listed = 0, n_ranked = 0;        // entries of the list, and those that are ranked for it
+  const key64* from = tokens;
   if (valid) {
-    if (!sh.lost && sh.n_tokens <= kTopCap) {
-      const int n = static_cast<int>(sh.n_tokens);
-      listed = min(P.K, n);
-      select_entries(sh, tokens, n, listed);
-    } else {
-      // more candidates than the buffers hold: K of them at least
-      listed = P.K;
-      select_from_row<ELT>(sh, row, P.V, listed);
+    const bool fits = !sh.lost && sh.n_tokens <= kTopCap;
+    n_ranked = static_cast<int>(sh.n_tokens);
+    listed = fits ? min(P.K, n_ranked) : P.K;
+    if (!fits || n_ranked > kTopCount) {
+      // more candidates than the buffers hold are K of them at least
+      if (fits) select_entries(sh, tokens, n_ranked, listed, top_key(t_min), top_key(M));
+      else select_from_row<ELT>(sh, row, P.V, listed);
+      from = sh.list;
+      n_ranked = listed;
     }
   }
-  // ---- in order: each entry's place is the number of larger ones
-  const float L = logf(S);
-  for (int j = tid; j < P.K; j += kTopThreads) {
-    if (j >= listed) {
-      ids[j] = -1;
-      logp[j] = valid ? -INFINITY : NAN;
-      continue;
-    }
-    const key64 mine = sh.list[j];
+  // ---- in order: each entry's place is the number of larger ones, counted by
+  // one thread or by two or four neighbours
+  const int lg = n_ranked <= kTopThreads / 4 ? 2 : n_ranked <= kTopThreads / 2 ? 1 : 0;
+  for (int i0 = 0; i0 < n_ranked; i0 += kTopThreads >> lg) {
+    const int j = i0 + (tid >> lg);
+    if (i0 + (warp * 32 >> lg) >= n_ranked) break;   // the whole warp
+    const key64 mine = from[min(j, n_ranked - 1)];
     int place = 0;
-    for (int i = 0; i < listed; ++i) place += sh.list[i] > mine;
-    const float z = key_value(static_cast<uint32_t>(mine >> 32));
-    ids[place] = static_cast<int>(~static_cast<uint32_t>(mine));
-    logp[place] = __fsub_rn(__fdiv_rn(__fsub_rn(z, M), P.T), L);
+#pragma unroll 4
+    for (int i = tid & ((1 << lg) - 1); i < n_ranked; i += 1 << lg) place += from[i] > mine;
+    if (lg >= 1) place += __shfl_xor_sync(0xffffffffu, place, 1);
+    if (lg >= 2) place += __shfl_xor_sync(0xffffffffu, place, 2);
+    if (j < n_ranked && place < listed && (tid & ((1 << lg) - 1)) == 0) {
+      const float z = key_value(static_cast<uint32_t>(mine >> 32));
+      ids[place] = static_cast<int>(~static_cast<uint32_t>(mine));
+      logp[place] = __fsub_rn(__fdiv_rn(__fsub_rn(z, M), P.T), L);
+    }
   }
+  for (int j = listed + tid; j < P.K; j += kTopThreads) ids[j] = -1, logp[j] = valid ? -INFINITY : NAN;
   if (tid == 0) P.lse[r] = valid ? __fadd_rn(__fdiv_rn(M, P.T), L) : M == -INFINITY ? -INFINITY : NAN;
 }
+
+template <int ELT>
+cudaError_t launch_top(TopParams p, int rows, cudaStream_t s) {
+  // A row is split only where there are few: each part has its own first tile,
+  // in which little is known of t, and its own end.  Half a tile at least to
+  // each part; long lists, whose parts cost more to join, are split less.
+  const int nvec = p.V / Vec<ELT>::N, most = p.K > 128 ? 4 : 8, full = p.K > 128 ? 32 : 304;
+  int cluster = 1;
+  while (cluster < most && static_cast<long long>(rows) * 2 * cluster <= full && nvec / (2 * cluster) >= kTopTile / 2) cluster *= 2;
+  const int smem = static_cast<int>(sizeof(TopShared));
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = cluster;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(rows) * cluster);
+  cfg.blockDim = dim3(kTopThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, top_kernel<ELT>, p);
+}
+static_assert(sizeof(TopShared) <= 48 * 1024, "no attribute needed to launch");
 
 }  // namespace
 }  // namespace sv
@@ -480,26 +657,10 @@ extern "C" sv_status spec_kd_top(int n_seq, int t_len, int V, sv_dtype dtype, co
   const double c2 = 1.4426950408889634 / static_cast<double>(temperature);
   if (!(c2 < 1e30)) return SV_ERR_INVALID_ARG;
   TopParams p{static_cast<const unsigned char*>(target_logits), n_rows, ids, logp, lse, t_len, V, K,
-              static_cast<float>(c2), temperature, (K + kTopWarps - 1) / kTopWarps};
-  // as many CTAs to a row as leave each two tiles, until there are enough of them
-  const int rows = n_seq * t_len, nvec = V / (16 / elt);
-  int cluster = 1;
-  while (cluster < 8 && static_cast<long long>(rows) * cluster < kTopFewRows && nvec / (2 * cluster) >= 2 * kTopTile) cluster *= 2;
+              static_cast<float>(c2), temperature, (K + kTopWarps - 1) / kTopWarps, K > 128 ? 256 : 192};
+  const int rows = n_seq * t_len;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   NvtxRange range("spec_kd_top");
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = cluster;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(rows) * cluster);
-  cfg.blockDim = dim3(kTopThreads);
-  cfg.dynamicSmemBytes = kTopSmem;
-  cfg.stream = reinterpret_cast<cudaStream_t>(stream);
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  // 105 KB a CTA: more than the 48 KB that need no asking
-  const void* fn = elt == 2 ? reinterpret_cast<const void*>(&top_kernel<2>) : reinterpret_cast<const void*>(&top_kernel<4>);
-  if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kTopSmem) != cudaSuccess) return SV_ERR_CUDA;
-  const cudaError_t e = elt == 2 ? cudaLaunchKernelEx(&cfg, top_kernel<2>, p) : cudaLaunchKernelEx(&cfg, top_kernel<4>, p);
+  const cudaError_t e = elt == 2 ? launch_top<2>(p, rows, st) : launch_top<4>(p, rows, st);
   return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? SV_OK : SV_ERR_CUDA;
 }
