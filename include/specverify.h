@@ -409,8 +409,8 @@ sv_status spec_kd_top(int n_seq, int t_len, int V, sv_dtype dtype, const void *t
  * read.  NaN or +inf in the draft row or the list, a draft row that is all
  * -inf, an id >= V or one listed twice give a NaN KL, NaN gradient and NaN
  * loss for the rollout; a listed token with p_j > 0 (or, with r > 0, all
- * others) at draft logit -inf gives KL = +inf.  K as for spec_kd_top,
- * V <= 524288.  Asynchronous on `stream`; no context, no workspace, no
+ * others) at draft logit -inf gives KL = +inf.  K and the rows as for
+ * spec_kd_top, V * sizeof(dtype) <= 1 MiB.  Asynchronous on `stream`; no context, no workspace, no
  * allocation; every sum is taken in a fixed order.  Host-checkable errors
  * return SV_ERR_INVALID_ARG and launch nothing. */
 typedef enum { SV_KD_TOP_TAIL = 0, SV_KD_TOP_RENORM = 1 } sv_kd_top_mode;
