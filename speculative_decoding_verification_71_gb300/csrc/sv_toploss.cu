@@ -12,13 +12,25 @@
 // logits.  So with E = 2^((z - M) c) the gradient of an unlisted token is one multiply,
 // E * w / T * (1 / Z - r / S), Z the row's whole sum scaled alike.
 //
-// A row goes to a cluster of up to 8 CTAs and stays in their registers: every
-// thread loads its vectors of the row once, the cluster exchanges each part's
-// (M, S) of the unlisted tokens and the same of the listed ones through
-// distributed shared memory, and the gradient is stored from the registers.
-// Each logit crosses HBM once and each gradient once, with no second read.
-// The listed tokens are marked in a bitmap of the part and gathered by a
-// thread each, which stores their gradients after the row's.
+// Rows go to clusters of 1 to 8 CTAs, two CTAs to an SM, row c + i * clusters
+// to cluster c; each CTA takes a part of the row.  A producer warp streams it
+// through a ring of three 32 KB slots, 8 consumer warps sum it and, for the
+// gradient, take it a second time from L2, where it was a few microseconds
+// before.  The ring runs ahead over the end of a row, and the SM's other CTA
+// fills what is left of the gap while a row's numbers are put together.  A
+// marking warp stands between producer and consumers: it puts -inf in the
+// listed tokens' places of a slot, so that the consumers need not look for
+// them (a look at a byte a vector was an eighth of their instructions).  Every
+// CTA gathers the listed tokens' logits itself, a thread each, so the CTAs of
+// a cluster exchange nothing but their (M, S), through distributed shared
+// memory; the listed tokens' gradients are stored after the row's.
+//
+// 4096 rows of 151936 bf16 logits with their gradients: 455 us, 5.5 TB/s of
+// each logit read and each gradient written once; the loss alone 190 us, 6.5
+// TB/s.  With one CTA to a row the rows at work do not stay in L2 (452 MB read
+// for 311 MB of rows) and the gradients take 523 us.  Kept in the registers of
+// a cluster's CTAs in place of read twice: 742 us, each CTA idle while the
+// row's numbers go round.
 
 #include <cuda_runtime.h>
 
@@ -64,19 +76,6 @@ struct TlRow {
   int valid;
 };
 
-template <int WARPS>
-struct TlShared {
-  TlPart part[kTlMaxCtas];     // the cluster's CTAs'
-  TlPart warp[WARPS];
-  float mass[WARPS];           // the warps' parts of P
-  float term[WARPS];           // ... of the listed tokens' divergence
-  float kl[kTlMaxCtas];        // (first CTA) the CTAs' parts of it
-  TlRow row;
-};
-
-__device__ __forceinline__ void tl_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
-__device__ __forceinline__ void tl_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
-
 // The parts of all lanes on their common maxima, the same in every lane and in
 // a fixed order; a NaN among the sums stays.
 __device__ __forceinline__ TlPart tl_combine(const TlPart& p, float c2, float inv_T) {
@@ -87,6 +86,35 @@ __device__ __forceinline__ TlPart tl_combine(const TlPart& p, float c2, float in
   r.s = warp_sum(p.m > -INFINITY ? p.s * fast_exp2(__fmul_rn(__fsub_rn(p.m, r.m), c2)) : p.s);
   r.sl = warp_sum(p.ml > -INFINITY ? p.sl * expf(__fmul_rn(__fsub_rn(p.ml, r.ml), inv_T)) : p.sl);
   return r;
+}
+
+// The row's numbers from its combined part: Ma = max(M, Ml), Z its whole sum.
+__device__ __forceinline__ TlRow tl_row(const TlPart& part, float mass, float scale, const TopLossParams& P) {
+  TlRow R;
+  R.Ma = fmaxf(part.m, part.ml);
+  R.valid = part.s == part.s && R.Ma > -INFINITY && R.Ma < INFINITY;
+  // the listed tokens carry most of Z: full-precision exponentials for them
+  const float lt = __fmul_rn(__fsub_rn(part.m, R.Ma), P.inv_T);
+  const float ft = part.m > -INFINITY ? expf(lt) : 0.f;
+  const float fl = part.ml > -INFINITY ? expf(__fmul_rn(__fsub_rn(part.ml, R.Ma), P.inv_T)) : 0.f;
+  R.Z = __fadd_rn(__fmul_rn(part.s, ft), __fmul_rn(part.sl, fl));
+  R.LZ = logf(R.Z);
+  R.mass = mass;
+  float rest = P.renorm ? 0.f : __fsub_rn(1.f, mass);
+  if (rest < kTlComplete) rest = 0.f;
+  R.a = R.valid ? scale * __fsub_rn(__fdiv_rn(ft, R.Z), part.s > 0.f ? __fdiv_rn(rest, part.s) : 0.f) : NAN;
+  R.base = part.m > -INFINITY ? part.m : 0.f;
+  R.kl = 0.f;
+  if (rest > 0.f) R.kl = part.s > 0.f ? rest * (logf(rest) - __fsub_rn(__fadd_rn(lt, logf(part.s)), R.LZ)) : INFINITY;
+  return R;
+}
+
+// Whether `x` holds for any of the `threads` threads at barrier 1.
+__device__ __forceinline__ bool tl_any(bool x, int threads) {
+  int any;
+  asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.s32 p, %1, 0;\n\tbarrier.red.or.pred q, 1, %2, p;\n\t"
+               "selp.s32 %0, 1, 0, q;\n\t}" : "=r"(any) : "r"(static_cast<int>(x)), "r"(threads) : "memory");
+  return any != 0;
 }
 
 // A vector with -inf in the places of `bits`.
@@ -103,275 +131,434 @@ __device__ __noinline__ uint4 with_neg_inf(uint4 w, uint32_t bits) {
 
 // A vector's gradients where it may reach past its row, or the rows lie unlike.
 template <int ELT>
-__device__ __noinline__ void store_edge(unsigned char* grad, int V, int t0, int same_shift, const float (&g)[Vec<ELT>::N]) {
+__device__ __noinline__ void store_edge(unsigned char* grad, int V, int t0, int same_shift, uint4 g) {
   constexpr int N = Vec<ELT>::N;
   if (same_shift && t0 >= 0 && t0 <= V - N) {
-    store_vec16(grad + static_cast<long long>(t0) * ELT, Vec<ELT>::pack(g));
+    store_vec16(grad + static_cast<long long>(t0) * ELT, g);
     return;
   }
+  float z[N];
+  Vec<ELT>::unpack(g, z);
+#pragma unroll
   for (int e = 0; e < N; ++e)
-    if (t0 + e >= 0 && t0 + e < V) Vec<ELT>::store_rounded(grad, t0 + e, g[e]);
+    if (t0 + e >= 0 && t0 + e < V) Vec<ELT>::store_rounded(grad, t0 + e, z[e]);   // exact: of the type already
 }
 
-// NV vectors of the row per thread, in registers throughout.
-template <int ELT, int THREADS, int NV, int CTAS>
-__global__ void __launch_bounds__(THREADS, CTAS) toploss_kernel(const __grid_constant__ TopLossParams P) {
+constexpr int kTrWarps = 8;                           // consumer warps
+constexpr int kTrConsumers = kTrWarps * 32;
+constexpr int kTrThreads = kTrConsumers + 64;         // + the producer and the marking warp
+constexpr int kTrCtas = 2;                            // to an SM
+constexpr int kTrSlots = 3;
+constexpr int kTrPerLane = 8;                         // vectors per lane and slot
+constexpr int kTrSlotVecs = kTrConsumers * kTrPerLane;
+constexpr int kTrHash = 1024;                         // places for a row's listed ids
+
+constexpr int kTrGrid = 152 * kTrCtas;                // CTAs that fit at once
+constexpr long long kTrInL2 = 72LL << 20;             // bytes of rows at work that L2 keeps
+constexpr int kTrMinPart = 16 * 1024;                 // a part's bytes where a row is split for want of rows
+
+struct TrShared {
+  uint64_t full[kTrSlots], ready[kTrSlots], empty[kTrSlots];
+  uint64_t joined[2];            // the cluster's parts of a row are here, by row parity as what follows
+  uint4 part[2][kTlMaxCtas];     // the CTAs' (M, S)
+  TlPart warp[2][kTrWarps];      // the warps' parts
+  float mass[2][kTrWarps];
+  float term[2][kTrWarps];
+  int ids[kTrHash];              // open addressing; -1: empty
+};
+constexpr int kTrRingAt = (static_cast<int>(sizeof(TrShared)) + 127) / 128 * 128;
+constexpr int kTrSmem = kTrRingAt + kTrSlots * kTrSlotVecs * 16;
+static_assert(kTrCtas * (kTrSmem + 1024) <= 228 * 1024, "the CTAs must fit on an SM");
+static_assert(kTrConsumers >= SV_KD_TOP_MAX, "a thread for each entry of the list");
+
+// Enters an id; its place, or -1 if it is there already.
+__device__ __forceinline__ int tr_enter(int* ids, int id) {
+  for (unsigned at = static_cast<unsigned>(id) * 2654435761u >> 22;; at = (at + 1) % kTrHash) {
+    const int there = atomicCAS(&ids[at], -1, id);
+    if (there == -1) return static_cast<int>(at);
+    if (there == id) return -1;
+  }
+}
+__device__ __forceinline__ bool tr_listed(const int* ids, int id) {
+  for (unsigned at = static_cast<unsigned>(id) * 2654435761u >> 22; ids[at] != -1; at = (at + 1) % kTrHash)
+    if (ids[at] == id) return true;
+  return false;
+}
+
+// A CTA's part of a row's whole vectors: the place of its first one, which of
+// the row's vectors that is, and their number (the row's ends are taken apart).
+struct TrRow {
+  const unsigned char* at;
+  int first, n;
+  template <int ELT>
+  __device__ __forceinline__ static TrRow of(const TopLossParams& P, long long r, int ctas, int rank) {
+    constexpr int N = Vec<ELT>::N;
+    const unsigned char* row = P.draft + r * P.V * ELT;
+    const int shift = row_shift<ELT>(row), nvec = row_vecs<ELT>(P.V, shift);
+    const int head = shift ? 1 : 0;
+    const int all = nvec - head - ((P.V + shift) % N && nvec > head ? 1 : 0);
+    const int per = (all + ctas - 1) / ctas;
+    TrRow t;
+    t.first = head + min(all, rank * per);
+    t.n = min(all, rank * per + per) - min(all, rank * per);
+    t.at = row + (static_cast<long long>(t.first) * N - shift) * ELT;
+    return t;
+  }
+};
+
+// Whether a row has a list, and whether anything is wrong with it, by one warp.
+__device__ __forceinline__ bool tr_has_list(const TopLossParams& P, long long r, int lane) {
+  bool any = false;
+  for (int j = lane; j < P.K; j += 32) {
+    const float lp = P.logp[r * P.K + j];
+    any |= P.ids[r * P.K + j] >= 0 || lp != lp || lp == INFINITY;
+  }
+  return __any_sync(0xffffffffu, any);
+}
+
+template <int ELT, bool GRAD>
+__global__ void __launch_bounds__(kTrThreads, kTrCtas) toploss_kernel(const __grid_constant__ TopLossParams P, int rows) {
   using VT = Vec<ELT>;
-  constexpr int N = VT::N, kWarps = THREADS / 32;
-  __shared__ TlShared<kWarps> sh;
-  __shared__ alignas(16) uint32_t listed_words[(THREADS * NV + 15) / 16 * 4];
-  uint8_t* listed = reinterpret_cast<uint8_t*>(listed_words);   // a bit per token of a vector: listed
+  constexpr int N = VT::N;
+  extern __shared__ __align__(1024) unsigned char smem[];
+  TrShared& sh = *reinterpret_cast<TrShared*>(smem);
+  unsigned char* ring = smem + kTrRingAt;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int ctas = cluster_ctas(), rank = cluster_rank();
-  const long long r = blockIdx.x / ctas;
-  const unsigned char* row = P.draft + r * P.V * ELT;
-  unsigned char* grad = P.grad ? P.grad + r * P.V * ELT : nullptr;
-  const int shift = row_shift<ELT>(row), nvec = row_vecs<ELT>(P.V, shift);
-  const int per = (nvec + ctas - 1) / ctas;
-  const int v0 = min(nvec, rank * per), v1 = min(nvec, v0 + per);
-  const int t_first = v0 * N - shift;      // token of the part's first element
-  // whether the part is of whole vectors only
-  const bool whole = t_first >= 0 && v1 * N - shift <= P.V;
-  const int n = v1 - v0 - tid;             // this thread's vectors: q THREADS < n
+  const int cluster = blockIdx.x / ctas, clusters = gridDim.x / ctas;
+  if (tid == 0) {
+    for (int b = 0; b < 2; ++b) mbar_init(&sh.joined[b], 1);
+    for (int s = 0; s < kTrSlots; ++s) {
+      mbar_init(&sh.full[s], 1);
+      mbar_init(&sh.ready[s], 1);
+      mbar_init(&sh.empty[s], kTrWarps + 1);
+    }
+    fence_mbar_init();
+  }
+  for (int w = tid; w < kTrHash; w += kTrThreads) sh.ids[w] = -1;
+  if (ctas > 1) cluster_sync();   // the others' barriers are set up too
+  else __syncthreads();
+  grid_dependents_launch();       // the sum of the rows may take its place on an SM
 
-  // ---- the list: thread j holds entries j and j + THREADS
-  constexpr int kE = (SV_KD_TOP_MAX + THREADS - 1) / THREADS;
-  int id[kE];
-  float lp[kE];
-  bool bad = false, any = false;
-#pragma unroll
-  for (int k = 0; k < kE; ++k) {
-    const int j = tid + k * THREADS;
-    id[k] = j < P.K ? P.ids[r * P.K + j] : -1;
-    lp[k] = j < P.K ? P.logp[r * P.K + j] : -INFINITY;
-  }
-  for (int w = tid; w < (per + 15) / 16; w += THREADS) reinterpret_cast<uint4*>(listed_words)[w] = make_uint4(0, 0, 0, 0);
-#pragma unroll
-  for (int k = 0; k < kE; ++k) {
-    bad |= lp[k] != lp[k] || lp[k] == INFINITY || id[k] >= P.V;
-    if (id[k] >= P.V) id[k] = -1;
-    any |= id[k] >= 0;
-  }
-  // a row without a list is not read and has no loss
-  if (!__syncthreads_or(any || bad)) {
-    if (rank == 0 && tid == 0) P.row_kl[r] = 0.f;
-    if (grad)
-      for (int v = v0 + tid; v < v1; v += THREADS) {
-        const int t0 = v * N - shift;
-        if (P.same_shift && t0 >= 0 && t0 <= P.V - N) {
-          store_vec16(grad + static_cast<long long>(t0) * ELT, make_uint4(0, 0, 0, 0));
-        } else {
-          for (int e = 0; e < N; ++e)
-            if (t0 + e >= 0 && t0 + e < P.V) VT::store_rounded(grad, t0 + e, 0.f);
+  if (warp == kTrWarps) {
+    // ---- the producer: every row with a list once, for the gradient twice
+    const uint64_t first_out = evict_first_policy();
+    unsigned q = 0;
+    for (long long r = cluster; r < rows; r += clusters) {
+      if (!tr_has_list(P, r, lane)) continue;
+      const TrRow row = TrRow::of<ELT>(P, r, ctas, rank);
+      for (int pass = 0; pass < (GRAD ? 2 : 1); ++pass)
+        for (int v = 0; v < row.n; v += kTrSlotVecs, ++q) {
+          const int s = q % kTrSlots;
+          int ok = 1;
+          if (lane == 0) ok = mbar_wait_bounded(&sh.empty[s], ((q / kTrSlots) & 1) ^ 1, kDrainLimitNs) ? 1 : 0;
+          if (!__shfl_sync(0xffffffffu, ok, 0)) return;   // the consumers give up as well
+          if (lane == 0) {
+            const uint32_t bytes = static_cast<uint32_t>(min(kTrSlotVecs, row.n - v)) * 16u;
+            const unsigned char* src = row.at + static_cast<long long>(v) * 16;
+            mbar_expect_tx(&sh.full[s], bytes);
+            // the last read of a row marks its lines first out of L2
+            if (GRAD && pass == 0) bulk_load(ring + s * kTrSlotVecs * 16, src, bytes, &sh.full[s]);
+            else bulk_load_hint(ring + s * kTrSlotVecs * 16, src, bytes, &sh.full[s], first_out);
+          }
         }
-      }
+    }
     return;
   }
-  uint4 w[NV];
-  if (whole) {
-    const unsigned char* at = row + (static_cast<long long>(v0 + tid) * N - shift) * ELT;
-#pragma unroll
-    for (int q = 0; q < NV; ++q) w[q] = q * THREADS < n ? load_vec16(at + q * THREADS * 16) : VT::neg_inf();
-  } else {
-#pragma unroll
-    for (int q = 0; q < NV; ++q)
-      w[q] = q * THREADS < n ? load_row_vec<ELT>(row, P.V, shift, v0 + q * THREADS + tid) : VT::neg_inf();
-  }
-  bool mine[kE];
-  float zj[kE];
-#pragma unroll
-  for (int k = 0; k < kE; ++k) {
-    const int at = id[k] - t_first;        // the entry's place in the part
-    mine[k] = id[k] >= 0 && at >= 0 && at < (v1 - v0) * N;
-    zj[k] = -INFINITY;
-    if (mine[k]) {
-      const int bit = at / N * 8 + at % N;
-      bad |= (atomicOr(&listed_words[bit >> 5], 1u << (bit & 31)) >> (bit & 31)) & 1u;   // listed twice
-      zj[k] = load_elem<ELT>(row, id[k]);
-      bad |= zj[k] != zj[k] || zj[k] == INFINITY;
-    }
-  }
-  float p[kE], mass = 0.f;
-#pragma unroll
-  for (int k = 0; k < kE; ++k) mass += p[k] = id[k] >= 0 ? expf(lp[k]) : 0.f;
-  __syncthreads();
 
-  // ---- the part's sums
+  if (warp == kTrWarps + 1) {
+    // ---- the marking warp: the listed tokens out of the first pass's slots
+    unsigned q = 0;
+    for (long long r = cluster; r < rows; r += clusters) {
+      if (!tr_has_list(P, r, lane)) continue;
+      const TrRow row = TrRow::of<ELT>(P, r, ctas, rank);
+      const int t_first = static_cast<int>((row.at - (P.draft + r * P.V * ELT)) / ELT);   // the first slot's first token
+      int at[SV_KD_TOP_MAX / 32];
 #pragma unroll
-  for (int q = 0; q < NV; ++q) {
-    const uint32_t in = q * THREADS < n ? listed[q * THREADS + tid] : 0u;
-    if (in) w[q] = with_neg_inf<ELT>(w[q], in);   // out of the unlisted tokens' sum
-  }
-  const float m = VT::vmax(w);             // NaN is passed over here and kept by the sum
-  const float mb = m > -INFINITY ? m : 0.f;
-  const f2 cc = pack2(P.c2, P.c2), mm = pack2(mb, mb);
-  f2 s2 = 0ull, s3 = 0ull;
+      for (int k = 0; k < SV_KD_TOP_MAX / 32; ++k) {
+        const int j = k * 32 + lane, id = j < P.K ? P.ids[r * P.K + j] : -1;
+        at[k] = id >= 0 && id < P.V ? id - t_first : -1;
+      }
+      for (int pass = 0; pass < (GRAD ? 2 : 1); ++pass)
+        for (int v = 0; v < row.n; v += kTrSlotVecs, ++q) {
+          const int s = q % kTrSlots;
+          if (!__all_sync(0xffffffffu, mbar_wait_bounded(&sh.full[s], (q / kTrSlots) & 1u, kDrainLimitNs))) return;
+          if (pass == 0) {
+            unsigned char* slot = ring + s * kTrSlotVecs * 16;
+            const unsigned n = static_cast<unsigned>(min(kTrSlotVecs, row.n - v)) * N;
 #pragma unroll
-  for (int q = 0; q < NV; ++q) {
-    f2 z[N / 2];
-    VT::pairs(w[q], z);
-#pragma unroll
-    for (int i = 0; i < N / 2; i += 2) {
-      s2 = add2(s2, exp2_2(mul2(sub2(z[i], mm), cc)));
-      s3 = add2(s3, exp2_2(mul2(sub2(z[i + 1], mm), cc)));
-    }
-  }
-  float s, s_hi;
-  unpack2(add2(s2, s3), s, s_hi);
-  TlPart part{m, s + s_hi, zj[0], zj[0] > -INFINITY ? 1.f : 0.f};
-#pragma unroll
-  for (int k = 1; k < kE; ++k) {
-    const float top = fmaxf(part.ml, zj[k]);
-    if (top > -INFINITY)
-      part.sl = (part.ml > -INFINITY ? part.sl * expf(__fmul_rn(__fsub_rn(part.ml, top), P.inv_T)) : 0.f) +
-                (zj[k] > -INFINITY ? expf(__fmul_rn(__fsub_rn(zj[k], top), P.inv_T)) : 0.f);
-    part.ml = top;
-  }
-  if (bad) part.s = NAN;
-  part = tl_combine(part, P.c2, P.inv_T);
-  mass = warp_sum(mass);
-  if (lane == 0) sh.warp[warp] = part, sh.mass[warp] = mass;
-  __syncthreads();
-  const TlPart none{-INFINITY, 0.f, -INFINITY, 0.f};
-  if (warp == 0) {
-    part = tl_combine(lane < kWarps ? sh.warp[lane] : none, P.c2, P.inv_T);
-    if (ctas == 1) {
-      if (lane == 0) sh.part[0] = part;
-    } else if (lane < ctas) {              // to every CTA of the cluster
-      asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};"
-                   :: "r"(peer(&sh.part[rank], lane)), "f"(part.m), "f"(part.s), "f"(part.ml), "f"(part.sl) : "memory");
-    }
-  }
-  if (ctas > 1) {
-    tl_arrive();
-    tl_wait();
-  } else {
-    __syncwarp();
-  }
-
-  // ---- the row against Ma = max(M, Ml); Z its whole sum
-  const float scale = grad ? P.weights[r / P.t_len] * P.inv_T : 0.f;
-  if (warp == 0) {
-    part = tl_combine(lane < ctas ? sh.part[lane] : none, P.c2, P.inv_T);
-    mass = warp_sum(lane < kWarps ? sh.mass[lane] : 0.f);
-    TlRow R;
-    R.Ma = fmaxf(part.m, part.ml);
-    R.valid = part.s == part.s && R.Ma > -INFINITY && R.Ma < INFINITY;
-    // the listed tokens carry most of Z: full-precision exponentials for them
-    const float lt = __fmul_rn(__fsub_rn(part.m, R.Ma), P.inv_T);
-    const float ft = part.m > -INFINITY ? expf(lt) : 0.f;
-    const float fl = part.ml > -INFINITY ? expf(__fmul_rn(__fsub_rn(part.ml, R.Ma), P.inv_T)) : 0.f;
-    R.Z = __fadd_rn(__fmul_rn(part.s, ft), __fmul_rn(part.sl, fl));
-    R.LZ = logf(R.Z);
-    R.mass = mass;
-    float rest = P.renorm ? 0.f : __fsub_rn(1.f, mass);
-    if (rest < kTlComplete) rest = 0.f;
-    R.a = R.valid ? scale * __fsub_rn(__fdiv_rn(ft, R.Z), part.s > 0.f ? __fdiv_rn(rest, part.s) : 0.f) : NAN;
-    R.base = part.m > -INFINITY ? part.m : 0.f;
-    R.kl = 0.f;
-    if (rest > 0.f) R.kl = part.s > 0.f ? rest * (logf(rest) - __fsub_rn(__fadd_rn(lt, logf(part.s)), R.LZ)) : INFINITY;
-    if (lane == 0) sh.row = R;
-  }
-  __syncthreads();
-  const TlRow R = sh.row;
-
-  // ---- the gradient
-  if (grad) {
-    const f2 bb = pack2(R.base, R.base), aa = pack2(R.a, R.a);
-    auto gradient = [&](const uint4& x, float (&g)[N]) {
-      f2 z[N / 2];
-      VT::pairs(x, z);
-#pragma unroll
-      for (int i = 0; i < N / 2; ++i) unpack2(mul2(aa, exp2_2(mul2(sub2(z[i], bb), cc))), g[2 * i], g[2 * i + 1]);
-    };
-    if (whole && P.same_shift) {
-      unsigned char* at = grad + (static_cast<long long>(v0 + tid) * N - shift) * ELT;
-#pragma unroll
-      for (int q = 0; q < NV; ++q)
-        if (q * THREADS < n) {
-          float g[N];
-          gradient(w[q], g);
-          store_vec16(at + q * THREADS * 16, VT::pack(g));
+            for (int k = 0; k < SV_KD_TOP_MAX / 32; ++k) {
+              const int in = at[k] - v * N;
+              if (at[k] >= 0 && static_cast<unsigned>(in) < n) VT::store_scalar(slot, in, -INFINITY);
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // before the slot is filled again
+          }
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&sh.ready[s]);
+            mbar_arrive(&sh.empty[s]);
+          }
         }
+    }
+    return;
+  }
+
+  // ---- the consumers
+  const f2 cc = pack2(P.c2, P.c2);
+  unsigned q = 0;
+  bool dead = false;             // a wait has expired: every row from then on is NaN
+  int turn = 0;
+  // this lane's vectors of the slot, -inf past the row's; the slot is released
+  // as soon as they are in registers
+  auto take = [&](uint4 (&w)[kTrPerLane], int n, bool marked) {
+    const int s = q % kTrSlots;
+    const uint32_t phase = (q / kTrSlots) & 1u;
+    bool ok = !dead && mbar_wait_bounded(&sh.full[s], phase, kDrainLimitNs);
+    if (marked) ok = ok && mbar_wait_bounded(&sh.ready[s], phase, kDrainLimitNs);
+    dead = !__all_sync(0xffffffffu, ok);
+    const uint4* src = reinterpret_cast<const uint4*>(ring + s * kTrSlotVecs * 16) + tid;
+    if (n >= kTrSlotVecs) {
+#pragma unroll
+      for (int k = 0; k < kTrPerLane; ++k) w[k] = src[k * kTrConsumers];
     } else {
 #pragma unroll
-      for (int q = 0; q < NV; ++q)
-        if (q * THREADS < n) {
-          float g[N];
-          gradient(w[q], g);
-          store_edge<ELT>(grad, P.V, (v0 + q * THREADS + tid) * N - shift, P.same_shift, g);
+      for (int k = 0; k < kTrPerLane; ++k) w[k] = tid + k * kTrConsumers < n ? src[k * kTrConsumers] : VT::neg_inf();
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh.empty[s]);
+    ++q;
+  };
+  // the next row's list is loaded while this one is at work
+  int next_id = -1;
+  float next_lp = -INFINITY, next_weight = 0.f;
+  auto load_list = [&](long long r) {
+    if (r >= rows) return;
+    if (tid < P.K) {
+      next_id = P.ids[r * P.K + tid];
+      next_lp = P.logp[r * P.K + tid];
+    }
+    if (GRAD) next_weight = P.weights[r / P.t_len];
+  };
+  load_list(cluster);
+  for (long long r = cluster; r < rows; r += clusters) {
+    unsigned char* grad = GRAD ? P.grad + r * P.V * ELT : nullptr;
+    const unsigned char* start = P.draft + r * P.V * ELT;
+    const int shift = row_shift<ELT>(start), nvec = row_vecs<ELT>(P.V, shift);
+    // ---- the list: thread j holds entry j
+    int id = next_id;
+    float lp = next_lp;
+    const float weight = GRAD ? next_weight : 0.f;
+    load_list(r + clusters);
+    bool bad = lp != lp || lp == INFINITY || id >= P.V;
+    if (id >= P.V) id = -1;
+    if (!tl_any(id >= 0 || bad, kTrConsumers)) {         // no list: no loss
+      if (tid == 0 && rank == 0) P.row_kl[r] = 0.f;
+      if (GRAD)
+        for (int v = rank * kTrConsumers + tid; v < nvec; v += ctas * kTrConsumers) {
+          const int t0 = v * N - shift;
+          if (P.same_shift && t0 >= 0 && t0 <= P.V - N) {
+            store_vec16(grad + static_cast<long long>(t0) * ELT, make_uint4(0, 0, 0, 0));
+          } else {
+            for (int e = 0; e < N; ++e)
+              if (t0 + e >= 0 && t0 + e < P.V) VT::store_rounded(grad, t0 + e, 0.f);
+          }
         }
+      continue;
     }
-  }
+    const int par = turn & 1, phase = turn >> 1 & 1;
+    ++turn;                                // rows with a list
+    float zj = -INFINITY, p = 0.f;
+    int place = -1;
+    if (id >= 0) {
+      place = tr_enter(sh.ids, id);
+      bad |= place < 0;                    // listed twice
+      zj = load_elem<ELT>(start, id);
+      p = expf(lp);
+    }
+    const TrRow row = TrRow::of<ELT>(P, r, ctas, rank);
+    named_barrier_sync(1, kTrConsumers);
 
-  // ---- the listed tokens: their gradients after the row's, and the divergence
-  float term = 0.f, ej[kE];
+    // ---- the unlisted tokens: running maximum and sum per lane
+    float m = -INFINITY;
+    f2 s2 = 0ull, s3 = 0ull;
+    auto add = [&](const uint4 (&w)[kTrPerLane]) {
+      const float vm = VT::vmax(w);        // NaN is passed over here and kept by the sum
+      if (vm > m) {
+        const float f = m > -INFINITY ? fast_exp2(__fmul_rn(__fsub_rn(m, vm), P.c2)) : 0.f;
+        s2 = mul2(s2, pack2(f, f));
+        s3 = mul2(s3, pack2(f, f));
+        m = vm;
+      }
+      const float mb = m > -INFINITY ? m : 0.f;
+      const f2 mm = pack2(mb, mb);
 #pragma unroll
-  for (int k = 0; k < kE; ++k) {
-    const float lj = __fmul_rn(__fsub_rn(zj[k], R.Ma), P.inv_T);
-    ej[k] = zj[k] > -INFINITY ? __fdiv_rn(expf(lj), R.Z) : 0.f;
-    if (P.renorm) {
-      lp[k] = R.mass > 0.f ? __fsub_rn(lp[k], logf(R.mass)) : -INFINITY;
-      p[k] = R.mass > 0.f ? __fdiv_rn(p[k], R.mass) : 0.f;
+      for (int k = 0; k < kTrPerLane; ++k) {
+        f2 z[N / 2];
+        VT::pairs(w[k], z);
+#pragma unroll
+        for (int i = 0; i < N / 2; i += 2) {
+          s2 = add2(s2, exp2_2(mul2(sub2(z[i], mm), cc)));
+          s3 = add2(s3, exp2_2(mul2(sub2(z[i + 1], mm), cc)));
+        }
+      }
+    };
+    // the row's ends, where they are not whole vectors, by two threads of the
+    // first CTA
+    int end = -1;
+    if (rank == 0 && tid == 0 && shift) end = 0;
+    if (rank == 0 && tid == 1 && (P.V + shift) % N && nvec > (shift ? 1 : 0)) end = nvec - 1;
+    uint4 end_vec = VT::neg_inf();
+    if (end >= 0) end_vec = load_row_vec<ELT>(start, P.V, shift, end);
+    for (int v = 0; v < row.n; v += kTrSlotVecs) {
+      uint4 w[kTrPerLane];
+      take(w, row.n - v, true);
+      add(w);
     }
-    if (mine[k] && p[k] > 0.f) term += __fmul_rn(p[k], __fsub_rn(lp[k], __fsub_rn(lj, R.LZ)));
-  }
-  term = warp_sum(term);
-  if (lane == 0) sh.term[warp] = term;
-  __syncthreads();
+    if (warp == 0) {
+      uint4 w[kTrPerLane];
 #pragma unroll
-  for (int k = 0; k < kE; ++k)
-    if (grad && mine[k]) VT::store_rounded(grad, id[k], R.valid ? scale * __fsub_rn(ej[k], p[k]) : NAN);
-  if (tid == 0) {
-    term = 0.f;
-    for (int c = 0; c < kWarps; ++c) term += sh.term[c];
-    asm volatile("st.shared::cluster.f32 [%0], %1;" :: "r"(peer(&sh.kl[rank], 0)), "f"(term) : "memory");
+      for (int k = 0; k < kTrPerLane; ++k) w[k] = VT::neg_inf();
+      if (end >= 0) {
+        uint32_t in = 0;
+        for (int e = 0; e < N; ++e) {
+          const int t = end * N - shift + e;
+          if (t >= 0 && t < P.V) in |= static_cast<uint32_t>(tr_listed(sh.ids, t)) << e;
+        }
+        w[0] = with_neg_inf<ELT>(end_vec, in);
+      }
+      add(w);
+    }
+    bad |= zj != zj || zj == INFINITY;
+    float s, s_hi;
+    unpack2(add2(s2, s3), s, s_hi);
+    TlPart part{m, s + s_hi, zj, zj > -INFINITY ? 1.f : 0.f};
+    if (bad || dead) part.s = NAN;
+    part = tl_combine(part, P.c2, P.inv_T);
+    float mass = warp_sum(p);
+    if (lane == 0) sh.warp[par][warp] = part, sh.mass[par][warp] = mass;
+    named_barrier_sync(1, kTrConsumers);
+    if (place >= 0) sh.ids[place] = -1;
+
+    // ---- the row's numbers, the same in every warp
+    const TlPart none{-INFINITY, 0.f, -INFINITY, 0.f};
+    part = tl_combine(lane < kTrWarps ? sh.warp[par][lane] : none, P.c2, P.inv_T);
+    if (ctas > 1) {
+      if (warp == 0) {
+        if (lane == 0) mbar_expect_tx(&sh.joined[par], static_cast<uint32_t>(ctas) * 16u);
+        if (lane < ctas)
+          st_async(peer(&sh.part[par][rank], lane), make_uint4(__float_as_uint(part.m), __float_as_uint(part.s), 0u, 0u),
+                   peer(&sh.joined[par], lane));
+      }
+      const bool ok = !dead && mbar_wait_bounded(&sh.joined[par], static_cast<uint32_t>(phase), kDrainLimitNs);
+      dead = !__all_sync(0xffffffffu, ok);
+      TlPart other = none;
+      if (lane < ctas && !dead) {
+        const uint4 x = sh.part[par][lane];
+        other.m = __uint_as_float(x.x);
+        other.s = __uint_as_float(x.y);
+      }
+      other = tl_combine(other, P.c2, P.inv_T);
+      part.m = other.m;
+      part.s = dead ? NAN : other.s;
+    }
+    mass = warp_sum(lane < kTrWarps ? sh.mass[par][lane] : 0.f);
+    const float scale = weight * P.inv_T;
+    const TlRow R = tl_row(part, mass, scale, P);
+
+    // ---- the gradient
+    if (GRAD) {
+      const f2 bb = pack2(R.base, R.base), aa = pack2(R.a, R.a);
+      auto gradient = [&](const uint4& x) {
+        f2 z[N / 2];
+        float g[N];
+        VT::pairs(x, z);
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) unpack2(mul2(aa, exp2_2(mul2(sub2(z[i], bb), cc))), g[2 * i], g[2 * i + 1]);
+        return VT::pack(g);
+      };
+      unsigned char* out = grad + (static_cast<long long>(row.first) * N - shift) * ELT;
+      for (int v = 0; v < row.n; v += kTrSlotVecs) {
+        uint4 w[kTrPerLane];
+        take(w, row.n - v, false);
+        unsigned char* at = out + static_cast<long long>(v + tid) * 16;
+        if (P.same_shift && row.n - v >= kTrSlotVecs) {
+#pragma unroll
+          for (int k = 0; k < kTrPerLane; ++k) store_vec16(at + k * kTrConsumers * 16, gradient(w[k]));
+        } else {
+#pragma unroll
+          for (int k = 0; k < kTrPerLane; ++k)
+            if (v + tid + k * kTrConsumers < row.n)
+              store_edge<ELT>(grad, P.V, (row.first + v + tid + k * kTrConsumers) * N - shift, P.same_shift, gradient(w[k]));
+        }
+      }
+      if (end >= 0) store_edge<ELT>(grad, P.V, end * N - shift, P.same_shift, gradient(end_vec));
+    }
+
+    // ---- the listed tokens: their gradients after the row's, and the divergence
+    const float lj = __fmul_rn(__fsub_rn(zj, R.Ma), P.inv_T);
+    if (P.renorm) {
+      lp = R.mass > 0.f ? __fsub_rn(lp, logf(R.mass)) : -INFINITY;
+      p = R.mass > 0.f ? __fdiv_rn(p, R.mass) : 0.f;
+    }
+    float term = id >= 0 && p > 0.f ? __fmul_rn(p, __fsub_rn(lp, __fsub_rn(lj, R.LZ))) : 0.f;
+    term = warp_sum(term);
+    if (lane == 0) sh.term[par][warp] = term;
+    named_barrier_sync(1, kTrConsumers);
+    const bool valid = R.valid && !dead;
+    const int in_row = id + shift, v_id = in_row / N - row.first;   // the entry's vector, in this part or not
+    const bool at_end = rank == 0 && ((shift && in_row < N) || (in_row / N == nvec - 1 && (P.V + shift) % N));
+    if (GRAD && id >= 0 && ((v_id >= 0 && v_id < row.n) || at_end)) {
+      const float qj = zj > -INFINITY ? __fdiv_rn(expf(lj), R.Z) : 0.f;
+      VT::store_rounded(grad, id, valid ? scale * __fsub_rn(qj, p) : NAN);
+    }
+    if (tid == 0 && rank == 0) {
+      float kl = R.kl;
+      for (int w = 0; w < kTrWarps; ++w) kl += sh.term[par][w];
+      P.row_kl[r] = valid ? kl : NAN;
+    }
   }
-  if (ctas > 1) {
-    tl_arrive();
-    if (rank != 0) return;                 // the first CTA's memory is written, and waits
-    tl_wait();
-  }
-  if (tid == 0) {
-    float kl = R.kl;
-    for (int c = 0; c < ctas; ++c) kl += sh.kl[c];
-    P.row_kl[r] = R.valid ? kl : NAN;
-  }
+  if (ctas > 1) cluster_sync();   // nothing is on its way to a CTA that has left
 }
 
 // loss[b] = w_b * sum_t row_kl[b, t], in position order.
 __global__ void toploss_sum_kernel(int n_seq, int t_len, const float* row_kl, const float* weights, float* loss) {
   const int b = blockIdx.x * blockDim.x + threadIdx.x;
+  grid_dependency_wait();
   if (b >= n_seq) return;
   double s = 0.0;
   for (int t = 0; t < t_len; ++t) s += static_cast<double>(row_kl[static_cast<long long>(b) * t_len + t]);
   loss[b] = static_cast<float>(static_cast<double>(weights[b]) * s);
 }
 
-template <int ELT, int THREADS, int NV, int CTAS>
-cudaError_t launch_parts(const TopLossParams& p, int rows, int nvec, cudaStream_t s) {
-  const int cluster = (nvec + THREADS * NV - 1) / (THREADS * NV);
+template <int ELT>
+cudaError_t launch_toploss(const TopLossParams& p, int rows, cudaStream_t s) {
+  // Few rows: as many CTAs to a row as give the SMs work (a row of 128256 bf16
+  // logits: 16.6 us with one, 8.7 us with eight).  Many rows with a gradient:
+  // two where the rows at work would not stay in L2 for their second reading
+  // (more than two wait for one another longer than that saves: 888 us with
+  // four).
+  const long long row_bytes = static_cast<long long>(p.V) * ELT;
+  int cluster = 1;
+  while (cluster < kTlMaxCtas && rows * 2 * cluster <= kTrGrid && row_bytes / (2 * cluster) >= kTrMinPart) cluster *= 2;
+  if (cluster == 1 && p.grad && (rows < kTrGrid ? rows : kTrGrid) * row_bytes > kTrInL2) cluster = 2;
+  const void* fn = p.grad ? reinterpret_cast<const void*>(&toploss_kernel<ELT, true>)
+                          : reinterpret_cast<const void*>(&toploss_kernel<ELT, false>);
+  const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kTrSmem);
+  if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeClusterDimension;
   attr.val.clusterDim.x = cluster;
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(rows) * cluster);
-  cfg.blockDim = dim3(THREADS);
+  const int clusters = kTrGrid / cluster;
+  cfg.gridDim = dim3(static_cast<unsigned>((rows < clusters ? rows : clusters) * cluster));
+  cfg.blockDim = dim3(kTrThreads);
+  cfg.dynamicSmemBytes = kTrSmem;
   cfg.stream = s;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, toploss_kernel<ELT, THREADS, NV, CTAS>, p);
-}
-
-template <int ELT>
-cudaError_t launch_toploss(const TopLossParams& p, int rows, cudaStream_t s) {
-  // the vectors of a row that lies anyhow on its 16-byte boundaries
-  const int nvec = (p.V + 2 * Vec<ELT>::N - 2) / Vec<ELT>::N;
-  if (nvec <= 128 * 4) return launch_parts<ELT, 128, 4, 8>(p, rows, nvec, s);
-  if (nvec <= kTlMaxCtas * 128 * 20) return launch_parts<ELT, 128, 20, 4>(p, rows, nvec, s);
-  if (nvec <= kTlMaxCtas * 256 * 20) return launch_parts<ELT, 256, 20, 2>(p, rows, nvec, s);
-  return launch_parts<ELT, 256, 33, 1>(p, rows, nvec, s);
+  return p.grad ? cudaLaunchKernelEx(&cfg, toploss_kernel<ELT, true>, p, rows)
+                : cudaLaunchKernelEx(&cfg, toploss_kernel<ELT, false>, p, rows);
 }
 
 }  // namespace
@@ -404,6 +591,16 @@ extern "C" sv_status spec_kd_top_loss(int n_seq, int t_len, int V, sv_dtype dtyp
   const int rows = n_seq * t_len;
   const cudaError_t e = elt == 2 ? launch_toploss<2>(p, rows, s) : launch_toploss<4>(p, rows, s);
   if (e != cudaSuccess || cudaGetLastError() != cudaSuccess) return SV_ERR_CUDA;
-  toploss_sum_kernel<<<(n_seq + 127) / 128, 128, 0, s>>>(n_seq, t_len, row_kl, weights, loss);
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>((n_seq + 127) / 128));
+  cfg.blockDim = dim3(128);
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, toploss_sum_kernel, n_seq, t_len, static_cast<const float*>(row_kl), weights, loss) != cudaSuccess)
+    return SV_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? SV_OK : SV_ERR_CUDA;
 }
