@@ -89,7 +89,7 @@ __device__ __forceinline__ TlPart tl_combine(const TlPart& p, float c2, float in
 }
 
 // The row's numbers from its combined part: Ma = max(M, Ml), Z its whole sum.
-__device__ __forceinline__ TlRow tl_row(const TlPart& part, float mass, float scale, const TopLossParams& P) {
+__device__ __forceinline__ TlRow tl_row(const TlPart& part, double mass, float scale, const TopLossParams& P) {
   TlRow R;
   R.Ma = fmaxf(part.m, part.ml);
   R.valid = part.s == part.s && R.Ma > -INFINITY && R.Ma < INFINITY;
@@ -97,15 +97,21 @@ __device__ __forceinline__ TlRow tl_row(const TlPart& part, float mass, float sc
   const float lt = __fmul_rn(__fsub_rn(part.m, R.Ma), P.inv_T);
   const float ft = part.m > -INFINITY ? expf(lt) : 0.f;
   const float fl = part.ml > -INFINITY ? expf(__fmul_rn(__fsub_rn(part.ml, R.Ma), P.inv_T)) : 0.f;
-  R.Z = __fadd_rn(__fmul_rn(part.s, ft), __fmul_rn(part.sl, fl));
+  const float tail = __fmul_rn(part.s, ft);   // of Z
+  R.Z = __fadd_rn(tail, __fmul_rn(part.sl, fl));
   R.LZ = logf(R.Z);
-  R.mass = mass;
-  float rest = P.renorm ? 0.f : __fsub_rn(1.f, mass);
+  R.mass = static_cast<float>(mass);
+  float rest = P.renorm ? 0.f : static_cast<float>(1.0 - mass);
   if (rest < kTlComplete) rest = 0.f;
   R.a = R.valid ? scale * __fsub_rn(__fdiv_rn(ft, R.Z), part.s > 0.f ? __fdiv_rn(rest, part.s) : 0.f) : NAN;
   R.base = part.m > -INFINITY ? part.m : 0.f;
+  // r (log r - log(1 - Q)), the logarithm of one ratio where 1 - Q can be
+  // written: r and 1 - Q are alike, and their logarithms' roundings are not
   R.kl = 0.f;
-  if (rest > 0.f) R.kl = part.s > 0.f ? rest * (logf(rest) - __fsub_rn(__fadd_rn(lt, logf(part.s)), R.LZ)) : INFINITY;
+  if (rest > 0.f)
+    R.kl = tail > 1e-30f   ? rest * logf(__fdiv_rn(__fmul_rn(rest, R.Z), tail))
+           : part.s > 0.f ? rest * (logf(rest) - __fsub_rn(__fadd_rn(lt, logf(part.s)), R.LZ))
+                          : INFINITY;
   return R;
 }
 
@@ -162,7 +168,7 @@ struct TrShared {
   uint64_t joined[2];            // the cluster's parts of a row are here, by row parity as what follows
   uint4 part[2][kTlMaxCtas];     // the CTAs' (M, S)
   TlPart warp[2][kTrWarps];      // the warps' parts
-  float mass[2][kTrWarps];
+  double mass[2][kTrWarps];      // P in 64 bits: 1 - P keeps what the log-probabilities have
   float term[2][kTrWarps];
   int ids[kTrHash];              // open addressing; -1: empty
 };
@@ -434,7 +440,7 @@ __global__ void __launch_bounds__(kTrThreads, kTrCtas) toploss_kernel(const __gr
     TlPart part{m, s + s_hi, zj, zj > -INFINITY ? 1.f : 0.f};
     if (bad || dead) part.s = NAN;
     part = tl_combine(part, P.c2, P.inv_T);
-    float mass = warp_sum(p);
+    double mass = warp * 32 < P.K ? warp_sum(static_cast<double>(p)) : 0.0;
     if (lane == 0) sh.warp[par][warp] = part, sh.mass[par][warp] = mass;
     named_barrier_sync(1, kTrConsumers);
     if (place >= 0) sh.ids[place] = -1;
@@ -461,7 +467,9 @@ __global__ void __launch_bounds__(kTrThreads, kTrCtas) toploss_kernel(const __gr
       part.m = other.m;
       part.s = dead ? NAN : other.s;
     }
-    mass = warp_sum(lane < kTrWarps ? sh.mass[par][lane] : 0.f);
+    mass = sh.mass[par][lane % kTrWarps];
+#pragma unroll
+    for (int o = kTrWarps / 2; o > 0; o >>= 1) mass += __shfl_xor_sync(0xffffffffu, mass, o);
     const float scale = weight * P.inv_T;
     const TlRow R = tl_row(part, mass, scale, P);
 
