@@ -470,21 +470,33 @@ def kd_loss(target, draft, weights, temperature=1.0, grad=True, stream=None):
     return row_kl, loss, g
 
 
-def _dtype_code(t):
-    if t.dtype == torch.bfloat16:
-        return SV_BF16
-    if t.dtype == torch.float32:
-        return SV_F32
-    raise TypeError("logits must be float32 or bfloat16")
+_DTYPE_CODES = {torch.float32: SV_F32, torch.bfloat16: SV_BF16}
 
 
 def _logit_rows(name, t):
+    """(shape, device, dtype code) of a contiguous [., ., V] CUDA tensor."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dim() != 3:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected three dimensions")
-    _check_dev(name, t, t.dtype, t.shape, t.device)
-    return t.shape, t.device, _dtype_code(t)
+    code = _DTYPE_CODES.get(t.dtype)
+    if code is None:
+        raise TypeError("logits must be float32 or bfloat16")
+    shape = t.shape
+    if len(shape) != 3:
+        raise ValueError(f"{name} has shape {tuple(shape)}, expected three dimensions")
+    if not (t.is_cuda and t.is_contiguous()):
+        _check_dev(name, t, t.dtype, shape, t.device)
+    return shape, t.device, code
+
+
+def _address(name, t, dtype, shape, dev):
+    """The tensor's address (None for None) once it is what the call takes;
+    ``_check_dev`` says what is wrong otherwise."""
+    if t is None:
+        return None
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == dev.index
+            and t.is_contiguous()):
+        _check_dev(name, t, dtype, shape, dev)
+    return t.data_ptr()
 
 
 class _on_stream:
@@ -494,21 +506,33 @@ class _on_stream:
 
     def __init__(self, device, stream):
         self.device, self.stream = device, stream
-        self.ctx = None
 
     def __enter__(self):
         if self.stream is not None:
             self.ctx = torch.cuda.stream(self.stream)
-        elif self.device.index != torch.cuda.current_device():
+            self.handle = self.stream.cuda_stream
+        else:
             self.ctx = torch.cuda.device(self.device)
-        if self.ctx is not None:
-            self.ctx.__enter__()
-        self.handle = torch.cuda.current_stream().cuda_stream
-        return self
+            self.handle = torch.cuda.current_stream(self.device).cuda_stream
+        self.ctx.__enter__()
+        return self.handle
 
     def __exit__(self, *exc):
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
+        self.ctx.__exit__(*exc)
+
+
+# the current stream's handle without a Stream object (2 us on a Grace core)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _launch(dev, stream, call):
+    """call(stream handle) on the tensors' device.  The common case, the
+    current stream of the current device, goes without a context manager."""
+    if stream is None and torch.cuda.current_device() == dev.index:
+        return call(_raw_stream(dev.index))
+    with _on_stream(dev, stream) as handle:
+        return call(handle)
 
 
 def process_logits(logits, history=None, prompt_len=None, history_len=None, tokens=None, draft_len=None,
@@ -532,6 +556,7 @@ def process_logits(logits, history=None, prompt_len=None, history_len=None, toke
     (B, R, V), dev, code = _logit_rows("logits", logits)
     i32, f32 = torch.int32, torch.float32
     H = stride = k = M = 0
+    history_at = None
     if history is not None:
         if not isinstance(history, torch.Tensor):
             raise TypeError("history must be a torch.Tensor")
@@ -545,39 +570,36 @@ def process_logits(logits, history=None, prompt_len=None, history_len=None, toke
         stride = history.stride(0) if B > 1 else H
         if H > 1 and history.stride(1) != 1 or stride < H:
             raise ValueError("history must have contiguous rows that do not overlap")
+        history_at = history.data_ptr()
     elif prompt_len is not None or history_len is not None:
         raise ValueError("prompt_len and history_len describe a history")
-    _check_dev("prompt_len", prompt_len, i32, (B,), dev)
-    _check_dev("history_len", history_len, i32, (B,), dev)
     if tokens is not None:
         k = tokens.shape[1] if isinstance(tokens, torch.Tensor) and tokens.dim() == 2 else R - 1
-        _check_dev("tokens", tokens, i32, (B, k), dev)
-        if R not in (k, k + 1):
+        if R != k and R != k + 1:
             raise ValueError(f"{R} rows for {k} drafts: expected {k} or {k + 1}")
     elif draft_len is not None:
         k = R - 1
-    _check_dev("draft_len", draft_len, i32, (B,), dev)
-    _check_dev("repetition", repetition, f32, (B,), dev)
-    _check_dev("presence", presence, f32, (B,), dev)
-    _check_dev("frequency", frequency, f32, (B,), dev)
     if (bias_ids is None) != (bias_values is None):
         raise ValueError("bias_ids and bias_values go together")
     if bias_ids is not None:
         M = bias_ids.shape[1] if isinstance(bias_ids, torch.Tensor) and bias_ids.dim() == 2 else 0
-        _check_dev("bias_ids", bias_ids, i32, (B, M), dev)
-        _check_dev("bias_values", bias_values, f32, (B, M), dev)
-    _check_dev("mask", mask, i32, (B, R, (V + 31) // 32), dev)
-    _check_dev("out", out, logits.dtype, (B, R, V), dev)
-    with _on_stream(dev, stream) as on:
-        if out is None:
-            out = torch.empty_like(logits)
-        st = lib.sv_process_logits(B, R, V, code, _ptr(logits), _ptr(out), H, stride, _ptr(history),
-                                   _ptr(prompt_len), _ptr(history_len), k, _ptr(tokens), _ptr(draft_len),
-                                   _ptr(repetition), _ptr(presence), _ptr(frequency), M, _ptr(bias_ids),
-                                   _ptr(bias_values), _ptr(mask), on.handle)
-    if st != SV_OK:
-        raise SpecVerifyError(st, "sv_process_logits")
-    return out
+    per = (B,)
+    args = [H, stride, history_at, _address("prompt_len", prompt_len, i32, per, dev),
+            _address("history_len", history_len, i32, per, dev), k, _address("tokens", tokens, i32, (B, k), dev),
+            _address("draft_len", draft_len, i32, per, dev), _address("repetition", repetition, f32, per, dev),
+            _address("presence", presence, f32, per, dev), _address("frequency", frequency, f32, per, dev), M,
+            _address("bias_ids", bias_ids, i32, (B, M), dev), _address("bias_values", bias_values, f32, (B, M), dev),
+            _address("mask", mask, i32, (B, R, (V + 31) // 32), dev)]
+    _address("out", out, logits.dtype, (B, R, V), dev)
+
+    def call(handle):
+        res = torch.empty_like(logits) if out is None else out
+        st = lib.sv_process_logits(B, R, V, code, logits.data_ptr(), res.data_ptr(), *args, handle)
+        if st != SV_OK:
+            raise SpecVerifyError(st, "sv_process_logits")
+        return res
+
+    return _launch(dev, stream, call)
 
 
 def kd_top(target, k, temperature=1.0, n_rows=None, stream=None):
@@ -592,16 +614,19 @@ def kd_top(target, k, temperature=1.0, n_rows=None, stream=None):
     k = int(k)
     if not 1 <= k <= SV_KD_TOP_MAX:
         raise ValueError(f"k is {k}, expected 1..{SV_KD_TOP_MAX}")
-    _check_dev("n_rows", n_rows, torch.int32, (n_seq,), dev)
-    with _on_stream(dev, stream) as on:
+    rows_at = _address("n_rows", n_rows, torch.int32, (n_seq,), dev)
+
+    def call(handle):
         ids = torch.empty((n_seq, t_len, k), dtype=torch.int32, device=dev)
         logp = torch.empty((n_seq, t_len, k), dtype=torch.float32, device=dev)
         lse = torch.empty((n_seq, t_len), dtype=torch.float32, device=dev)
-        st = lib.spec_kd_top(n_seq, t_len, V, code, _ptr(target), _ptr(n_rows), k, float(temperature), _ptr(ids),
-                             _ptr(logp), _ptr(lse), on.handle)
-    if st != SV_OK:
-        raise SpecVerifyError(st, "spec_kd_top")
-    return ids, logp, lse
+        st = lib.spec_kd_top(n_seq, t_len, V, code, target.data_ptr(), rows_at, k, temperature, ids.data_ptr(),
+                             logp.data_ptr(), lse.data_ptr(), handle)
+        if st != SV_OK:
+            raise SpecVerifyError(st, "spec_kd_top")
+        return ids, logp, lse
+
+    return _launch(dev, stream, call)
 
 
 def kd_top_loss(ids, logp, draft, weights, temperature=1.0, tail=True, grad=True, stream=None):
@@ -615,19 +640,22 @@ def kd_top_loss(ids, logp, draft, weights, temperature=1.0, tail=True, grad=True
     lib = load_library()
     (n_seq, t_len, V), dev, code = _logit_rows("draft", draft)
     K = ids.shape[2] if isinstance(ids, torch.Tensor) and ids.dim() == 3 else 0
-    _check_dev("ids", ids, torch.int32, (n_seq, t_len, K), dev)
-    _check_dev("logp", logp, torch.float32, (n_seq, t_len, K), dev)
-    _check_dev("weights", weights, torch.float32, (n_seq,), dev)
-    with _on_stream(dev, stream) as on:
+    ids_at = _address("ids", ids, torch.int32, (n_seq, t_len, K), dev)
+    logp_at = _address("logp", logp, torch.float32, (n_seq, t_len, K), dev)
+    weights_at = _address("weights", weights, torch.float32, (n_seq,), dev)
+    mode = SV_KD_TOP_TAIL if tail else SV_KD_TOP_RENORM
+
+    def call(handle):
         row_kl = torch.empty((n_seq, t_len), dtype=torch.float32, device=dev)
         loss = torch.empty((n_seq,), dtype=torch.float32, device=dev)
         g = torch.empty_like(draft) if grad else None
-        st = lib.spec_kd_top_loss(n_seq, t_len, V, code, K, _ptr(ids), _ptr(logp), _ptr(draft), _ptr(weights),
-                                  float(temperature), SV_KD_TOP_TAIL if tail else SV_KD_TOP_RENORM, _ptr(row_kl),
-                                  _ptr(loss), _ptr(g), on.handle)
-    if st != SV_OK:
-        raise SpecVerifyError(st, "spec_kd_top_loss")
-    return row_kl, loss, g
+        st = lib.spec_kd_top_loss(n_seq, t_len, V, code, K, ids_at, logp_at, draft.data_ptr(), weights_at, temperature,
+                                  mode, row_kl.data_ptr(), loss.data_ptr(), g.data_ptr() if grad else None, handle)
+        if st != SV_OK:
+            raise SpecVerifyError(st, "spec_kd_top_loss")
+        return row_kl, loss, g
+
+    return _launch(dev, stream, call)
 
 
 def measure_ex2(iters=4096):

@@ -42,6 +42,7 @@ namespace {
 
 constexpr int kLgThreads = 256;
 constexpr int kLgCtas = 4;                // resident per SM
+constexpr int kLgEnough = 1000;           // CTAs that larger slices have to leave
 constexpr int kLgMaxDrafts = 32;
 // A table word: in the prompt, among the drafts, the last bias's entry + 1
 // and the times generated in the history.
@@ -132,20 +133,24 @@ struct RowPart {
     return P.same_shift && t0 >= 0 && t0 <= P.V - N;
   }
 
+  // The mask's bits for the pass; its vectors are loaded by them later.
+  __device__ __forceinline__ void load_mask(const LogitsParams& P, long long r, int s0) {
+    if (!MASK) return;
+    const int s = s0 - row_shift<ELT>(P.logits + r * P.V * ELT);
+    const int* mask = P.mask + r * ((P.V + 31) / 32);
+    const bool all = inside(P, s);
+#pragma unroll
+    for (int q = 0; q < U; ++q) allowed[q] = all || whole(P, token(q, s)) ? bits_at<N>(mask, token(q, s)) : 0u;
+  }
   __device__ __forceinline__ void load(const LogitsParams& P, long long r, int s0, bool in_place) {
     const unsigned char* in = P.logits + r * P.V * ELT;
     const int s = s0 - row_shift<ELT>(in);
     const unsigned char* at = in + static_cast<long long>(token(0, s)) * ELT;
-    const bool all = inside(P, s);
     if (MASK) {
-      const int* mask = P.mask + r * ((P.V + 31) / 32);
-#pragma unroll
-      for (int q = 0; q < U; ++q)
-        allowed[q] = all || whole(P, token(q, s)) ? bits_at<N>(mask, token(q, s)) : 0u;
 #pragma unroll
       for (int q = 0; q < U; ++q)
         if (allowed[q] && !(in_place && allowed[q] == kAll)) w[q] = load_vec16(at + q * kLgThreads * 16);
-    } else if (all) {
+    } else if (inside(P, s)) {
 #pragma unroll
       for (int q = 0; q < U; ++q) w[q] = load_vec16(at + q * kLgThreads * 16);
     } else {
@@ -257,7 +262,10 @@ __global__ void __launch_bounds__(kLgThreads, kLgCtas) logits_kernel(const __gri
     load_history(h, 0, P.history_max, P.history_vec, t);
   }
   RowPart<ELT, U, MASK> part;
-  if (copies) part.load(P, r0, s0, in_place);
+  if (copies) {
+    part.load_mask(P, r0, s0);
+    part.load(P, r0, s0, in_place);
+  }
 
   // ---- the table of the slice's tokens
   int n_fixes = 0;
@@ -349,34 +357,66 @@ __global__ void __launch_bounds__(kLgThreads, kLgCtas) logits_kernel(const __gri
     }
   }
 
-  // ---- the mask and the copy, a pass ahead
-  for (int i = 0, q = 0; copies && i < rows;) {
-    const int at = i, of = q;
-    if (++q == P.parts) q = 0, ++i;
+  // ---- the mask and the copy: a pass's logits are loaded a pass ahead, its
+  // mask two
+  if (copies) {
+    const int passes = rows * P.parts;
+    int i = 0, q = 0;                // the pass two ahead of the one stored
+    auto next = [&] {
+      if (++q == P.parts) q = 0, ++i;
+    };
+    next();
+    int at_row = 0, at_s = s0;
     RowPart<ELT, U, MASK> ahead;
-    if (i < rows) ahead.load(P, r0 + i, s0 + q * kPart, in_place);
-    part.store(P, r0 + at, s0 + of * kPart, in_place);
-    part = ahead;
+    if (passes > 1) ahead.load_mask(P, r0 + i, s0 + q * kPart);
+    for (int pass = 0; pass < passes; ++pass) {
+      const int row_ahead = i, s_ahead = s0 + q * kPart;
+      if (pass + 1 < passes) ahead.load(P, r0 + row_ahead, s_ahead, in_place);
+      next();
+      RowPart<ELT, U, MASK> after;
+      if (MASK && pass + 2 < passes) after.load_mask(P, r0 + i, s0 + q * kPart);
+      part.store(P, r0 + at_row, at_s, in_place);
+      part = ahead;
+      if (MASK) {
+#pragma unroll
+        for (int k = 0; k < U; ++k) ahead.allowed[MASK ? k : 0] = after.allowed[MASK ? k : 0];
+      }
+      at_row = row_ahead;
+      at_s = s_ahead;
+    }
   }
   if (n_fixes == 0) return;
 
   // ---- the tokens of the table, their stores after the copy's: a thread for
   // each token of each row
   __syncthreads();
-  for (int j = tid; j < n_fixes; j += kLgThreads) {
+  auto correct = [&](const LogitsFix& f, int j) {
     const int i = j % rows, u = list[j / rows];
-    if (j != tid) fix.load<ELT>(P, r0 + i, s0, n_slice, tab[u], u, b);
-    if (!fix.mine) continue;
-    int n = static_cast<int>(fix.word & kLgCount);
-    if (fix.word & kLgDraft)
+    if (!f.mine) return;
+    int n = static_cast<int>(f.word & kLgCount);
+    if (f.word & kLgDraft)
       for (int d = 0; d < min(i, n_drafts); ++d) n += drafts[d] == first + u;
-    const bool seen = n > 0 || (fix.word & kLgPrompt);
-    if (!seen && !(fix.word & kLgBias)) continue;   // drafted only later
-    float z = fix.z;
+    const bool seen = n > 0 || (f.word & kLgPrompt);
+    if (!seen && !(f.word & kLgBias)) return;   // drafted only later
+    float z = f.z;
     if (seen) z = z > 0.f ? __fdiv_rn(z, numbers[0]) : __fmul_rn(z, numbers[0]);
     if (n > 0) z = __fsub_rn(__fsub_rn(z, __fmul_rn(numbers[2], static_cast<float>(n))), numbers[1]);
-    if (fix.word & kLgBias) z = __fadd_rn(z, fix.bias);
+    if (f.word & kLgBias) z = __fadd_rn(z, f.bias);
     VT::store_rounded(P.out + ((r0 + i) * P.V + first + u) * ELT, 0, z);
+  };
+  if (tid < n_fixes) correct(fix, tid);
+  // more than a thread each: four at a time, so that their loads overlap
+  constexpr int kMore = 4;
+  for (int j0 = kLgThreads + tid; j0 < n_fixes; j0 += kLgThreads * kMore) {
+    LogitsFix more[kMore];
+#pragma unroll
+    for (int q = 0; q < kMore; ++q) {
+      const int j = min(j0 + q * kLgThreads, n_fixes - 1), u = list[j / rows];
+      more[q].load<ELT>(P, r0 + j % rows, s0, n_slice, tab[u], u, b);
+    }
+#pragma unroll
+    for (int q = 0; q < kMore; ++q)
+      if (j0 + q * kLgThreads < n_fixes) correct(more[q], j0 + q * kLgThreads);
   }
 }
 
@@ -435,9 +475,9 @@ extern "C" sv_status sv_process_logits(int B, int R, int V, sv_dtype dtype, cons
   const int n = elt == 2 ? 8 : 4;
   int unroll = 1;
   auto slices = [&](int u) { return (V + n - 1 + kLgThreads * u * n - 1) / (kLgThreads * u * n); };
-  while (unroll < 4 && static_cast<long long>(B) * slices(2 * unroll) >= 1216) unroll *= 2;
+  while (unroll < 4 && static_cast<long long>(B) * slices(2 * unroll) >= kLgEnough) unroll *= 2;
   // fp32 slices of as many tokens as bf16's: the history is read once a slice
-  p.parts = elt == 4 && unroll == 4 && p.history && static_cast<long long>(B) * slices(8) >= 608 ? 2 : 1;
+  p.parts = elt == 4 && unroll == 4 && p.history && static_cast<long long>(B) * slices(8) >= kLgEnough ? 2 : 1;
   const long long ctas = static_cast<long long>(B) * slices(unroll * p.parts);
   if (ctas > 0x7fffffffLL) return SV_ERR_INVALID_ARG;
   const int n_tokens = kLgThreads * unroll * n * p.parts;

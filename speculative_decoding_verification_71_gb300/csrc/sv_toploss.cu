@@ -34,6 +34,7 @@
 
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 
@@ -551,8 +552,17 @@ cudaError_t launch_toploss(const TopLossParams& p, int rows, cudaStream_t s) {
   if (cluster == 1 && p.grad && (rows < kTrGrid ? rows : kTrGrid) * row_bytes > kTrInL2) cluster = 2;
   const void* fn = p.grad ? reinterpret_cast<const void*>(&toploss_kernel<ELT, true>)
                           : reinterpret_cast<const void*>(&toploss_kernel<ELT, false>);
-  const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kTrSmem);
+  // the shared-memory limit, raised once per instance and device
+  static std::atomic<unsigned long long> raised[2];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  const unsigned long long bit = 1ULL << (dev & 63);
+  if (dev >= 64 || !(raised[p.grad != nullptr].load(std::memory_order_relaxed) & bit)) {
+    e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kTrSmem);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) raised[p.grad != nullptr].fetch_or(bit, std::memory_order_relaxed);
+  }
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeClusterDimension;
   attr.val.clusterDim.x = cluster;
