@@ -19,14 +19,18 @@
 //     read; in place, only what the mask forbids is touched); its first loads
 //     are under way while the history is counted;
 //   - the tokens of the bitmap, a thread for each token of each row.
-// Looking the table up while streaming cost more than the stream: nearly
-// every warp holds some repeated token, and ran the rule for one or two of
-// its lanes (193 us against 106 on 256 sequences of up to four rows of
-// 128256 bf16 logits, histories of up to 4096 tokens).  The counting is
-// without a result that a thread would wait for and without a branch per
-// token: listing the tokens while counting them, or sharing the history among
-// a cluster's CTAs with additions into each other's tables (3.6 cycles an
-// addition and SM), took 105 and 110 us against @@.
+// On 256 sequences of up to four rows of 128256 bf16 logits with histories of
+// up to 4096 tokens: 74 us (4.5 TB/s of what has to be read and written), the
+// copy alone 53 us.  Bound by the chain of short phases that each CTA goes
+// through besides its copy (count, list, correct: 4 us for the counting, 16 us
+// for the corrections, though they move little).  Measured the other way:
+// looking the table up while streaming 193 us (nearly every warp holds some
+// repeated token and runs the rule for one or two of its lanes); listing the
+// tokens while counting them 105 us; one history for a cluster's CTAs, with
+// additions into each other's tables, 110 us (3.6 cycles an addition and SM);
+// persistent CTAs 149 us (rows differ too much); slices of interleaved blocks,
+// which share out a vocabulary's frequent first tokens evenly, 80 to 95 us
+// (more instructions for each token counted).
 
 #include <cuda_runtime.h>
 
@@ -42,7 +46,7 @@ namespace {
 
 constexpr int kLgThreads = 256;
 constexpr int kLgCtas = 4;                // resident per SM
-constexpr int kLgEnough = 1000;           // CTAs that larger slices have to leave
+constexpr int kLgEnough = 1216;           // CTAs that larger slices have to leave
 constexpr int kLgMaxDrafts = 32;
 // A table word: in the prompt, among the drafts, the last bias's entry + 1
 // and the times generated in the history.
