@@ -21,14 +21,14 @@
 // their parts of t without a barrier but one, after the first tile (an older
 // part is smaller and lets more through).  A thread whose four vectors of a
 // tile hold a value of at least t notes them, with one ballot and one addition
-// a warp (their values in shared memory while there is room; the others are
-// read again, from L2); once t is final, their tokens at or above t are kept.
+// a warp, and their largest value; once t is final, those that still pass are
+// read again, from L2, and their tokens at or above t kept.
 // On 1024 ragged rows of 128256 bf16 logits, K = 64: 50 us; appending token by
 // token while streaming 116 us.
 //
 // The CTAs hand their tokens at or above t, and their M and S, to the
-// cluster's first one and leave; it ranks them by counting the larger ones of
-// each.  Notes or tokens that outgrow their buffer (rows of few distinct
+// cluster's first one and leave; it sorts them, after a selection by
+// histogram where they are many.  Notes or tokens that outgrow their buffer (rows of few distinct
 // values, or masked with a finite value) are dropped, and the first CTA
 // selects from the row itself.
 
@@ -50,12 +50,9 @@ constexpr int kTopWarps = kTopThreads / 32;
 constexpr int kTopMaxK = SV_KD_TOP_MAX;
 constexpr int kTopUnroll = 4;             // 16-byte vectors of a tile per thread
 constexpr int kTopTile = kTopThreads * kTopUnroll;
-constexpr int kTopPlaces = 2048;          // (thread, tile) places a CTA can note: more than a part
-                                          // that leaves threads idle has
-constexpr int kTopHeld = 256;             // ... with their values
-constexpr int kTopCap = 1792;             // tokens to rank or to select from
+constexpr int kTopLeft = 768;             // noted places that hold a token at or above the final t
 constexpr int kTopEdge = 128;             // entries that share the last one's bin, told apart by counting
-constexpr int kTopCount = 256;            // tokens ranked by counting; of more the K are selected first
+constexpr int kTopCount = 256;            // tokens sorted; of more the K are selected first
 
 struct TopParams {
   const unsigned char* rows;   // [n_seq, t_len, V]
@@ -68,6 +65,10 @@ struct TopParams {
   float T;
   int quota;                   // ceil(K / warps)
   int push;                    // tokens that a CTA hands on at most (>= K)
+  // sizes of a CTA's buffers
+  int places;                  // (thread, tile) places noted: more than a part that leaves threads idle has
+  int held;                    // ... with their values
+  int cap;                     // tokens to sort or to select from
 };
 
 typedef unsigned long long key64;   // key and id: larger for a larger value, then a lower id
@@ -92,8 +93,9 @@ struct TopShared {
   volatile int wt[kTopWarps];           // the warps' parts of t, as ordered keys
   unsigned int hist[256];
   unsigned int warp_n[kTopWarps];
-  unsigned int n_places;                // places noted (may pass kTopPlaces)
-  unsigned int n_tokens;                // tokens to select from (may pass kTopCap)
+  unsigned int n_places;                // places noted (may pass `places`)
+  unsigned int n_left;                  // ... that hold a token at or above the final t (may pass kTopLeft)
+  unsigned int n_tokens;                // tokens to select from (may pass `cap`)
   unsigned int n_list;
   unsigned int base;                    // where this CTA's tokens go in the first one's
   unsigned int lost;                    // (first CTA) some CTA's tokens outgrew its buffers
@@ -102,10 +104,14 @@ struct TopShared {
   unsigned int n_edge;
   key64 edge[kTopEdge];
   key64 list[kTopMaxK];
-  int places[kTopPlaces];               // a thread's first vector of a tile
-  uint4 held[kTopUnroll][kTopHeld];
-  key64 tokens[kTopCap];
+  int lefts[kTopLeft];                  // the places that hold a token at or above the final t
 };
+// and, as large as the call needs them:
+//   key64 tokens[cap]
+//   uint4 held[kTopUnroll][held]
+//   int places[places]      a thread's first vector of a tile; ~ of a row's end
+//   float tops[places]      ... and the largest value of its vectors
+constexpr int kTopBuffersAt = (static_cast<int>(sizeof(TopShared)) + 15) / 16 * 16;
 
 // All threads of the cluster: arrive (what they wrote before is visible to
 // those that wait after), and wait.
@@ -186,7 +192,7 @@ __device__ __forceinline__ void find_bin(TopShared& sh, int left) {
   }
 }
 
-// The n_list largest of n distinct entries (n_list <= n <= kTopCap), all of
+// The n_list largest of n distinct entries (n_list <= n <= cap), all of
 // keys from `least` on, into sh.list in any order.  One histogram of 256 bins
 // spread over the keys' own range; then what falls into the bin of the
 // n_list-th largest is told apart by counting.  Where that bin is too full to
@@ -355,7 +361,10 @@ __global__ void __launch_bounds__(kTopThreads, 4) top_kernel(const __grid_consta
   constexpr int N = VT::N;
   extern __shared__ __align__(16) unsigned char smem[];
   TopShared& sh = *reinterpret_cast<TopShared*>(smem);
-  key64* tokens = sh.tokens;
+  key64* tokens = reinterpret_cast<key64*>(smem + kTopBuffersAt);
+  uint4* held = reinterpret_cast<uint4*>(tokens + P.cap);
+  int* places = reinterpret_cast<int*>(held + kTopUnroll * P.held);
+  float* tops = reinterpret_cast<float*>(places + P.places);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int ctas = cluster_ctas(), rank = cluster_rank();
   const long long r = blockIdx.x / ctas;
@@ -372,7 +381,7 @@ __global__ void __launch_bounds__(kTopThreads, 4) top_kernel(const __grid_consta
   const int shift = row_shift<ELT>(row), nvec = row_vecs<ELT>(P.V, shift);
   const int part = (nvec + ctas - 1) / ctas;
   int v0 = min(nvec, rank * part), v1 = min(nvec, v0 + part);
-  if (tid == 0) sh.n_places = sh.n_tokens = sh.n_list = sh.lost = 0;
+  if (tid == 0) sh.n_places = sh.n_left = sh.n_tokens = sh.n_list = sh.lost = 0;
   if (tid < kTopWarps) sh.wt[tid] = ordered_key(-FLT_MAX);
   __syncthreads();
   if (ctas > 1) cluster_arrive();      // the counters are set
@@ -409,22 +418,22 @@ __global__ void __launch_bounds__(kTopThreads, 4) top_kernel(const __grid_consta
     t = from_ordered_key(__reduce_min_sync(0xffffffffu, sh.wt[lane & (kTopWarps - 1)]));
     const unsigned who = __ballot_sync(0xffffffffu, vm >= t);
     if (who) {
-      unsigned note = 0;
-      if (lane == 0) note = atomicAdd(&sh.n_places, __popc(who));
+      int note = 0;
+      if (lane == 0) note = static_cast<int>(atomicAdd(&sh.n_places, __popc(who)));
       note = __shfl_sync(0xffffffffu, note, 0) + __popc(who & below);
-      if (vm >= t) {
-        if (note < kTopPlaces) sh.places[note] = at;
-        if (note < kTopHeld) {
+      if (vm >= t && note < P.places) {
+        places[note] = at;
+        tops[note] = vm;
+        if (note < P.held) {
 #pragma unroll
-          for (int q = 0; q < kTopUnroll; ++q) sh.held[q][note] = w[q];
+          for (int q = 0; q < kTopUnroll; ++q) held[q * P.held + note] = w[q];
         }
       }
     }
   };
 
   // ---- a first tile of the row's ends where they are not whole vectors (two
-  // threads, in the CTAs that have them, padded with -inf; nothing is known of
-  // t then, so they are noted whatever they hold, and first), then full tiles,
+  // threads, in the CTAs that have them, padded with -inf), then full tiles,
   // the next one's loads ahead, then the rest
   const bool head = shift != 0 && v0 == 0, tail = v1 == nvec && (P.V + shift) % N != 0 && v1 > v0;
   const int ends = head || tail;
@@ -433,8 +442,8 @@ __global__ void __launch_bounds__(kTopThreads, 4) top_kernel(const __grid_consta
   if (ends) {
 #pragma unroll
     for (int q = 0; q < kTopUnroll; ++q) a[q] = VT::neg_inf();
-    if (tid == 0 && head) a[0] = load_row_vec<ELT>(row, P.V, shift, place = 0);
-    if (tid == 1 && tail && nvec > head) a[0] = load_row_vec<ELT>(row, P.V, shift, place = nvec - 1);
+    if (tid == 0 && head) a[0] = load_row_vec<ELT>(row, P.V, shift, 0), place = ~0;
+    if (tid == 1 && tail && nvec > head) a[0] = load_row_vec<ELT>(row, P.V, shift, nvec - 1), place = ~(nvec - 1);
     v0 += head;
     v1 -= tail;
   }
@@ -500,24 +509,36 @@ __global__ void __launch_bounds__(kTopThreads, 4) top_kernel(const __grid_consta
       first_store(&sh.t[rank], t);
     }
   }
-  // ---- the noted vectors' tokens at or above t
-  const bool whole = sh.n_places <= kTopPlaces;
-  const int n_places = static_cast<int>(whole ? sh.n_places : 0u);
-  for (int i0 = warp * 32; i0 < n_places; i0 += kTopThreads) {
-    const int i = i0 + lane;
-    if (i >= n_places) break;
-    const int first = sh.places[i];
+  // ---- the noted vectors' tokens at or above t: the places that still hold
+  // one, and those again
+  bool whole = static_cast<int>(sh.n_places) <= P.places;
+  int n_left = static_cast<int>(whole ? sh.n_places : 0u);
+  const bool few = n_left <= kTopThreads;   // one to a thread
+  if (!few) {
+    for (int i = tid; i < n_left; i += kTopThreads)
+      if (tops[i] >= t) {
+        const unsigned k = atomicAdd(&sh.n_left, 1u);
+        if (k < kTopLeft) sh.lefts[k] = i;
+      }
+    __syncthreads();
+    whole = sh.n_left <= kTopLeft;
+    n_left = static_cast<int>(whole ? sh.n_left : 0u);
+  }
+  for (int j = tid; j < n_left; j += kTopThreads) {
+    const int i = few ? j : sh.lefts[j];
+    if (few && tops[i] < t) continue;
+    const int noted = places[i], first = noted < 0 ? ~noted : noted;
     uint4 w[kTopUnroll];
-    if (i < kTopHeld) {
+    if (i < P.held) {
 #pragma unroll
-      for (int q = 0; q < kTopUnroll; ++q) w[q] = sh.held[q][i];
+      for (int q = 0; q < kTopUnroll; ++q) w[q] = held[q * P.held + i];
     } else {
-      // (never a row's end: those are noted first)
 #pragma unroll
       for (int q = 0; q < kTopUnroll; ++q) {
         const int v = first + q * kTopThreads;
-        w[q] = v < v1 ? load_vec16(row + (static_cast<long long>(v) * N - shift) * ELT) : VT::neg_inf();
+        w[q] = noted >= 0 && v < v1 ? load_vec16(row + (static_cast<long long>(v) * N - shift) * ELT) : VT::neg_inf();
       }
+      if (noted < 0) w[0] = load_row_vec<ELT>(row, P.V, shift, first);
     }
     unsigned in = 0;                     // the vectors with a token at or above t
 #pragma unroll
@@ -535,7 +556,7 @@ __global__ void __launch_bounds__(kTopThreads, 4) top_kernel(const __grid_consta
       for (int e = 0; e < N; ++e)
         if (z[e] >= t) {
           const unsigned at = atomicAdd(&sh.n_tokens, 1u);
-          if (at < kTopCap) tokens[at] = top_entry(top_key(z[e]), static_cast<uint32_t>(t0 + e));
+          if (at < static_cast<unsigned>(P.cap)) tokens[at] = top_entry(top_key(z[e]), static_cast<uint32_t>(t0 + e));
         }
     }
   }
@@ -544,13 +565,13 @@ __global__ void __launch_bounds__(kTopThreads, 4) top_kernel(const __grid_consta
     // at most P.push: where there are more, the K largest
     unsigned n = sh.n_tokens;
     const key64* from = tokens;
-    if (n > P.push && n <= kTopCap) {
+    if (n > static_cast<unsigned>(P.push) && n <= static_cast<unsigned>(P.cap)) {
       select_entries(sh, tokens, static_cast<int>(n), P.K, top_key(t), 0xffffffffu);
       from = sh.list;
       n = P.K;
     }
     if (tid == 0) {
-      const bool lost = !whole || n > kTopCap;
+      const bool lost = !whole || n > static_cast<unsigned>(P.cap);
       if (lost) first_add(&sh.lost, 1u);
       sh.base = first_add(&sh.n_tokens, lost ? 0u : n);
       if (lost) sh.n_tokens = 0;
@@ -558,7 +579,7 @@ __global__ void __launch_bounds__(kTopThreads, 4) top_kernel(const __grid_consta
     __syncthreads();
     if (sh.n_tokens)
       for (unsigned i = tid; i < n; i += kTopThreads)
-        if (sh.base + i < kTopCap) first_store(&tokens[sh.base + i], from[i]);
+        if (sh.base + i < static_cast<unsigned>(P.cap)) first_store(&tokens[sh.base + i], from[i]);
     cluster_arrive();                  // and leave
     return;
   }
@@ -582,7 +603,7 @@ __global__ void __launch_bounds__(kTopThreads, 4) top_kernel(const __grid_consta
   int listed = 0, n_ranked = 0;        // entries of the list, and those that are ranked for it
   const key64* from = tokens;
   if (valid) {
-    const bool fits = !sh.lost && sh.n_tokens <= kTopCap;
+    const bool fits = !sh.lost && sh.n_tokens <= static_cast<unsigned>(P.cap);
     n_ranked = static_cast<int>(sh.n_tokens);
     listed = fits ? min(P.K, n_ranked) : P.K;
     if (!fits || n_ranked > kTopCount) {
@@ -593,23 +614,41 @@ __global__ void __launch_bounds__(kTopThreads, 4) top_kernel(const __grid_consta
       n_ranked = listed;
     }
   }
-  // ---- in order: each entry's place is the number of larger ones, counted by
-  // one thread or by two or four neighbours
-  const int lg = n_ranked <= kTopThreads / 4 ? 2 : n_ranked <= kTopThreads / 2 ? 1 : 0;
-  for (int i0 = 0; i0 < n_ranked; i0 += kTopThreads >> lg) {
-    const int j = i0 + (tid >> lg);
-    if (i0 + (warp * 32 >> lg) >= n_ranked) break;   // the whole warp
-    const key64 mine = from[min(j, n_ranked - 1)];
-    int place = 0;
-#pragma unroll 4
-    for (int i = tid & ((1 << lg) - 1); i < n_ranked; i += 1 << lg) place += from[i] > mine;
-    if (lg >= 1) place += __shfl_xor_sync(0xffffffffu, place, 1);
-    if (lg >= 2) place += __shfl_xor_sync(0xffffffffu, place, 2);
-    if (j < n_ranked && place < listed && (tid & ((1 << lg) - 1)) == 0) {
-      const float z = key_value(static_cast<uint32_t>(mine >> 32));
-      ids[place] = static_cast<int>(~static_cast<uint32_t>(mine));
-      logp[place] = __fsub_rn(__fdiv_rn(__fsub_rn(z, M), P.T), L);
-    }
+  // ---- in order: of a few, four neighbours count the larger ones of an entry;
+  // of more a bitonic sort of the least power of two that holds them, an entry
+  // a thread, in registers across a warp's lanes
+  static_assert(kTopThreads >= kTopCount && kTopThreads >= kTopMaxK, "an entry a thread");
+  key64 mine;
+  int to = tid;
+  if (n_ranked <= kTopThreads / 4) {
+    mine = from[min(tid >> 2, max(n_ranked, 1) - 1)];
+    to = 0;
+    for (int i = tid & 3; i < n_ranked; i += 4) to += from[i] > mine;
+    to += __shfl_xor_sync(0xffffffffu, to, 1);
+    to += __shfl_xor_sync(0xffffffffu, to, 2);
+    if ((tid & 3) || (tid >> 2) >= n_ranked) to = kTopMaxK;
+  } else {
+    mine = tid < n_ranked ? from[tid] : 0;   // (0 is less than any)
+    __syncthreads();
+    for (int size = 2; size < 2 * n_ranked; size <<= 1)
+      for (int o = size >> 1; o > 0; o >>= 1) {
+        key64 other;
+        if (o < 32) {
+          other = __shfl_xor_sync(0xffffffffu, mine, o);
+        } else {
+          sh.list[tid] = mine;
+          __syncthreads();
+          other = sh.list[tid ^ o];
+          __syncthreads();
+        }
+        const bool keep_max = ((tid & o) == 0) == ((tid & size) == 0);
+        mine = (mine > other) == keep_max ? mine : other;
+      }
+  }
+  if (to < listed) {
+    const float z = key_value(static_cast<uint32_t>(mine >> 32));
+    ids[to] = static_cast<int>(~static_cast<uint32_t>(mine));
+    logp[to] = __fsub_rn(__fdiv_rn(__fsub_rn(z, M), P.T), L);
   }
   for (int j = listed + tid; j < P.K; j += kTopThreads) ids[j] = -1, logp[j] = valid ? -INFINITY : NAN;
   if (tid == 0) P.lse[r] = valid ? __fadd_rn(__fdiv_rn(M, P.T), L) : M == -INFINITY ? -INFINITY : NAN;
@@ -623,7 +662,11 @@ cudaError_t launch_top(TopParams p, int rows, cudaStream_t s) {
   const int nvec = p.V / Vec<ELT>::N, most = p.K > 128 ? 4 : 8, full = p.K > 128 ? 32 : 304;
   int cluster = 1;
   while (cluster < most && static_cast<long long>(rows) * 2 * cluster <= full && nvec / (2 * cluster) >= kTopTile / 2) cluster *= 2;
-  const int smem = static_cast<int>(sizeof(TopShared));
+  // long lists note more, which is read again; short ones keep it all
+  p.places = p.K > 64 ? 1792 : 1024;
+  p.held = p.K > 64 ? 0 : 256;
+  p.cap = cluster > 1 ? 1792 : p.K > 64 ? 1280 : 768;
+  const int smem = kTopBuffersAt + p.cap * 8 + p.held * kTopUnroll * 16 + p.places * 8;   // below 48 KB
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeClusterDimension;
   attr.val.clusterDim.x = cluster;
@@ -637,7 +680,6 @@ cudaError_t launch_top(TopParams p, int rows, cudaStream_t s) {
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, top_kernel<ELT>, p);
 }
-static_assert(sizeof(TopShared) <= 48 * 1024, "no attribute needed to launch");
 
 }  // namespace
 }  // namespace sv
