@@ -256,17 +256,17 @@ __device__ __noinline__ void select_entries(TopShared& sh, const key64* cand, in
   __syncthreads();
 }
 
-// The n_list largest tokens of a row (of which at least n_list are above
-// -inf) from the row itself, into sh.list in any order: a radix selection on
-// the values, then of the tokens that tie with the last one the lowest ids.
+// The key of the n_list-th largest value of a row, and how many of the tokens
+// that have it are needed: radix, most significant byte first.
 template <int ELT>
-__device__ __noinline__ void select_from_row(TopShared& sh, const unsigned char* row, int V, int n_list) {
+__device__ __noinline__ void select_value(TopShared& sh, const unsigned char* row, int V, int n_list, int& need,
+                                          uint32_t& prefix) {
   using VT = Vec<ELT>;
   constexpr int N = VT::N;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x;
   const int shift = row_shift<ELT>(row), nvec = row_vecs<ELT>(V, shift);
-  int need = n_list;
-  uint32_t prefix = 0;
+  need = n_list;
+  prefix = 0;
   for (int bits = 24; bits >= 0; bits -= 8) {
     if (tid < 256) sh.hist[tid] = 0;
     __syncthreads();
@@ -286,9 +286,54 @@ __device__ __noinline__ void select_from_row(TopShared& sh, const unsigned char*
     prefix |= static_cast<uint32_t>(sh.digit) << bits;
     need = sh.left;
   }
-  // `need` of the tokens that tie with key `prefix`, and every larger one
+}
+
+// The n_list largest tokens of a row from the row itself, into sh.list in any
+// order; at least n_list of its tokens reach t (which is above -inf).  Those
+// above t, and where they are fewer of those that tie with t the lowest ids,
+// which a row of few values or one masked with a finite value has at its very
+// front.  Where more are above t than `tokens` holds, a radix selection on the
+// values first.
+template <int ELT>
+__device__ __noinline__ void select_from_row(TopShared& sh, const unsigned char* row, int V, int n_list, float t, float M,
+                                             key64* tokens, int cap) {
+  using VT = Vec<ELT>;
+  constexpr int N = VT::N;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int shift = row_shift<ELT>(row), nvec = row_vecs<ELT>(V, shift);
+  __syncthreads();
+  if (tid == 0) sh.n_tokens = sh.n_list = 0;
+  __syncthreads();
+  for (int v = tid; v < nvec; v += kTopThreads) {
+    const uint4 one[1] = {load_row_vec<ELT>(row, V, shift, v)};
+    if (!(VT::vmax(one) > t)) continue;
+    float z[N];
+    VT::unpack(one[0], z);
+#pragma unroll
+    for (int e = 0; e < N; ++e)
+      if (z[e] > t) {
+        const unsigned at = atomicAdd(&sh.n_tokens, 1u);
+        if (at < static_cast<unsigned>(cap)) tokens[at] = top_entry(top_key(z[e]), static_cast<uint32_t>(v * N - shift + e));
+      }
+  }
+  __syncthreads();
+  const int above = static_cast<int>(min(sh.n_tokens, 0x7fffffffu));
+  if (above >= n_list && above <= cap) {
+    select_entries(sh, tokens, above, n_list, top_key(t), top_key(M));
+    return;
+  }
+  int need = n_list - above;
+  uint32_t prefix = top_key(t);
+  if (above < n_list) {
+    for (int i = tid; i < above; i += kTopThreads) sh.list[i] = tokens[i];
+  } else {
+    select_value<ELT>(sh, row, V, n_list, need, prefix);
+  }
+  // `need` of the tokens that tie with key `prefix` (and, after a selection,
+  // every larger one)
+  const bool larger = above >= n_list;
   unsigned ties_before = 0;
-  for (int v0 = 0; v0 < nvec; v0 += kTopThreads) {
+  for (int v0 = 0; v0 < nvec && (larger || ties_before < static_cast<unsigned>(need)); v0 += kTopThreads) {
     const int v = v0 + tid;
     float z[N];
     unsigned tie = 0;
@@ -297,7 +342,7 @@ __device__ __noinline__ void select_from_row(TopShared& sh, const unsigned char*
 #pragma unroll
       for (int e = 0; e < N; ++e) {
         const uint32_t key = top_key(z[e]);
-        if (key > prefix) sh.list[atomicAdd(&sh.n_list, 1u)] = top_entry(key, static_cast<uint32_t>(v * N - shift + e));
+        if (larger && key > prefix) sh.list[atomicAdd(&sh.n_list, 1u)] = top_entry(key, static_cast<uint32_t>(v * N - shift + e));
         else if (key == prefix && key > kKeyNegInf) tie |= 1u << e;
       }
     }
@@ -592,8 +637,8 @@ __global__ void __launch_bounds__(kTopThreads, 4) top_kernel(const __grid_consta
   }
 
   // ---- the row's M and S
-  float M = -INFINITY, S = 0.f, t_min = INFINITY;
-  for (int c = 0; c < ctas; ++c) t_min = fminf(t_min, sh.t[c]);
+  float M = -INFINITY, S = 0.f, t_min = INFINITY, t_max = -FLT_MAX;
+  for (int c = 0; c < ctas; ++c) t_min = fminf(t_min, sh.t[c]), t_max = fmaxf(t_max, sh.t[c]);
   for (int c = 0; c < ctas; ++c) M = fmax_nan(M, sh.M[c]);
   for (int c = 0; c < ctas; ++c)
     if (sh.M[c] > -INFINITY) S += sh.S[c] * fast_exp2(__fsub_rn(top_scale(sh.M[c], P.c2), top_scale(M, P.c2)));
@@ -609,7 +654,7 @@ __global__ void __launch_bounds__(kTopThreads, 4) top_kernel(const __grid_consta
     if (!fits || n_ranked > kTopCount) {
       // more candidates than the buffers hold are K of them at least
       if (fits) select_entries(sh, tokens, n_ranked, listed, top_key(t_min), top_key(M));
-      else select_from_row<ELT>(sh, row, P.V, listed);
+      else select_from_row<ELT>(sh, row, P.V, listed, t_max, M, tokens, P.cap);
       from = sh.list;
       n_ranked = listed;
     }
