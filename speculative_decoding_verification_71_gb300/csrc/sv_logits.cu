@@ -20,10 +20,12 @@
 //     are under way while the history is counted;
 //   - the tokens of the bitmap, a thread for each token of each row.
 // On 256 sequences of up to four rows of 128256 bf16 logits with histories of
-// up to 4096 tokens: 74 us (4.5 TB/s of what has to be read and written), the
+// up to 4096 tokens: 71 us (4.7 TB/s of what has to be read and written), the
 // copy alone 53 us.  Bound by the chain of short phases that each CTA goes
-// through besides its copy (count, list, correct: 4 us for the counting, 16 us
-// for the corrections, though they move little).  Measured the other way:
+// through besides its copy (count, list, correct: they move little, and grow
+// with the distinct tokens, from 57 us at histories of 64 tokens to 71 us at
+// 4096).  Every load whose address is known goes out before the first barrier:
+// 74 us with the drafts' and numbers' loads behind it.  Measured the other way:
 // looking the table up while streaming 193 us (nearly every warp holds some
 // repeated token and runs the rule for one or two of its lanes); listing the
 // tokens while counting them 105 us; one history for a cluster's CTAs, with
@@ -265,6 +267,14 @@ __global__ void __launch_bounds__(kLgThreads, kLgCtas) logits_kernel(const __gri
     plen = P.prompt_len ? P.prompt_len[b] : 0;
     load_history(h, 0, P.history_max, P.history_vec, t);
   }
+  int draft = -1;                                  // thread j has draft j
+  float number = 0.f;                              // and one of the sequence's numbers
+  if (P.table) {
+    if (P.tokens && tid < P.k) draft = P.tokens[static_cast<long long>(b) * P.k + tid];
+    if (tid == 0) number = P.repetition ? P.repetition[b] : 1.f;
+    if (tid == 1) number = P.presence ? P.presence[b] : 0.f;
+    if (tid == 2) number = P.frequency ? P.frequency[b] : 0.f;
+  }
   RowPart<ELT, U, MASK> part;
   if (copies) {
     part.load_mask(P, r0, s0);
@@ -276,20 +286,14 @@ __global__ void __launch_bounds__(kLgThreads, kLgCtas) logits_kernel(const __gri
   if (P.table) {
     uint4* zero = reinterpret_cast<uint4*>(smem);
     for (int w = tid; w < (span + n_bitmap) / 4; w += kLgThreads) zero[w] = make_uint4(0, 0, 0, 0);
-    if (tid == 0) {
-      n_listed = 0;
-      numbers[0] = P.repetition ? P.repetition[b] : 1.f;
-    }
-    if (tid == 1) numbers[1] = P.presence ? P.presence[b] : 0.f;
-    if (tid == 2) numbers[2] = P.frequency ? P.frequency[b] : 0.f;
+    if (tid == 0) n_listed = 0;
+    __syncthreads();                             // waits for none of the loads
   }
   if (kb < 0 || kb > P.k) return;                // the verifier reports it
   const int rows = P.draft_len ? min(P.R, kb + (P.R - P.k)) : P.R;
   const int n_drafts = P.tokens ? kb : 0;
   LogitsFix fix;                                 // this thread's first (token, row) pair
   if (P.table) {
-    if (tid < n_drafts) drafts[tid] = P.tokens[static_cast<long long>(b) * P.k + tid];
-    __syncthreads();
     auto touch = [&](int u) { atomicOr(&touched[u >> 5], 1u << (u & 31)); };
     // a token's place in this CTA's table, or -1
     auto place = [&](int x) {
@@ -304,8 +308,10 @@ __global__ void __launch_bounds__(kLgThreads, kLgCtas) logits_kernel(const __gri
       }
       __syncthreads();
     }
+    if (tid < 3) numbers[tid] = number;
     if (tid < n_drafts) {
-      const int u = place(drafts[tid]);
+      drafts[tid] = draft;
+      const int u = place(draft);
       if (u >= 0) atomicOr(&tab[u], kLgDraft), touch(u);
     }
     if (P.history) {
