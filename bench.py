@@ -88,7 +88,7 @@ def parse():
     ap.add_argument("--profile-kernels", default="",
                     help="run each named kernel's representative case twice (for ncu, one kernel per "
                          "capture): comma list of verify (the default schedule), verify_cluster, verify_dense, early_exit, "
-                         "compact, debug, kd, tree, ctrl")
+                         "compact, debug, kd, tree, ctrl, process, kd_top, kd_top_loss")
     return ap.parse_args()
 
 
@@ -840,6 +840,11 @@ def profile_kernels(args):
       tree            spec_verify_tree on the tree workload (B=64, 15 nodes, V=151936 bf16): tree_kernel
       ctrl            spec_ctrl_observe + spec_ctrl_choose (B=1024 slots, max_k=7): ctrl_observe_kernel +
                       ctrl_choose_kernel
+      process         process_logits on the ragged batch's target rows, histories of up to 4096 tokens, the three
+                      penalties: logits_kernel
+      kd_top          kd_top of the ragged batch's emitted rows, 64 tokens a row: top_kernel
+      kd_top_loss     kd_top_loss with the gradient, 16 rollouts x 64 positions, V=151936 bf16, lists of 64 tokens:
+                      toploss_kernel + toploss_sum_kernel
     """
     import torch
 
@@ -920,6 +925,23 @@ def profile_kernels(args):
                 ch = torch.empty(1, dtype=torch.int32, device=device)
                 c.observe(ids, kb, on)
                 c.choose(ids, nxt, ch)
+            elif name == "process":
+                g = torch.Generator(device=device).manual_seed(12)
+                # tokens by a rough power law, as text repeats itself
+                h = (torch.rand(w.B, 4096, generator=g, device=device).pow(6) * w.V).to(torch.int32)
+                n = torch.randint(512, 4097, (w.B,), generator=g, device=device, dtype=torch.int32)
+                svp.process_logits(inp["target"], h, n // 4, n, inp["tokens"], inp["draft_len"],
+                                   torch.full((w.B,), 1.1, device=device), torch.full((w.B,), 0.2, device=device),
+                                   torch.full((w.B,), 0.1, device=device))
+            elif name == "kd_top":
+                svp.kd_top(inp["target"], 64, n_rows=ol)
+            elif name == "kd_top_loss":
+                g = torch.Generator(device=device).manual_seed(13)
+                t = torch.randn(16, 64, 151936, generator=g, device=device) * 3.0
+                d = (t + torch.randn(t.shape, generator=g, device=device) * 0.7).to(torch.bfloat16)
+                ids, logp, _ = svp.kd_top(t.to(torch.bfloat16), 64)
+                svp.kd_top_loss(ids, logp, d, torch.rand(16, generator=g, device=device))
+                del t, d
             else:
                 raise SystemExit(f"unknown kernel case {name}")
             torch.cuda.synchronize()

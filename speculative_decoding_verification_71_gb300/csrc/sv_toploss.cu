@@ -60,7 +60,7 @@ struct TopLossParams {
   int t_len, V, K;
   int renorm;
   int same_shift;              // draft and grad lie alike: 16-byte stores
-  float c2, T, inv_T;
+  float c2, inv_T;              // log2(e) / T, 1 / T
 };
 
 // A part's sums: the unlisted tokens' about their maximum m, the listed ones'
@@ -603,7 +603,7 @@ extern "C" sv_status spec_kd_top_loss(int n_seq, int t_len, int V, sv_dtype dtyp
   if (!(c2 < 1e30)) return SV_ERR_INVALID_ARG;
   TopLossParams p{ids, logp, static_cast<const unsigned char*>(draft_logits), weights, row_kl,
                   static_cast<unsigned char*>(grad), t_len, V, K, mode == SV_KD_TOP_RENORM, (a % 16) == (g % 16),
-                  static_cast<float>(c2), temperature, 1.f / temperature};
+                  static_cast<float>(c2), 1.f / temperature};
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   NvtxRange range("spec_kd_top_loss");
   const int rows = n_seq * t_len;
