@@ -362,8 +362,8 @@ __global__ void __launch_bounds__(kLgThreads, kLgCtas) logits_kernel(const __gri
     __syncthreads();
     n_fixes = n_listed * rows;
     if (tid < n_fixes) {   // what it reads arrives during the copy
-      const int i = tid % rows;
-      fix.load<ELT>(P, r0 + i, s0, n_slice, tab[list[tid / rows]], list[tid / rows], b);
+      const int i = tid / n_listed, u = list[tid - i * n_listed];
+      fix.load<ELT>(P, r0 + i, s0, n_slice, tab[u], u, b);
     }
   }
 
@@ -398,10 +398,12 @@ __global__ void __launch_bounds__(kLgThreads, kLgCtas) logits_kernel(const __gri
   if (n_fixes == 0) return;
 
   // ---- the tokens of the table, their stores after the copy's: a thread for
-  // each token of each row
+  // each token of each row, row by row, so that a warp's tokens are neighbours
+  // where a slice holds many (48 sequences of eight rows with histories of
+  // 16384: 68.5 us, with a token's rows side by side 70.2)
   __syncthreads();
   auto correct = [&](const LogitsFix& f, int j) {
-    const int i = j % rows, u = list[j / rows];
+    const int i = j / n_listed, u = list[j - i * n_listed];
     if (!f.mine) return;
     int n = static_cast<int>(f.word & kLgCount);
     if (f.word & kLgDraft)
@@ -421,8 +423,8 @@ __global__ void __launch_bounds__(kLgThreads, kLgCtas) logits_kernel(const __gri
     LogitsFix more[kMore];
 #pragma unroll
     for (int q = 0; q < kMore; ++q) {
-      const int j = min(j0 + q * kLgThreads, n_fixes - 1), u = list[j / rows];
-      more[q].load<ELT>(P, r0 + j % rows, s0, n_slice, tab[u], u, b);
+      const int j = min(j0 + q * kLgThreads, n_fixes - 1), i = j / n_listed, u = list[j - i * n_listed];
+      more[q].load<ELT>(P, r0 + i, s0, n_slice, tab[u], u, b);
     }
 #pragma unroll
     for (int q = 0; q < kMore; ++q)
@@ -486,8 +488,13 @@ extern "C" sv_status sv_process_logits(int B, int R, int V, sv_dtype dtype, cons
   int unroll = 1;
   auto slices = [&](int u) { return (V + n - 1 + kLgThreads * u * n - 1) / (kLgThreads * u * n); };
   while (unroll < 4 && static_cast<long long>(B) * slices(2 * unroll) >= kLgEnough) unroll *= 2;
-  // fp32 slices of as many tokens as bf16's: the history is read once a slice
-  p.parts = elt == 4 && unroll == 4 && p.history && static_cast<long long>(B) * slices(8) >= kLgEnough ? 2 : 1;
+  // fp32 slices of as many tokens as bf16's, as the history is read once a
+  // slice; but not where the corrections of a slice of frequent tokens would
+  // outlast the rest.  B=512 rows with histories of 16384: 159 us against 190;
+  // R=2 92 against 104; R=4 and 4096 118 against 125, 16384 181 against 155;
+  // R=8 and 2048 89 against 83, 16384 138 against 109
+  const bool few = R <= 2 || (R <= 4 && history_max <= 8192);
+  p.parts = elt == 4 && unroll == 4 && p.history && few && static_cast<long long>(B) * slices(8) >= kLgEnough ? 2 : 1;
   const long long ctas = static_cast<long long>(B) * slices(unroll * p.parts);
   if (ctas > 0x7fffffffLL) return SV_ERR_INVALID_ARG;
   const int n_tokens = kLgThreads * unroll * n * p.parts;
