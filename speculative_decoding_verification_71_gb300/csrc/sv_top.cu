@@ -709,6 +709,10 @@ cudaError_t launch_top(TopParams p, int rows, cudaStream_t s) {
   while (cluster < most && static_cast<long long>(rows) * 2 * cluster <= full && nvec / (2 * cluster) >= kTopTile / 2) cluster *= 2;
   // long lists note more, which is read again; short ones keep it all
   p.places = p.K > 64 ? 1792 : 1024;
+  // a long row notes as many again each time its length doubles (384 fp32 rows
+  // of 262144, K=256: 80 us, with 1792 places 204 us as they run out; 2 % more
+  // at 100000 where they do not, as the rows' loads have less L1)
+  if (nvec / cluster > 20 * kTopTile) p.places += p.K > 64 ? 1280 : 512;
   p.held = p.K > 64 ? 0 : 256;
   p.cap = cluster > 1 ? 1792 : p.K > 64 ? 1280 : 768;
   const int smem = kTopBuffersAt + p.cap * 8 + p.held * kTopUnroll * 16 + p.places * 8;   // below 48 KB

@@ -97,6 +97,12 @@ def test_top_matches_the_definition(n_seq, t_len, V, dtype, K, T):
     check_top(randn(n_seq, t_len, V, seed=V, dtype=dtype), K, T)
 
 
+@pytest.mark.parametrize("V,dtype,K", [(262147, torch.float32, 256), (262147, torch.float32, 64),
+                                       (200003, torch.bfloat16, 256), (140001, torch.float32, 200)])
+def test_top_of_long_rows_that_are_not_split(V, dtype, K):
+    check_top(randn(6, 3 if K > 128 else 26, V, seed=V + K, dtype=dtype), K)
+
+
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("K", [1, 20, 64, 256])
 @pytest.mark.parametrize("V", [300, 9001, 70000])
