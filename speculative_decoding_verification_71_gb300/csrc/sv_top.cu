@@ -48,6 +48,7 @@ namespace {
 constexpr int kTopThreads = 256;
 constexpr int kTopWarps = kTopThreads / 32;
 constexpr int kTopMaxK = SV_KD_TOP_MAX;
+constexpr int kTopSms = 152;
 constexpr int kTopUnroll = 4;             // 16-byte vectors of a tile per thread
 constexpr int kTopTile = kTopThreads * kTopUnroll;
 constexpr int kTopLeft = 768;             // noted places that hold a token at or above the final t
@@ -440,6 +441,18 @@ __global__ void __launch_bounds__(kTopThreads, 4) top_kernel(const __grid_consta
   auto take = [&](const uint4 (&w)[kTopUnroll], int at, bool publish, bool barrier) {
     const float vm = VT::vmax(w);        // NaN is passed over here and kept by the sum
     m2 = fmaxf(m2, fminf(m, vm));
+    // The first tile has no second maximum but within itself: 384 bf16 rows of
+    // 6937, K=255: 16 us, without it 43 us (t is low and the buffers overflow).
+    if (barrier && P.quota > 16) {
+      float most = -INFINITY;
+#pragma unroll
+      for (int q = 0; q < kTopUnroll; ++q) {
+        const uint4 one[1] = {w[q]};
+        const float x = VT::vmax(one);
+        m2 = fmaxf(m2, fminf(most, x));
+        most = fmaxf(most, x);
+      }
+    }
     if (vm > m) {
       const float kn = fmaxf(__fmul_rn(vm, P.c2), -FLT_MAX);
       const float f = m > -INFINITY ? fast_exp2(__fsub_rn(k0, kn)) : 0.f;
@@ -701,12 +714,22 @@ __global__ void __launch_bounds__(kTopThreads, 4) top_kernel(const __grid_consta
 
 template <int ELT>
 cudaError_t launch_top(TopParams p, int rows, cudaStream_t s) {
-  // A row is split only where there are few: each part has its own first tile,
-  // in which little is known of t, and its own end.  Half a tile at least to
-  // each part; long lists, whose parts cost more to join, are split less.
-  const int nvec = p.V / Vec<ELT>::N, most = p.K > 128 ? 4 : 8, full = p.K > 128 ? 32 : 304;
+  // A row is split only where there are few, as each part has its own first
+  // tile, in which little is known of t, and its own end; half a tile at least
+  // to each part.  The parts of long lists cost more to join, so only long rows
+  // are split for them, and where the SMs have about a row each, two CTAs to a
+  // row are for long rows alone.  In us, split and whole, bf16:
+  //   16 rows of  32000: K=64  9.5 and 10.5, K=128 17.1 and 14.0
+  //   16 rows of 128256: K=64 11.8 and 17.9, K=128 18.5 and 21.3, K=256 23.5 and 24.0
+  //  140 rows of  64000: K=64 16.6 and 14.0, K=128 21.8 and 17.0
+  //  140 rows of 128256: K=64 19.3 and 21.3, K=128 26.5 and 24.7
+  //  140 rows of 262144: K=64 26.0 and 33.4, K=128 35.0 and 37.4
+  const int nvec = p.V / Vec<ELT>::N, most = p.K > 128 ? 4 : 8;
+  const int least = rows > kTopSms / 2 ? (p.K > 64 ? 20 : 12) : p.K > 64 ? 12 : 0;   // tiles
   int cluster = 1;
-  while (cluster < most && static_cast<long long>(rows) * 2 * cluster <= full && nvec / (2 * cluster) >= kTopTile / 2) cluster *= 2;
+  while (cluster < most && static_cast<long long>(rows) * 2 * cluster <= 2 * kTopSms && nvec >= least * kTopTile &&
+         nvec / (2 * cluster) >= kTopTile / 2)
+    cluster *= 2;
   // long lists note more, which is read again; short ones keep it all
   p.places = p.K > 64 ? 1792 : 1024;
   // a long row notes as many again each time its length doubles (384 fp32 rows
@@ -715,7 +738,12 @@ cudaError_t launch_top(TopParams p, int rows, cudaStream_t s) {
   if (nvec / cluster > 20 * kTopTile) p.places += p.K > 64 ? 1280 : 512;
   p.held = p.K > 64 ? 0 : 256;
   p.cap = cluster > 1 ? 1792 : p.K > 64 ? 1280 : 768;
-  const int smem = kTopBuffersAt + p.cap * 8 + p.held * kTopUnroll * 16 + p.places * 8;   // below 48 KB
+  const int smem = kTopBuffersAt + p.cap * 8 + p.held * kTopUnroll * 16 + p.places * 8;
+  // long rows split in two take more than the 48 KB that need no asking
+  if (smem > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(top_kernel<ELT>, cudaFuncAttributeMaxDynamicSharedMemorySize, 64 * 1024);
+    if (e != cudaSuccess) return e;
+  }
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeClusterDimension;
   attr.val.clusterDim.x = cluster;

@@ -103,6 +103,19 @@ def test_top_of_long_rows_that_are_not_split(V, dtype, K):
     check_top(randn(6, 3 if K > 128 else 26, V, seed=V + K, dtype=dtype), K)
 
 
+@pytest.mark.parametrize("V,dtype,K,rows", [(300001, torch.float32, 64, 90), (300001, torch.float32, 200, 90),
+                                            (700001, torch.float32, 256, 2), (700001, torch.bfloat16, 128, 40)])
+def test_top_of_long_rows_that_are_split(V, dtype, K, rows):
+    check_top(randn(rows, 1, V, seed=V + K, dtype=dtype), K)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("K", [129, 200, 256])
+@pytest.mark.parametrize("V", [257, 1100, 4001, 8190])
+def test_top_of_short_rows_with_long_lists(V, K, dtype):
+    check_top(randn(7, 3, V, seed=V + K, dtype=dtype), K)
+
+
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("K", [1, 20, 64, 256])
 @pytest.mark.parametrize("V", [300, 9001, 70000])
