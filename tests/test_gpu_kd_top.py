@@ -322,6 +322,11 @@ def test_loss_matches_the_definition(n_seq, t_len, V, dtype, K, T, tail):
     check_loss(*pair(n_seq, t_len, V, dtype, K, T, seed=V), T, tail)
 
 
+@pytest.mark.parametrize("n_seq,t_len", [(1, 1500), (3, 257), (9, 256), (300, 1)])
+def test_loss_of_few_and_many_positions(n_seq, t_len):
+    check_loss(*pair(n_seq, t_len, 130, torch.float32, 8, 1.0, seed=n_seq), 1.0, True)
+
+
 @pytest.mark.parametrize("tail", [True, False], ids=["tail", "renorm"])
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("V", [333, 40001])
