@@ -12,7 +12,8 @@
 // logits.  So with E = 2^((z - M) c) the gradient of an unlisted token is one multiply,
 // E * w / T * (1 / Z - r / S), Z the row's whole sum scaled alike.
 //
-// Rows go to clusters of 1 to 8 CTAs, two CTAs to an SM, row c + i * clusters
+// Short rows take a CTA each and stay in its registers.  Longer ones go to
+// clusters of 1 to 8 CTAs, two CTAs to an SM, row c + i * clusters
 // to cluster c; each CTA takes a part of the row.  A producer warp streams it
 // through a ring of three 32 KB slots, 8 consumer warps sum it and, for the
 // gradient, take it a second time from L2, where it was a few microseconds
@@ -529,6 +530,146 @@ __global__ void __launch_bounds__(kTrThreads, kTrCtas) toploss_kernel(const __gr
   if (ctas > 1) cluster_sync();   // nothing is on its way to a CTA that has left
 }
 
+// ---- short rows: a CTA to a row, which stays in its registers
+//
+// What a streamed row costs besides its bytes (the ring's hand-overs, five
+// barriers and a list among two CTAs an SM, 5 us) is more than a short row's
+// time on the wire; here twice the CTAs work at once and the row is read once.
+// Bound by its instructions: the list and the row's numbers cost as much as
+// 8000 logits (with every warp working out the row's numbers for itself 50000
+// rows of 4000 took 391 us).
+constexpr int kTsThreads = 256, kTsWarps = kTsThreads / 32;
+static_assert(kTsThreads >= SV_KD_TOP_MAX && kTsWarps == kTrWarps, "a thread for each entry of the list");
+
+template <int ELT, int U, bool GRAD>
+__global__ void __launch_bounds__(kTsThreads, U > 4 ? 3 : 4) toploss_short_kernel(const __grid_constant__ TopLossParams P) {
+  using VT = Vec<ELT>;
+  constexpr int N = VT::N;
+  __shared__ uint32_t listed[kTsThreads * U * N / 32];   // a bit for each place of the row's vectors
+  __shared__ TlPart parts[kTsWarps];
+  __shared__ double masses[kTsWarps];
+  __shared__ float terms[kTsWarps];
+  __shared__ TlRow total;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const long long r = blockIdx.x;
+  unsigned char* grad = GRAD ? P.grad + r * P.V * ELT : nullptr;
+  const unsigned char* row = P.draft + r * P.V * ELT;
+  const int shift = row_shift<ELT>(row), nvec = row_vecs<ELT>(P.V, shift);
+  // ---- every load goes out at once; thread j holds entry j of the list
+  int id = -1;
+  float lp = -INFINITY;
+  if (tid < P.K) {
+    id = P.ids[r * P.K + tid];
+    lp = P.logp[r * P.K + tid];
+  }
+  const float weight = GRAD ? P.weights[r / P.t_len] : 0.f;
+  uint4 w[U];
+#pragma unroll
+  for (int k = 0; k < U; ++k)
+    w[k] = tid + k * kTsThreads < nvec ? load_row_vec<ELT>(row, P.V, shift, tid + k * kTsThreads) : VT::neg_inf();
+  for (int i = tid; i < kTsThreads * U * N / 32; i += kTsThreads) listed[i] = 0;
+  grid_dependents_launch();
+  bool bad = lp != lp || lp == INFINITY || id >= P.V;
+  if (id >= P.V) id = -1;
+  if (!__syncthreads_or(id >= 0 || bad)) {             // no list: no loss
+    if (tid == 0) P.row_kl[r] = 0.f;
+    if (GRAD)
+#pragma unroll
+      for (int k = 0; k < U; ++k)
+        if (tid + k * kTsThreads < nvec)
+          store_edge<ELT>(grad, P.V, (tid + k * kTsThreads) * N - shift, P.same_shift, make_uint4(0, 0, 0, 0));
+    return;
+  }
+  float zj = -INFINITY, p = 0.f;
+  if (id >= 0) {
+    const uint32_t bit = 1u << ((id + shift) & 31);
+    bad |= (atomicOr(&listed[(id + shift) >> 5], bit) & bit) != 0;   // listed twice
+    zj = load_elem<ELT>(row, id);
+    p = expf(lp);
+  }
+  __syncthreads();
+
+  // ---- the unlisted tokens' maximum and sum
+#pragma unroll
+  for (int k = 0; k < U; ++k) {
+    const int at = (tid + k * kTsThreads) * N;
+    const uint32_t in = (listed[at >> 5] >> (at & 31)) & ((1u << N) - 1u);
+    if (in) w[k] = with_neg_inf<ELT>(w[k], in);
+  }
+  const f2 cc = pack2(P.c2, P.c2);
+  const float m = VT::vmax(w);             // NaN is passed over here and kept by the sum
+  const float mb = m > -INFINITY ? m : 0.f;
+  const f2 mm = pack2(mb, mb);
+  f2 s2 = 0ull, s3 = 0ull;
+#pragma unroll
+  for (int k = 0; k < U; ++k) {
+    f2 z[N / 2];
+    VT::pairs(w[k], z);
+#pragma unroll
+    for (int i = 0; i < N / 2; i += 2) {
+      s2 = add2(s2, exp2_2(mul2(sub2(z[i], mm), cc)));
+      s3 = add2(s3, exp2_2(mul2(sub2(z[i + 1], mm), cc)));
+    }
+  }
+  bad |= zj != zj || zj == INFINITY;
+  float s, s_hi;
+  unpack2(add2(s2, s3), s, s_hi);
+  TlPart part{m, s + s_hi, zj, zj > -INFINITY ? 1.f : 0.f};
+  if (bad) part.s = NAN;
+  part = tl_combine(part, P.c2, P.inv_T);
+  double mass = warp * 32 < P.K ? warp_sum(static_cast<double>(p)) : 0.0;
+  if (lane == 0) parts[warp] = part, masses[warp] = mass;
+  __syncthreads();
+
+  // ---- the row's numbers, by one warp for all
+  const float scale = weight * P.inv_T;
+  if (warp == 0) {
+    const TlPart none{-INFINITY, 0.f, -INFINITY, 0.f};
+    part = tl_combine(lane < kTsWarps ? parts[lane] : none, P.c2, P.inv_T);
+    mass = masses[lane % kTsWarps];
+#pragma unroll
+    for (int o = kTsWarps / 2; o > 0; o >>= 1) mass += __shfl_xor_sync(0xffffffffu, mass, o);
+    const TlRow mine = tl_row(part, mass, scale, P);
+    if (lane == 0) total = mine;
+  }
+  __syncthreads();
+  const TlRow R = total;
+
+  // ---- the gradient, the listed tokens' after the others'
+  if (GRAD) {
+    const f2 bb = pack2(R.base, R.base), aa = pack2(R.a, R.a);
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      f2 z[N / 2];
+      float g[N];
+      VT::pairs(w[k], z);
+#pragma unroll
+      for (int i = 0; i < N / 2; ++i) unpack2(mul2(aa, exp2_2(mul2(sub2(z[i], bb), cc))), g[2 * i], g[2 * i + 1]);
+      const int v = tid + k * kTsThreads, t0 = v * N - shift;
+      if (P.same_shift && t0 >= 0 && t0 <= P.V - N) store_vec16(grad + static_cast<long long>(t0) * ELT, VT::pack(g));
+      else if (v < nvec) store_edge<ELT>(grad, P.V, t0, P.same_shift, VT::pack(g));
+    }
+  }
+  const float lj = __fmul_rn(__fsub_rn(zj, R.Ma), P.inv_T);
+  if (P.renorm) {
+    lp = R.mass > 0.f ? __fsub_rn(lp, logf(R.mass)) : -INFINITY;
+    p = R.mass > 0.f ? __fdiv_rn(p, R.mass) : 0.f;
+  }
+  float term = id >= 0 && p > 0.f ? __fmul_rn(p, __fsub_rn(lp, __fsub_rn(lj, R.LZ))) : 0.f;
+  term = warp_sum(term);
+  if (lane == 0) terms[warp] = term;
+  __syncthreads();
+  if (GRAD && id >= 0) {
+    const float qj = zj > -INFINITY ? __fdiv_rn(expf(lj), R.Z) : 0.f;
+    VT::store_rounded(grad, id, R.valid ? scale * __fsub_rn(qj, p) : NAN);
+  }
+  if (tid == 0) {
+    float kl = R.kl;
+    for (int i = 0; i < kTsWarps; ++i) kl += terms[i];
+    P.row_kl[r] = R.valid ? kl : NAN;
+  }
+}
+
 // loss[b] = w_b * sum_t row_kl[b, t] in 64 bits and a fixed order: by a warp,
 // by all warps of a CTA where positions are many (one rollout of 4096: 3 us,
 // by one thread 300).
@@ -567,6 +708,20 @@ cudaError_t launch_toploss(const TopLossParams& p, int rows, cudaStream_t s) {
   // (more than two wait for one another longer than that saves: 888 us with
   // four).
   const long long row_bytes = static_cast<long long>(p.V) * ELT;
+  // Rows that fit in a CTA's registers, up to 32 KB, the lists' bits with them
+  // (two vectors more for a row off the 16-byte boundary): 50000 bf16 rows of
+  // 4000 logits with gradients 357 us, streamed 903; 25000 of 8000 258 and 482;
+  // 12500 of 16000 248 and 290; 16 of 16000 8.5 and 9.3.
+  const int vecs = static_cast<int>(row_bytes / 16) + 2;
+  if (vecs <= 8 * kTsThreads) {
+    auto launch = [&](auto kernel) {
+      kernel<<<static_cast<unsigned>(rows), kTsThreads, 0, s>>>(p);
+      return cudaGetLastError();
+    };
+#define SV_LAUNCH(U) (p.grad ? launch(toploss_short_kernel<ELT, U, true>) : launch(toploss_short_kernel<ELT, U, false>))
+    return vecs <= 2 * kTsThreads ? SV_LAUNCH(2) : vecs <= 4 * kTsThreads ? SV_LAUNCH(4) : SV_LAUNCH(8);
+#undef SV_LAUNCH
+  }
   int cluster = 1;
   while (cluster < kTlMaxCtas && rows * 2 * cluster <= kTrGrid && row_bytes / (2 * cluster) >= kTrMinPart) cluster *= 2;
   if (cluster == 1 && p.grad && (rows < kTrGrid ? rows : kTrGrid) * row_bytes > kTrInL2) cluster = 2;

@@ -322,6 +322,13 @@ def test_loss_matches_the_definition(n_seq, t_len, V, dtype, K, T, tail):
     check_loss(*pair(n_seq, t_len, V, dtype, K, T, seed=V), T, tail)
 
 
+@pytest.mark.parametrize("tail", [True, False], ids=["tail", "renorm"])
+@pytest.mark.parametrize("dtype,V", [(torch.bfloat16, V) for V in (4072, 4073, 8175, 8177, 16360, 16367, 16369)] +
+                         [(torch.float32, V) for V in (2035, 2041, 4085, 4091, 8181, 8185)])
+def test_loss_where_the_row_length_changes_the_kernel(dtype, V, tail):
+    check_loss(*pair(3, 3, V, dtype, 70, 0.9, seed=V), 0.9, tail)
+
+
 @pytest.mark.parametrize("n_seq,t_len", [(1, 1500), (3, 257), (9, 256), (300, 1)])
 def test_loss_of_few_and_many_positions(n_seq, t_len):
     check_loss(*pair(n_seq, t_len, 130, torch.float32, 8, 1.0, seed=n_seq), 1.0, True)
