@@ -347,7 +347,7 @@ sv_status spec_kd_launch_shape(int V, sv_dtype dtype, int with_grad, int *cluste
  * 2^20.  Asynchronous on `stream`; no context, no
  * workspace, no allocation; deterministic.  Host-checkable errors (sizes,
  * NULL pointers, overlap, pointers not aligned to dtype) return
- * SV_ERR_INVALID_ARG and launch nothing.  Any V; rows of more than 1 GiB are
+ * SV_ERR_INVALID_ARG and launch nothing.  Any V; rows of more than 1 GiB - 64 KiB are
  * SV_ERR_INVALID_ARG. */
 #define SV_MAX_BIASES 1023
 

@@ -10,8 +10,8 @@
 //   z <- z + bias(v);  z <- -inf where the row's mask has bit v clear
 // in fp32, rounded once to the logits' type.
 //
-// A CTA takes one slice of the vocabulary of one sequence and all its rows.
-// It counts the history's tokens of its slice into a shared-memory table (an
+// A CTA takes one slice of the vocabulary of one sequence and, where there are
+// enough CTAs, all its rows, else a few of them.  It counts the history's tokens of its slice into a shared-memory table (an
 // integer word per token, so the order of the additions cannot show) and
 // marks them in a bitmap.  Two passes over the slice's rows follow:
 //   - the mask and the copy, 16 bytes at a time and without a look at the
@@ -25,7 +25,9 @@
 // through besides its copy (count, list, correct: they move little, and grow
 // with the distinct tokens, from 57 us at histories of 64 tokens to 71 us at
 // 4096).  Every load whose address is known goes out before the first barrier:
-// 74 us with the drafts' and numbers' loads behind it.  Measured the other way:
+// 74 us with the drafts' and numbers' loads behind it; the grid has a dimension
+// for each of a CTA's coordinates, as dividing one index cost 0.4 us a wave.
+// Measured the other way:
 // looking the table up while streaming 193 us (nearly every warp holds some
 // repeated token and runs the rule for one or two of its lanes); listing the
 // tokens while counting them 105 us; one history for a cluster's CTAs, with
@@ -48,7 +50,7 @@ namespace {
 
 constexpr int kLgThreads = 256;
 constexpr int kLgCtas = 4;                // resident per SM
-constexpr int kLgEnough = 1216;           // CTAs that larger slices have to leave
+constexpr int kLgEnough = 912, kLgMost = 2432;   // CTAs: one and a half times those resident, and four times
 constexpr int kLgMaxDrafts = 32;
 // A table word: in the prompt, among the drafts, the last bias's entry + 1
 // and the times generated in the history.
@@ -75,6 +77,7 @@ struct LogitsParams {
   long long history_stride;
   int history_max;
   int B, R, V, k, n_bias;
+  int group_rows;                // rows that a CTA takes
   int parts;                     // passes of 256 U vectors that a slice takes per row
   int list_max;                  // tokens that a table can hold at most
   int history_vec;               // history rows lie on 16 bytes
@@ -252,8 +255,9 @@ __global__ void __launch_bounds__(kLgThreads, kLgCtas) logits_kernel(const __gri
   const int tid = threadIdx.x;
   // slice-major: a vocabulary's first tokens are its most frequent, so the
   // slices with the most to look up go first
-  const int b = blockIdx.x % P.B, s0 = blockIdx.x / P.B * n_slice, first = s0 - kLgPad;
-  const long long r0 = static_cast<long long>(b) * P.R;
+  const int b = blockIdx.x, s0 = static_cast<int>(blockIdx.z) * n_slice, first = s0 - kLgPad;
+  const int i0 = static_cast<int>(blockIdx.y) * P.group_rows;   // this CTA's first row
+  const long long r0 = static_cast<long long>(b) * P.R + i0;
   const bool in_place = P.logits == P.out;
   const bool copies = MASK || !in_place;
 
@@ -290,7 +294,8 @@ __global__ void __launch_bounds__(kLgThreads, kLgCtas) logits_kernel(const __gri
     __syncthreads();                             // waits for none of the loads
   }
   if (kb < 0 || kb > P.k) return;                // the verifier reports it
-  const int rows = P.draft_len ? min(P.R, kb + (P.R - P.k)) : P.R;
+  const int rows = min(P.group_rows, (P.draft_len ? min(P.R, kb + (P.R - P.k)) : P.R) - i0);
+  if (rows <= 0) return;
   const int n_drafts = P.tokens ? kb : 0;
   LogitsFix fix;                                 // this thread's first (token, row) pair
   if (P.table) {
@@ -407,7 +412,7 @@ __global__ void __launch_bounds__(kLgThreads, kLgCtas) logits_kernel(const __gri
     if (!f.mine) return;
     int n = static_cast<int>(f.word & kLgCount);
     if (f.word & kLgDraft)
-      for (int d = 0; d < min(i, n_drafts); ++d) n += drafts[d] == first + u;
+      for (int d = 0; d < min(i0 + i, n_drafts); ++d) n += drafts[d] == first + u;
     const bool seen = n > 0 || (f.word & kLgPrompt);
     if (!seen && !(f.word & kLgBias)) return;   // drafted only later
     float z = f.z;
@@ -455,7 +460,7 @@ extern "C" sv_status sv_process_logits(int B, int R, int V, sv_dtype dtype, cons
   if (history_max > static_cast<int>(kLgCount) || (history_max && history_stride < history_max)) return SV_ERR_INVALID_ARG;
   if (static_cast<long long>(B) * R > (1LL << 30)) return SV_ERR_INVALID_ARG;
   const int elt = dtype == SV_F32 ? 4 : 2;
-  if (static_cast<long long>(V) * elt > (1LL << 30)) return SV_ERR_INVALID_ARG;
+  if (static_cast<long long>(V) * elt > (1LL << 30) - (1 << 16)) return SV_ERR_INVALID_ARG;   // 65535 slices
   const uintptr_t a = reinterpret_cast<uintptr_t>(logits), o = reinterpret_cast<uintptr_t>(out);
   const uintptr_t bytes = static_cast<uintptr_t>(B) * R * V * elt;
   if (a % elt || o % elt) return SV_ERR_INVALID_ARG;
@@ -483,11 +488,19 @@ extern "C" sv_status sv_process_logits(int B, int R, int V, sv_dtype dtype, cons
   p.table = p.history || p.tokens || n_bias;
   p.same_shift = (a % 16) == (o % 16);
 
-  // the largest slices that still give every SM several CTAs
+  // Slices as large as give the SMs enough CTAs with two rows to a CTA: a
+  // history is read once a CTA, and a slice of frequent tokens, which has the
+  // most to correct, is shared out by its rows.  256 rows of 32000 with
+  // histories of 4096: 15.4 us at 1024 CTAs, with half the slice 19.4; 14
+  // sequences of 8 rows of 42896 and 16384: 22 us at 336, 19.8 at 1176.
+  // Then CTAs take fewer rows, down to two, up to kLgMost CTAs (48 sequences of
+  // 8 rows of 100003 fp32 logits: 67.6 us with 4, with 8 79.8), and one as long
+  // as all fit on the SMs twice (33 sequences of 4 rows of 9951: 6.8 us, with
+  // 2 rows 8.4; 64 of 8 of 32000, which would not: 19.1 and 16.4).
   const int n = elt == 2 ? 8 : 4;
   int unroll = 1;
   auto slices = [&](int u) { return (V + n - 1 + kLgThreads * u * n - 1) / (kLgThreads * u * n); };
-  while (unroll < 4 && static_cast<long long>(B) * slices(2 * unroll) >= kLgEnough) unroll *= 2;
+  while (unroll < 4 && static_cast<long long>(B) * slices(2 * unroll) * ((R + 1) / 2) >= kLgEnough) unroll *= 2;
   // fp32 slices of as many tokens as bf16's, as the history is read once a
   // slice; but not where the corrections of a slice of frequent tokens would
   // outlast the rest.  B=512 rows with histories of 16384: 159 us against 190;
@@ -495,8 +508,12 @@ extern "C" sv_status sv_process_logits(int B, int R, int V, sv_dtype dtype, cons
   // R=8 and 2048 89 against 83, 16384 138 against 109
   const bool few = R <= 2 || (R <= 4 && history_max <= 8192);
   p.parts = elt == 4 && unroll == 4 && p.history && few && static_cast<long long>(B) * slices(8) >= kLgEnough ? 2 : 1;
-  const long long ctas = static_cast<long long>(B) * slices(unroll * p.parts);
-  if (ctas > 0x7fffffffLL) return SV_ERR_INVALID_ARG;
+  const long long slice_ctas = static_cast<long long>(B) * slices(unroll * p.parts);
+  int groups = 1;
+  while (groups < (R + 1) / 2 && slice_ctas * (groups + 1) <= kLgMost) ++groups;
+  while (groups < R && slice_ctas * (groups + 1) <= kLgMost / 2) ++groups;
+  p.group_rows = (R + groups - 1) / groups;
+  const dim3 grid(B, (R + p.group_rows - 1) / p.group_rows, slices(unroll * p.parts));
   const int n_tokens = kLgThreads * unroll * n * p.parts;
   const long long held = (p.history ? history_max : 0LL) + (p.tokens ? k : 0) + n_bias;
   p.list_max = static_cast<int>(held < n_tokens + kLgPad ? held : n_tokens + kLgPad);
@@ -509,7 +526,7 @@ extern "C" sv_status sv_process_logits(int B, int R, int V, sv_dtype dtype, cons
     if (smem > 48 * 1024 &&
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 64 * 1024) != cudaSuccess)
       return SV_ERR_CUDA;
-    kernel<<<static_cast<unsigned>(ctas), kLgThreads, smem, s>>>(p);
+    kernel<<<grid, kLgThreads, smem, s>>>(p);
     return cudaGetLastError() == cudaSuccess ? SV_OK : SV_ERR_CUDA;
   };
 #define SV_LAUNCH(ELT, U) (mask ? launch(logits_kernel<ELT, U, true>) : launch(logits_kernel<ELT, U, false>))
