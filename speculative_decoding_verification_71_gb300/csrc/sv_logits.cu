@@ -11,9 +11,10 @@
 // in fp32, rounded once to the logits' type.
 //
 // A CTA takes one slice of the vocabulary of one sequence and, where there are
-// enough CTAs, all its rows, else a few of them.  It counts the history's tokens of its slice into a shared-memory table (an
-// integer word per token, so the order of the additions cannot show) and
-// marks them in a bitmap.  Two passes over the slice's rows follow:
+// CTAs enough, all its rows, else a few of them.  It counts the history's
+// tokens of its slice into a shared-memory table (an integer word per token, so
+// the order of the additions cannot show) and marks them in a bitmap.  Two
+// passes over the slice's rows follow:
 //   - the mask and the copy, 16 bytes at a time and without a look at the
 //     table (a vector that is masked altogether is written without being
 //     read; in place, only what the mask forbids is touched); its first loads
@@ -24,17 +25,19 @@
 // copy alone 53 us.  Bound by the chain of short phases that each CTA goes
 // through besides its copy (count, list, correct: they move little, and grow
 // with the distinct tokens, from 57 us at histories of 64 tokens to 71 us at
-// 4096).  Every load whose address is known goes out before the first barrier:
-// 74 us with the drafts' and numbers' loads behind it; the grid has a dimension
-// for each of a CTA's coordinates, as dividing one index cost 0.4 us a wave.
-// Measured the other way:
-// looking the table up while streaming 193 us (nearly every warp holds some
-// repeated token and runs the rule for one or two of its lanes); listing the
-// tokens while counting them 105 us; one history for a cluster's CTAs, with
-// additions into each other's tables, 110 us (3.6 cycles an addition and SM);
-// persistent CTAs 149 us (rows differ too much); slices of interleaved blocks,
-// which share out a vocabulary's frequent first tokens evenly, 80 to 95 us
-// (more instructions for each token counted).
+// 4096).  Every load whose address is known goes out before the first barrier
+// (74 us with the drafts' and numbers' loads behind it); the grid has a
+// dimension for each of a CTA's coordinates, as dividing one index apart took
+// 0.4 us a wave.  Measured the other way: looking the table up while streaming
+// 193 us (nearly every warp holds some repeated token and runs the rule for one
+// or two of its lanes); listing the tokens while counting them 105 us, marking
+// each with its first addition's result 72.2, finding them in the table
+// afterwards 78; a slice of many tokens row by row through the rule, without a
+// list, 94 (its one CTA outlasts the rest); one history for a cluster's CTAs,
+// with additions into each other's tables, 110 us (3.6 cycles an addition and
+// SM); persistent CTAs 149 us (rows differ too much); slices of interleaved
+// blocks, which share out a vocabulary's frequent first tokens evenly, 80 to
+// 95 us (more instructions for each token counted).
 
 #include <cuda_runtime.h>
 
