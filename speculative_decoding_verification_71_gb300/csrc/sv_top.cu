@@ -131,6 +131,14 @@ __device__ __forceinline__ void first_store(key64* p, key64 v) {
   asm volatile("st.shared::cluster.u64 [%0], %1;" :: "r"(peer(p, 0)), "l"(v) : "memory");
 }
 
+// Element e of a vector, e not known to the compiler.
+template <int ELT>
+__device__ __forceinline__ float element_of(const uint4& v, int e) {
+  const int w = ELT == 4 ? e : e >> 1;
+  const uint32_t lo = w & 1 ? v.y : v.x, hi = w & 1 ? v.w : v.z, x = w & 2 ? hi : lo;
+  return __uint_as_float(ELT == 4 ? x : e & 1 ? x & 0xffff0000u : x << 16);
+}
+
 // The warp's lanes' values in descending order.
 __device__ __forceinline__ float warp_sort(float v, int lane) {
 #pragma unroll
@@ -609,13 +617,15 @@ __global__ void __launch_bounds__(kTopThreads, 4) top_kernel(const __grid_consta
       const uint4 one = q == 0 ? w[0] : q == 1 ? w[1] : q == 2 ? w[2] : w[3];
       float z[N];
       VT::unpack(one, z);
-      const int t0 = (first + q * kTopThreads) * N - shift;
+      unsigned hits = 0;
 #pragma unroll
-      for (int e = 0; e < N; ++e)
-        if (z[e] >= t) {
-          const unsigned at = atomicAdd(&sh.n_tokens, 1u);
-          if (at < static_cast<unsigned>(P.cap)) tokens[at] = top_entry(top_key(z[e]), static_cast<uint32_t>(t0 + e));
-        }
+      for (int e = 0; e < N; ++e) hits |= static_cast<unsigned>(z[e] >= t) << e;
+      unsigned at = atomicAdd(&sh.n_tokens, static_cast<unsigned>(__popc(hits)));
+      const int t0 = (first + q * kTopThreads) * N - shift;
+      for (; hits; hits &= hits - 1, ++at) {
+        const int e = __ffs(hits) - 1;
+        if (at < static_cast<unsigned>(P.cap)) tokens[at] = top_entry(top_key(element_of<ELT>(one, e)), static_cast<uint32_t>(t0 + e));
+      }
     }
   }
   if (rank != 0) {
@@ -673,8 +683,8 @@ __global__ void __launch_bounds__(kTopThreads, 4) top_kernel(const __grid_consta
     }
   }
   // ---- in order: of a few, four neighbours count the larger ones of an entry;
-  // of more a bitonic sort of the least power of two that holds them, an entry
-  // a thread, in registers across a warp's lanes
+  // of more every warp sorts 32, an entry a thread, and looks each up in the
+  // other warps' lists
   static_assert(kTopThreads >= kTopCount && kTopThreads >= kTopMaxK, "an entry a thread");
   key64 mine;
   int to = tid;
@@ -687,21 +697,37 @@ __global__ void __launch_bounds__(kTopThreads, 4) top_kernel(const __grid_consta
     if ((tid & 3) || (tid >> 2) >= n_ranked) to = kTopMaxK;
   } else {
     mine = tid < n_ranked ? from[tid] : 0;   // (0 is less than any)
-    __syncthreads();
-    for (int size = 2; size < 2 * n_ranked; size <<= 1)
-      for (int o = size >> 1; o > 0; o >>= 1) {
-        key64 other;
-        if (o < 32) {
-          other = __shfl_xor_sync(0xffffffffu, mine, o);
-        } else {
-          sh.list[tid] = mine;
-          __syncthreads();
-          other = sh.list[tid ^ o];
-          __syncthreads();
+    const int lists = (n_ranked + 31) / 32;
+    if (warp < lists) {
+#pragma unroll
+      for (int size = 2; size <= 32; size <<= 1)
+#pragma unroll
+        for (int o = size >> 1; o > 0; o >>= 1) {
+          const key64 other = __shfl_xor_sync(0xffffffffu, mine, o);
+          const bool keep_max = ((lane & o) == 0) == ((lane & size) == 0);
+          mine = (mine > other) == keep_max ? mine : other;
         }
-        const bool keep_max = ((tid & o) == 0) == ((tid & size) == 0);
-        mine = (mine > other) == keep_max ? mine : other;
+    }
+    __syncthreads();                       // `from` may be the list
+    sh.list[tid] = mine;
+    __syncthreads();
+    to = kTopMaxK;
+    if (mine != 0) {
+      to = lane;
+      for (int w0 = 0; w0 < lists; w0 += 4) {
+        int larger[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int step = 16; step > 0; step >>= 1)
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            if (sh.list[(w0 + q) * 32 + larger[q] + step - 1] > mine) larger[q] += step;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          larger[q] += sh.list[(w0 + q) * 32 + larger[q]] > mine;
+          if (w0 + q != warp) to += larger[q];
+        }
       }
+    }
   }
   if (to < listed) {
     const float z = key_value(static_cast<uint32_t>(mine >> 32));
