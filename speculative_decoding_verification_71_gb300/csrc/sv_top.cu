@@ -660,11 +660,13 @@ __global__ void __launch_bounds__(kTopThreads, 4) top_kernel(const __grid_consta
   }
 
   // ---- the row's M and S
-  float M = -INFINITY, S = 0.f, t_min = INFINITY, t_max = -FLT_MAX;
-  for (int c = 0; c < ctas; ++c) t_min = fminf(t_min, sh.t[c]), t_max = fmaxf(t_max, sh.t[c]);
-  for (int c = 0; c < ctas; ++c) M = fmax_nan(M, sh.M[c]);
-  for (int c = 0; c < ctas; ++c)
-    if (sh.M[c] > -INFINITY) S += sh.S[c] * fast_exp2(__fsub_rn(top_scale(sh.M[c], P.c2), top_scale(M, P.c2)));
+  float M = sh.M[0], S = sh.S[0], t_min = sh.t[0], t_max = sh.t[0];
+  if (ctas > 1) {
+    for (int c = 1; c < ctas; ++c) M = fmax_nan(M, sh.M[c]), t_min = fminf(t_min, sh.t[c]), t_max = fmaxf(t_max, sh.t[c]);
+    S = 0.f;
+    for (int c = 0; c < ctas; ++c)
+      if (sh.M[c] > -INFINITY) S += sh.S[c] * fast_exp2(__fsub_rn(top_scale(sh.M[c], P.c2), top_scale(M, P.c2)));
+  }
   if (S == 0.f && isfinite(M)) S = sum_again<ELT>(sh, row, P.V, M, P.c2);
   const bool valid = S > 0.f && isfinite(S) && isfinite(M);   // not NaN, +inf, or nothing but -inf
   const float L = __fmaf_rn(0.6931471805599453f, top_residue(M, P.c2), logf(S));
