@@ -23,7 +23,7 @@
 // tile hold a value of at least t notes them, with one ballot and one addition
 // a warp, and their largest value; once t is final, those that still pass are
 // read again, from L2, and their tokens at or above t kept.
-// On 1024 ragged rows of 128256 bf16 logits, K = 64: 50 us; appending token by
+// On 1024 ragged rows of 128256 bf16 logits, K = 64: 46 us; appending token by
 // token while streaming 116 us.
 //
 // The CTAs hand their tokens at or above t, and their M and S, to the
@@ -450,7 +450,7 @@ __global__ void __launch_bounds__(kTopThreads, 4) top_kernel(const __grid_consta
     const float vm = VT::vmax(w);        // NaN is passed over here and kept by the sum
     m2 = fmaxf(m2, fminf(m, vm));
     // The first tile has no second maximum but within itself: 384 bf16 rows of
-    // 6937, K=255: 16 us, without it 43 us (t is low and the buffers overflow).
+    // 6937, K=255: 13 us, without it 40 us (t is low and the buffers overflow).
     if (barrier && P.quota > 16) {
       float most = -INFINITY;
 #pragma unroll
@@ -747,13 +747,14 @@ cudaError_t launch_top(TopParams p, int rows, cudaStream_t s) {
   // to each part.  The parts of long lists cost more to join, so only long rows
   // are split for them, and where the SMs have about a row each, two CTAs to a
   // row are for long rows alone.  In us, split and whole, bf16:
-  //   16 rows of  32000: K=64  9.5 and 10.5, K=128 17.1 and 14.0
-  //   16 rows of 128256: K=64 11.8 and 17.9, K=128 18.5 and 21.3, K=256 23.5 and 24.0
-  //  140 rows of  64000: K=64 16.6 and 14.0, K=128 21.8 and 17.0
-  //  140 rows of 128256: K=64 19.3 and 21.3, K=128 26.5 and 24.7
-  //  140 rows of 262144: K=64 26.0 and 33.4, K=128 35.0 and 37.4
+  //   16 rows of  32000: K=64  8.6 and  8.4, K=128 14.9 and 11.1
+  //   16 rows of  64000: K=64  9.1 and 11.4, K=128 15.4 and 13.8
+  //   16 rows of 128256: K=64 11.2 and 15.9, K=128 16.5 and 18.9, K=256 20.8 and 21.2
+  //  140 rows of  64000: K=64 14.7 and 12.0, K=128 19.0 and 14.5
+  //  140 rows of 128256: K=64 18.0 and 19.4, K=128 23.8 and 22.3
+  //  140 rows of 262144: K=64 24.8 and 31.3, K=128 32.7 and 34.6
   const int nvec = p.V / Vec<ELT>::N, most = p.K > 128 ? 4 : 8;
-  const int least = rows > kTopSms / 2 ? (p.K > 64 ? 20 : 12) : p.K > 64 ? 12 : 0;   // tiles
+  const int least = rows > kTopSms / 2 ? (p.K > 64 ? 20 : 12) : p.K > 64 ? 12 : 4;   // tiles
   int cluster = 1;
   while (cluster < most && static_cast<long long>(rows) * 2 * cluster <= 2 * kTopSms && nvec >= least * kTopTile &&
          nvec / (2 * cluster) >= kTopTile / 2)
@@ -761,7 +762,7 @@ cudaError_t launch_top(TopParams p, int rows, cudaStream_t s) {
   // long lists note more, which is read again; short ones keep it all
   p.places = p.K > 64 ? 1792 : 1024;
   // a long row notes as many again each time its length doubles (384 fp32 rows
-  // of 262144, K=256: 80 us, with 1792 places 204 us as they run out; 2 % more
+  // of 262144, K=256: 79 us, with 1792 places 203 us as they run out; 2 % more
   // at 100000 where they do not, as the rows' loads have less L1)
   if (nvec / cluster > 20 * kTopTile) p.places += p.K > 64 ? 1280 : 512;
   p.held = p.K > 64 ? 0 : 256;
