@@ -172,6 +172,7 @@ struct TrShared {
   TlPart warp[2][kTrWarps];      // the warps' parts
   double mass[2][kTrWarps];      // P in 64 bits: 1 - P keeps what the log-probabilities have
   float term[2][kTrWarps];
+  TlRow row[2];
   int ids[kTrHash];              // open addressing; -1: empty
 };
 constexpr int kTrRingAt = (static_cast<int>(sizeof(TrShared)) + 127) / 128 * 128;
@@ -447,33 +448,36 @@ __global__ void __launch_bounds__(kTrThreads, kTrCtas) toploss_kernel(const __gr
     named_barrier_sync(1, kTrConsumers);
     if (place >= 0) sh.ids[place] = -1;
 
-    // ---- the row's numbers, the same in every warp
-    const TlPart none{-INFINITY, 0.f, -INFINITY, 0.f};
-    part = tl_combine(lane < kTrWarps ? sh.warp[par][lane] : none, P.c2, P.inv_T);
-    if (ctas > 1) {
-      if (warp == 0) {
+    // ---- the row's numbers, by one warp for all
+    const float scale = weight * P.inv_T;
+    if (warp == 0) {
+      const TlPart none{-INFINITY, 0.f, -INFINITY, 0.f};
+      part = tl_combine(lane < kTrWarps ? sh.warp[par][lane] : none, P.c2, P.inv_T);
+      if (ctas > 1) {
         if (lane == 0) mbar_expect_tx(&sh.joined[par], static_cast<uint32_t>(ctas) * 16u);
         if (lane < ctas)
           st_async(peer(&sh.part[par][rank], lane), make_uint4(__float_as_uint(part.m), __float_as_uint(part.s), 0u, 0u),
                    peer(&sh.joined[par], lane));
+        const bool ok = !dead && mbar_wait_bounded(&sh.joined[par], static_cast<uint32_t>(phase), kDrainLimitNs);
+        dead = !__all_sync(0xffffffffu, ok);
+        TlPart other = none;
+        if (lane < ctas && !dead) {
+          const uint4 x = sh.part[par][lane];
+          other.m = __uint_as_float(x.x);
+          other.s = __uint_as_float(x.y);
+        }
+        other = tl_combine(other, P.c2, P.inv_T);
+        part.m = other.m;
+        part.s = dead ? NAN : other.s;
       }
-      const bool ok = !dead && mbar_wait_bounded(&sh.joined[par], static_cast<uint32_t>(phase), kDrainLimitNs);
-      dead = !__all_sync(0xffffffffu, ok);
-      TlPart other = none;
-      if (lane < ctas && !dead) {
-        const uint4 x = sh.part[par][lane];
-        other.m = __uint_as_float(x.x);
-        other.s = __uint_as_float(x.y);
-      }
-      other = tl_combine(other, P.c2, P.inv_T);
-      part.m = other.m;
-      part.s = dead ? NAN : other.s;
-    }
-    mass = sh.mass[par][lane % kTrWarps];
+      mass = sh.mass[par][lane % kTrWarps];
 #pragma unroll
-    for (int o = kTrWarps / 2; o > 0; o >>= 1) mass += __shfl_xor_sync(0xffffffffu, mass, o);
-    const float scale = weight * P.inv_T;
-    const TlRow R = tl_row(part, mass, scale, P);
+      for (int o = kTrWarps / 2; o > 0; o >>= 1) mass += __shfl_xor_sync(0xffffffffu, mass, o);
+      const TlRow mine = tl_row(part, mass, scale, P);
+      if (lane == 0) sh.row[par] = mine;
+    }
+    named_barrier_sync(1, kTrConsumers);
+    const TlRow R = sh.row[par];
 
     // ---- the gradient
     if (GRAD) {
