@@ -390,7 +390,7 @@ __global__ void __launch_bounds__(kTrThreads, kTrCtas) toploss_kernel(const __gr
     // ---- the unlisted tokens: running maximum and sum per lane
     float m = -INFINITY;
     f2 s2 = 0ull, s3 = 0ull;
-    auto add = [&](const uint4 (&w)[kTrPerLane]) {
+    auto add = [&](const auto& w) {        // an array of vectors
       const float vm = VT::vmax(w);        // NaN is passed over here and kept by the sum
       if (vm > m) {
         const float f = m > -INFINITY ? fast_exp2(__fmul_rn(__fsub_rn(m, vm), P.c2)) : 0.f;
@@ -401,9 +401,9 @@ __global__ void __launch_bounds__(kTrThreads, kTrCtas) toploss_kernel(const __gr
       const float mb = m > -INFINITY ? m : 0.f;
       const f2 mm = pack2(mb, mb);
 #pragma unroll
-      for (int k = 0; k < kTrPerLane; ++k) {
+      for (const uint4& x : w) {
         f2 z[N / 2];
-        VT::pairs(w[k], z);
+        VT::pairs(x, z);
 #pragma unroll
         for (int i = 0; i < N / 2; i += 2) {
           s2 = add2(s2, exp2_2(mul2(sub2(z[i], mm), cc)));
@@ -423,19 +423,14 @@ __global__ void __launch_bounds__(kTrThreads, kTrCtas) toploss_kernel(const __gr
       take(w, row.n - v, true);
       add(w);
     }
-    if (warp == 0) {
-      uint4 w[kTrPerLane];
-#pragma unroll
-      for (int k = 0; k < kTrPerLane; ++k) w[k] = VT::neg_inf();
-      if (end >= 0) {
-        uint32_t in = 0;
-        for (int e = 0; e < N; ++e) {
-          const int t = end * N - shift + e;
-          if (t >= 0 && t < P.V) in |= static_cast<uint32_t>(tr_listed(sh.ids, t)) << e;
-        }
-        w[0] = with_neg_inf<ELT>(end_vec, in);
+    if (end >= 0) {
+      uint32_t in = 0;
+      for (int e = 0; e < N; ++e) {
+        const int t = end * N - shift + e;
+        if (t >= 0 && t < P.V) in |= static_cast<uint32_t>(tr_listed(sh.ids, t)) << e;
       }
-      add(w);
+      const uint4 one[1] = {with_neg_inf<ELT>(end_vec, in)};
+      add(one);
     }
     bad |= zj != zj || zj == INFINITY;
     float s, s_hi;
