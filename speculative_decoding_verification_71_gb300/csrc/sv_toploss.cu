@@ -421,7 +421,14 @@ __global__ void __launch_bounds__(kTrThreads, kTrCtas) toploss_kernel(const __gr
     for (int v = 0; v < row.n; v += kTrSlotVecs) {
       uint4 w[kTrPerLane];
       take(w, row.n - v, true);
-      add(w);
+      if (row.n - v > kTrSlotVecs / 2) {
+        add(w);
+      } else {   // a last slot of half the vectors at most (10000 rows of 20000: 245 us, as a whole one 250)
+        uint4 half[kTrPerLane / 2];
+#pragma unroll
+        for (int k = 0; k < kTrPerLane / 2; ++k) half[k] = w[k];
+        add(half);
+      }
     }
     if (end >= 0) {
       uint32_t in = 0;
