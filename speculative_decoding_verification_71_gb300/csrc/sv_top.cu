@@ -28,9 +28,12 @@
 //
 // The CTAs hand their tokens at or above t, and their M and S, to the
 // cluster's first one and leave; it sorts them, after a selection by
-// histogram where they are many.  Notes or tokens that outgrow their buffer (rows of few distinct
-// values, or masked with a finite value) are dropped, and the first CTA
-// selects from the row itself.
+// histogram where they are many: every warp sorts 32, and each of these looks
+// its rank up in the other warps' lists (one barrier for a bitonic sort's
+// twelve; 1024 ragged rows went from 50 to 47 us with it and with a vector's
+// tokens counted before they are placed).  Notes or tokens that outgrow their
+// buffer (rows of few distinct values, or masked with a finite value) are
+// dropped, and the first CTA selects from the row itself.
 
 #include <cuda_runtime.h>
 

@@ -13,9 +13,9 @@
 // E * w / T * (1 / Z - r / S), Z the row's whole sum scaled alike.
 //
 // Short rows take a CTA each and stay in its registers.  Longer ones go to
-// clusters of 1 to 8 CTAs, two CTAs to an SM, row c + i * clusters
-// to cluster c; each CTA takes a part of the row.  A producer warp streams it
-// through a ring of three 32 KB slots, 8 consumer warps sum it and, for the
+// clusters of 1 to 8 CTAs, two CTAs to an SM, row c + i * clusters to cluster
+// c; each CTA takes a part of the row.  A producer warp streams it through a
+// ring of three 32 KB slots, 8 consumer warps sum it and, for the
 // gradient, take it a second time from L2, where it was a few microseconds
 // before.  The ring runs ahead over the end of a row, and the SM's other CTA
 // fills what is left of the gap while a row's numbers are put together.  A
@@ -27,7 +27,7 @@
 // memory; the listed tokens' gradients are stored after the row's.
 //
 // 4096 rows of 151936 bf16 logits with their gradients: 455 us, 5.5 TB/s of
-// each logit read and each gradient written once; the loss alone 190 us, 6.5
+// each logit read and each gradient written once; the loss alone 187 us, 6.7
 // TB/s.  With one CTA to a row the rows at work do not stay in L2 (452 MB read
 // for 311 MB of rows) and the gradients take 523 us.  Kept in the registers of
 // a cluster's CTAs in place of read twice: 742 us, each CTA idle while the
@@ -716,8 +716,8 @@ cudaError_t launch_toploss(const TopLossParams& p, int rows, cudaStream_t s) {
   const long long row_bytes = static_cast<long long>(p.V) * ELT;
   // Rows that fit in a CTA's registers, up to 32 KB, the lists' bits with them
   // (two vectors more for a row off the 16-byte boundary): 50000 bf16 rows of
-  // 4000 logits with gradients 357 us, streamed 903; 25000 of 8000 258 and 482;
-  // 12500 of 16000 248 and 290; 16 of 16000 8.5 and 9.3.
+  // 4000 logits with gradients 358 us, streamed 790; 25000 of 8000 259 and 427;
+  // 12500 of 16000 249 and 263; 16 of 16000 8.6 and 9.2.
   const int vecs = static_cast<int>(row_bytes / 16) + 2;
   if (vecs <= 8 * kTsThreads) {
     auto launch = [&](auto kernel) {
