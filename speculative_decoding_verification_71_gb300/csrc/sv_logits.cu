@@ -506,9 +506,9 @@ extern "C" sv_status sv_process_logits(int B, int R, int V, sv_dtype dtype, cons
   while (unroll < 4 && static_cast<long long>(B) * slices(2 * unroll) * ((R + 1) / 2) >= kLgEnough) unroll *= 2;
   // fp32 slices of as many tokens as bf16's, as the history is read once a
   // slice; but not where the corrections of a slice of frequent tokens would
-  // outlast the rest.  B=512 rows with histories of 16384: 159 us against 190;
-  // R=2 92 against 104; R=4 and 4096 118 against 125, 16384 181 against 155;
-  // R=8 and 2048 89 against 83, 16384 138 against 109
+  // outlast the rest.  512 sequences of one row with histories of 16384: 156 us
+  // against 187; 192 of two 91 and 103; 256 of four with 4096 117 and 123, with
+  // 16384 180 and 153; 96 of eight with 2048 89 and 82, with 16384 137 and 108
   const bool few = R <= 2 || (R <= 4 && history_max <= 8192);
   p.parts = elt == 4 && unroll == 4 && p.history && few && static_cast<long long>(B) * slices(8) >= kLgEnough ? 2 : 1;
   const long long slice_ctas = static_cast<long long>(B) * slices(unroll * p.parts);
