@@ -6,9 +6,13 @@
 //   L = ln S + ln 2 (K0 - M c) = ln sum_x e^((z(x) - M) / T),
 //   lse = M / T + L,  logp(x) = (z(x) - M) / T - L,
 // K0 - M c exactly (a fused multiply-add again), so that a likely token's logp
-// keeps its digits whatever the row's level.  Where M c overflows (a row of
-// nothing but the type's lowest values) the sum is taken of 2^((z - M) c)
-// instead.  The K tokens are those with the largest z, ties
+// keeps its digits.  That holds while K0 - M c, half a unit in K0's last place
+// at most, is small beside the exponent's range: the largest term is 2^(M c -
+// K0).  So K0 is kept within +-2^24 (top_base), and a row whose M c lies
+// outside (one forced to 1e10, or masked whole with -1e30) takes its sum again,
+// of 2^((z - M) c) with the difference first, L = ln S (sum_again).  Taking the
+// difference first everywhere would cost an instruction a pair of logits.
+// The K tokens are those with the largest z, ties
 // to the lower id; a token of probability 0 (z = -inf) is never listed.
 //
 // A row goes to a cluster of 1 to 8 CTAs, each streaming its part of it once:
@@ -385,15 +389,18 @@ __device__ __noinline__ void select_from_row(TopShared& sh, const unsigned char*
   __syncthreads();
 }
 
-// fl(m c), kept in range, and how far it lies above m c (0 where it does not
-// stand for m c: see sum_again).
-__device__ __forceinline__ float top_scale(float m, float c) { return fmaxf(__fmul_rn(m, c), -FLT_MAX); }
-__device__ __forceinline__ float top_residue(float m, float c) {
-  const float k = __fmul_rn(m, c);
-  return k > -FLT_MAX ? -__fmaf_rn(m, c, -k) : 0.f;
+// The base of a sum of maximum m: fl(m c), but within +-kTopFar.  There a term is
+// at most 2^(1/2).  Below -kTopFar the terms vanish against a row whose maximum is
+// above; past kTopFar a sum may be +inf, but then this and every later base is
+// kTopFar, so it is only ever scaled by 1, and NaN comes from NaN alone.
+constexpr float kTopFar = 16777216.f;
+__device__ __forceinline__ float top_base(float m, float c) {
+  return fminf(fmaxf(__fmul_rn(m, c), -kTopFar), kTopFar);
 }
+// ... which is not fl(m c): the sum about it says nothing of a row with this maximum.
+__device__ __forceinline__ bool top_far(float m, float c) { return !(fabsf(__fmul_rn(m, c)) < kTopFar); }
 
-// S of a row whose M c is below the range, as 2^((z - M) c).
+// S of a row whose M c is far, as 2^((z - M) c).
 template <int ELT>
 __device__ __noinline__ float sum_again(TopShared& sh, const unsigned char* row, int V, float M, float c) {
   const int shift = row_shift<ELT>(row), nvec = row_vecs<ELT>(V, shift);
@@ -401,7 +408,9 @@ __device__ __noinline__ float sum_again(TopShared& sh, const unsigned char* row,
   for (int v = threadIdx.x; v < nvec; v += kTopThreads) {
     float z[Vec<ELT>::N];
     Vec<ELT>::unpack(load_row_vec<ELT>(row, V, shift, v), z);
-    for (int e = 0; e < Vec<ELT>::N; ++e) s += fast_exp2(__fmul_rn(__fsub_rn(z[e], M), c));
+    float part = 0.f;
+    for (int e = 0; e < Vec<ELT>::N; ++e) part += fast_exp2(__fmul_rn(__fsub_rn(z[e], M), c));
+    s += part;
   }
   s = warp_sum(s);
   __syncthreads();
@@ -467,7 +476,7 @@ __global__ void __launch_bounds__(kTopThreads, 4) top_kernel(const __grid_consta
     // (a base that follows only where terms would pass 2^24 is 1 % faster, but
     // the largest terms' exponents then lose four bits)
     if (vm > m) {
-      const float kn = fmaxf(__fmul_rn(vm, P.c2), -FLT_MAX);
+      const float kn = top_base(vm, P.c2);
       const float f = m > -INFINITY ? fast_exp2(__fsub_rn(k0, kn)) : 0.f;
       s2 = mul2(s2, pack2(f, f));
       m = vm;
@@ -562,7 +571,7 @@ __global__ void __launch_bounds__(kTopThreads, 4) top_kernel(const __grid_consta
   // a NaN is carried by the maximum
   float wm = from_ordered_key(__reduce_max_sync(0xffffffffu, ordered_key(m)));
   if (__any_sync(0xffffffffu, s != s)) wm = NAN;
-  const float ws = warp_sum(m > -INFINITY ? s * fast_exp2(__fsub_rn(k0, top_scale(wm, P.c2))) : 0.f);
+  const float ws = warp_sum(m > -INFINITY ? s * fast_exp2(__fsub_rn(k0, top_base(wm, P.c2))) : 0.f);
   if (lane == 0) sh.wm[warp] = wm, sh.ws[warp] = ws;
   __syncthreads();
   if (ctas > 1) cluster_wait();        // the first CTA's counters are set
@@ -573,7 +582,7 @@ __global__ void __launch_bounds__(kTopThreads, 4) top_kernel(const __grid_consta
     float M = lm;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) M = fmax_nan(M, __shfl_xor_sync(0xffffffffu, M, o));
-    const float S = warp_sum(lm > -INFINITY ? sh.ws[lane] * fast_exp2(__fsub_rn(top_scale(lm, P.c2), top_scale(M, P.c2))) : 0.f);
+    const float S = warp_sum(lm > -INFINITY ? sh.ws[lane] * fast_exp2(__fsub_rn(top_base(lm, P.c2), top_base(M, P.c2))) : 0.f);
     if (lane == 0) {
       first_store(&sh.M[rank], M);
       first_store(&sh.S[rank], S);
@@ -670,11 +679,14 @@ __global__ void __launch_bounds__(kTopThreads, 4) top_kernel(const __grid_consta
     for (int c = 1; c < ctas; ++c) M = fmax_nan(M, sh.M[c]), t_min = fminf(t_min, sh.t[c]), t_max = fmaxf(t_max, sh.t[c]);
     S = 0.f;
     for (int c = 0; c < ctas; ++c)
-      if (sh.M[c] > -INFINITY) S += sh.S[c] * fast_exp2(__fsub_rn(top_scale(sh.M[c], P.c2), top_scale(M, P.c2)));
+      if (sh.M[c] > -INFINITY) S += sh.S[c] * fast_exp2(__fsub_rn(top_base(sh.M[c], P.c2), top_base(M, P.c2)));
   }
-  if (S == 0.f && isfinite(M)) S = sum_again<ELT>(sh, row, P.V, M, P.c2);
+  const bool far = top_far(M, P.c2);
+  if (far && isfinite(M)) S = sum_again<ELT>(sh, row, P.V, M, P.c2);
   const bool valid = S > 0.f && isfinite(S) && isfinite(M);   // not NaN, +inf, or nothing but -inf
-  const float L = __fmaf_rn(0.6931471805599453f, top_residue(M, P.c2), logf(S));
+  // ln S and ln 2 (K0 - M c)
+  const float K0 = __fmul_rn(M, P.c2), residue = far ? 0.f : -__fmaf_rn(M, P.c2, -K0);
+  const float L = __fmaf_rn(0.6931471805599453f, residue, logf(S));
   int listed = 0, n_ranked = 0;        // entries of the list, and those that are ranked for it
   const key64* from = tokens;
   if (valid) {

@@ -156,6 +156,81 @@ def test_top_of_masked_and_invalid_rows(V, dtype):
         check_top(z, K)
 
 
+# Rows far from 0.  The sum is of 2^((z - M) c) at any level, so the bounds at
+# the head of this file hold; a value that passes float32's range is infinite.
+LEVELS = [x * s for x in (1e6, 2e7, 1e8, 1e9, 1e10, 1e12, 1e30, 2.4e38, 3e38) for s in (1.0, -1.0)] + ["lowest"]
+
+
+def rows_at(level, V, dtype):
+    """[7, V]: rows of one level, of levels near it, and with ordinary logits
+    beside it."""
+    at = torch.finfo(dtype).min if level == "lowest" else level
+    r = torch.arange(V, dtype=torch.float32)
+    z = randn(7, V, seed=V, dtype=dtype)
+    z[0] = at                                                # everything
+    z[1, V // 3] = at                                        # one token: forced, or alone masked
+    z[2, V // 4:V // 2] = at                                 # a block
+    z[3] = at if level == "lowest" else (at * (1 + (r * 7 % 13).floor() / 128)).to(dtype)
+    z[4] = at                                                # all but a few, as behind a narrow mask
+    few = (torch.arange(5) * 2357 + 11) % V
+    z[4, few] = randn(5, seed=8, dtype=dtype)
+    z[5] = torch.finfo(dtype).min if abs(at) < 1e31 else 0.0  # a token at that level, the rest masked
+    z[5, V - 1] = at
+    z[6] = -INF
+    z[6, ::2] = at
+    return z
+
+
+def check_top_rows(z, K, T, times=1):
+    """Rows [n, V], `times` times over in one call, against the definition rounded to float32."""
+    n, V = z.shape
+    ids, logp, lse = (x.cpu().numpy() for x in svp.kd_top(z.repeat(times, 1)[:, None].to(DEV), K, T))
+    for i in range(n):
+        x = z[i].double().numpy()
+        m = x.max()
+        log_sum = math.log(np.exp((x - m) / T).sum())
+        order = np.argsort(-x, kind="stable")[:K]
+        kept = x[order] > -np.inf
+        want_ids = np.concatenate([np.where(kept, order, -1), np.full(K - len(order), -1)])
+        want = np.concatenate([np.where(kept, (x[order] - m) / T - log_sum, -np.inf), np.full(K - len(order), -np.inf)])
+        for j in range(i, n * times, n):
+            assert np.array_equal(ids[j, 0], want_ids), (i, j)
+            with np.errstate(over="ignore"):
+                for got, ref in ((logp[j, 0], want), (lse[j], np.array([m / T + log_sum]))):
+                    near = np.isfinite(ref.astype(np.float32)) & np.isfinite(got)
+                    same = got == ref.astype(np.float32)
+                    off = np.abs(np.where(near, got.astype(np.float64) - np.where(near, ref, 0), 0))
+                    assert (same | near).all() and (off <= 1e-5 + 5e-7 * np.abs(np.where(near, ref, 0))).all(), (i, j, got[:4], ref[:4])
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("T", [0.6, 0.7, 0.8, 1.0, 1.3, 1.5, 2.0, 4.0])
+def test_top_of_rows_at_any_level(T, dtype):
+    for V in (50, 1003, 20001):
+        for level in LEVELS:
+            check_top_rows(rows_at(level, V, dtype), 20, T)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("T,level", [(0.6, -1e9), (0.8, -1e10), (1.0, -1e30), (1.0, 1e10), (1.0, 3e38), (1.5, "lowest"),
+                                     (1.5, -1e30), (4.0, "lowest"), (2.0, -1e12)])
+def test_top_of_long_rows_at_any_level(T, level, dtype):
+    z = rows_at(level, 140001, dtype)
+    check_top_rows(z, 20, T)                 # a cluster of 8 CTAs to a row
+    check_top_rows(z, 200, T, times=4)       # of 4
+    check_top_rows(z, 64, T, times=24)       # a CTA to a row
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_top_of_invalid_rows_at_any_level(dtype):
+    for V in (50, 20001, 140001):
+        z = torch.stack([torch.full((V,), x) for x in (1e10, -1e30, 3e38, -3e38, 0.0)]).to(dtype)
+        z[0, V // 2] = z[1, V - 1] = z[2, 0] = float("nan")
+        z[3, V // 3] = z[4, V - 1] = INF
+        ids, logp, lse = svp.kd_top(z[:, None].contiguous().to(DEV), 10)
+        assert (ids == -1).all() and logp.isnan().all() and lse.isnan().all()
+
+
 def test_top_rows_past_a_sequences_own_are_not_read():
     z = randn(5, 4, 2003, seed=4, dtype=torch.bfloat16)
     n = [0, 1, 4, 2, 9]
