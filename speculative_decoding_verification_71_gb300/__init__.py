@@ -537,7 +537,7 @@ def _launch(dev, stream, call):
 
 def process_logits(logits, history=None, prompt_len=None, history_len=None, tokens=None, draft_len=None,
                    repetition=None, presence=None, frequency=None, bias_ids=None, bias_values=None, mask=None,
-                   out=None, stream=None):
+                   out=None, stream=None, k=None):
     """Penalties, biases and grammar masks on logit rows (``sv_process_logits``
     in include/specverify.h): what a rollout applies to target or draft rows
     before ``SpecVerifier.verify``.
@@ -547,7 +547,10 @@ def process_logits(logits, history=None, prompt_len=None, history_len=None, toke
     strided), of which the first history_len [B] tokens count and the first
     prompt_len [B] of those are the prompt; tokens [B, k] int32 and draft_len
     [B] int32 with R = k + 1 (target rows) or R = k (draft rows), rows past
-    the drafts left alone; repetition, presence, frequency [B] float32;
+    the drafts left alone, and so is a sequence whose draft_len lies outside
+    [0, k].  ``k`` is taken from tokens; without tokens draft_len is read as
+    that of target rows, k = R - 1, so pass ``k=R`` for draft rows.
+    repetition, presence, frequency [B] float32;
     bias_ids [B, M] int32 with bias_values [B, M] float32; mask
     [B, R, ceil(V / 32)] int32, a set bit allows its token.  ``out=logits``
     works in place; without ``out`` the result is a new tensor (whose rows
@@ -555,7 +558,7 @@ def process_logits(logits, history=None, prompt_len=None, history_len=None, toke
     lib = load_library()
     (B, R, V), dev, code = _logit_rows("logits", logits)
     i32, f32 = torch.int32, torch.float32
-    H = stride = k = M = 0
+    H = stride = M = 0
     history_at = None
     if history is not None:
         if not isinstance(history, torch.Tensor):
@@ -573,12 +576,17 @@ def process_logits(logits, history=None, prompt_len=None, history_len=None, toke
         history_at = history.data_ptr()
     elif prompt_len is not None or history_len is not None:
         raise ValueError("prompt_len and history_len describe a history")
+    if k is not None and type(k) is not int:
+        raise TypeError("k must be an int")
     if tokens is not None:
-        k = tokens.shape[1] if isinstance(tokens, torch.Tensor) and tokens.dim() == 2 else R - 1
-        if R != k and R != k + 1:
-            raise ValueError(f"{R} rows for {k} drafts: expected {k} or {k + 1}")
-    elif draft_len is not None:
-        k = R - 1
+        n = tokens.shape[1] if isinstance(tokens, torch.Tensor) and tokens.dim() == 2 else R - 1
+        if k is not None and k != n:
+            raise ValueError(f"k is {k}, tokens hold {n} drafts")
+        k = n
+    if k is None:
+        k = R - 1 if draft_len is not None else 0
+    elif k < 0 or R != k and R != k + 1:
+        raise ValueError(f"{R} rows for {k} drafts: expected {k} or {k + 1}")
     if (bias_ids is None) != (bias_values is None):
         raise ValueError("bias_ids and bias_values go together")
     if bias_ids is not None:

@@ -193,6 +193,49 @@ def test_draft_rows(dtype):
     check(logits(B, k, V, dtype, 6), a, k)
 
 
+@pytest.mark.parametrize("in_place", [False, True], ids=["apart", "in_place"])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_draft_rows_without_drafts(dtype, in_place):
+    # a mask and biases on draft rows, full drafts among them, before any is drawn
+    B, k, V = 6, 4, 3001
+    a = rules(B, k, k, V, seed=55, drafts=False, penalties=False, n_bias=4, mask=0.6)
+    a["draft_len"] = torch.tensor([k, 0, 1, k, k - 1, 2], dtype=torch.int32)
+    z = logits(B, k, V, dtype, 56)
+    dev = z.to(DEV)
+    out = dev if in_place else torch.full_like(dev, -77.0)
+    svp.process_logits(dev, out=out, k=k, **gpu(a))
+    got, (ref, mag, kind) = out.cpu(), reference(z, a, k)
+    close(got, z, ref, mag, kind)
+    left = torch.from_numpy(kind[:, :, 0] == 2)
+    assert left.sum() == 4 + 3 + 1 + 2 and torch.equal(got[left], z[left] if in_place else torch.full_like(z, -77.0)[left])
+
+
+def test_target_rows_without_drafts():
+    B, k, V = 4, 3, 700
+    a = rules(B, k + 1, k, V, seed=57, drafts=False, H=30, mask=0.6)
+    a["draft_len"] = torch.tensor([k, 0, k + 1, 2], dtype=torch.int32)    # one is out of range
+    z = logits(B, k + 1, V, torch.float32, 58)
+    got = check(z, a, k)
+    said = svp.process_logits(z.to(DEV), k=k, out=torch.full_like(z, -77.0, device=DEV), **gpu(a))
+    assert torch.equal(said.cpu(), got)
+
+
+def test_k_has_to_fit_the_rows_and_the_drafts():
+    z = torch.zeros(2, 3, 64, device=DEV)
+    i32 = lambda *s: torch.zeros(*s, dtype=torch.int32, device=DEV)
+    for k in (0, 1, 4, -1):
+        with pytest.raises(ValueError):
+            svp.process_logits(z, draft_len=i32(2), k=k)
+        with pytest.raises(ValueError):
+            svp.process_logits(z, k=k)
+    with pytest.raises(ValueError):
+        svp.process_logits(z, tokens=i32(2, 2), k=3)               # tokens says two
+    for k in (2.0, True, "2"):
+        with pytest.raises(TypeError):
+            svp.process_logits(z, draft_len=i32(2), k=k)
+    assert svp.process_logits(z, tokens=i32(2, 3), draft_len=i32(2), k=3).shape == z.shape
+
+
 @pytest.mark.parametrize("shift,out_shift", [(1, 0), (3, 0), (0, 1), (5, 2)])
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_bases_off_the_16_byte_boundary(dtype, shift, out_shift):
