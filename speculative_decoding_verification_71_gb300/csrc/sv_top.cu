@@ -751,7 +751,11 @@ __global__ void __launch_bounds__(kTopThreads, 4) top_kernel(const __grid_consta
   if (to < listed) {
     const float z = key_value(static_cast<uint32_t>(mine >> 32));
     ids[to] = static_cast<int>(~static_cast<uint32_t>(mine));
-    logp[to] = __fsub_rn(__fdiv_rn(__fsub_rn(z, M), P.T), L);
+    // (the lowest values below a maximum of 1e32 and more: a difference past the
+    // range, of which a T above 1 may leave a number)
+    const float d = __fsub_rn(z, M);
+    const float at = d > -INFINITY ? __fdiv_rn(d, P.T) : __fsub_rn(__fdiv_rn(z, P.T), __fdiv_rn(M, P.T));
+    logp[to] = __fsub_rn(at, L);
   }
   for (int j = listed + tid; j < P.K; j += kTopThreads) ids[j] = -1, logp[j] = valid ? -INFINITY : NAN;
   if (tid == 0) P.lse[r] = valid ? __fadd_rn(__fdiv_rn(M, P.T), L) : M == -INFINITY ? -INFINITY : NAN;

@@ -222,6 +222,18 @@ def test_top_of_long_rows_at_any_level(T, level, dtype):
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("T", [1.0, 1.7, 2.0, 4.0, 100.0])
+def test_top_of_rows_as_wide_as_the_type(T, dtype):
+    # z - M passes the range, (z - M) / T need not
+    for V in (9, 3000):
+        z = torch.zeros(3, V, dtype=dtype)
+        z[0], z[0, 2] = torch.finfo(dtype).min, 3e38
+        z[1, ::2], z[1, 1::2] = -2e38, 2e38
+        z[2, 0], z[2, 1] = torch.finfo(dtype).max, torch.finfo(dtype).min
+        check_top_rows(z, 9, T)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_top_of_invalid_rows_at_any_level(dtype):
     for V in (50, 20001, 140001):
         z = torch.stack([torch.full((V,), x) for x in (1e10, -1e30, 3e38, -3e38, 0.0)]).to(dtype)
