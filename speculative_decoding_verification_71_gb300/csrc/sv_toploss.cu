@@ -78,6 +78,13 @@ struct TlRow {
   int valid;
 };
 
+// (z - m) / T: by difference, as the logits may be large and alike; apart where
+// the difference passes the range, which a T above 1 may undo.
+__device__ __forceinline__ float tl_below(float z, float m, float inv_T) {
+  const float d = __fsub_rn(z, m);
+  return d > -INFINITY ? __fmul_rn(d, inv_T) : __fsub_rn(__fmul_rn(z, inv_T), __fmul_rn(m, inv_T));
+}
+
 // The parts of all lanes on their common maxima, the same in every lane and in
 // a fixed order; a NaN among the sums stays.
 __device__ __forceinline__ TlPart tl_combine(const TlPart& p, float c2, float inv_T) {
@@ -96,7 +103,7 @@ __device__ __forceinline__ TlRow tl_row(const TlPart& part, double mass, float s
   R.Ma = fmaxf(part.m, part.ml);
   R.valid = part.s == part.s && R.Ma > -INFINITY && R.Ma < INFINITY;
   // the listed tokens carry most of Z: full-precision exponentials for them
-  const float lt = __fmul_rn(__fsub_rn(part.m, R.Ma), P.inv_T);
+  const float lt = tl_below(part.m, R.Ma, P.inv_T);
   const float ft = part.m > -INFINITY ? expf(lt) : 0.f;
   const float fl = part.ml > -INFINITY ? expf(__fmul_rn(__fsub_rn(part.ml, R.Ma), P.inv_T)) : 0.f;
   const float tail = __fmul_rn(part.s, ft);   // of Z
@@ -511,7 +518,7 @@ __global__ void __launch_bounds__(kTrThreads, kTrCtas) toploss_kernel(const __gr
     }
 
     // ---- the listed tokens: their gradients after the row's, and the divergence
-    const float lj = __fmul_rn(__fsub_rn(zj, R.Ma), P.inv_T);
+    const float lj = tl_below(zj, R.Ma, P.inv_T);
     if (P.renorm) {
       lp = R.mass > 0.f ? __fsub_rn(lp, logf(R.mass)) : -INFINITY;
       p = R.mass > 0.f ? __fdiv_rn(p, R.mass) : 0.f;
@@ -656,7 +663,7 @@ __global__ void __launch_bounds__(kTsThreads, U > 4 ? 3 : 4) toploss_short_kerne
       else if (v < nvec) store_edge<ELT>(grad, P.V, t0, P.same_shift, VT::pack(g));
     }
   }
-  const float lj = __fmul_rn(__fsub_rn(zj, R.Ma), P.inv_T);
+  const float lj = tl_below(zj, R.Ma, P.inv_T);
   if (P.renorm) {
     lp = R.mass > 0.f ? __fsub_rn(lp, logf(R.mass)) : -INFINITY;
     p = R.mass > 0.f ? __fdiv_rn(p, R.mass) : 0.f;

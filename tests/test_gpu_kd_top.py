@@ -450,6 +450,40 @@ def test_loss_of_unusual_rows(V, dtype, tail):
     check_loss(ids, lp, z, w, 1.0, tail)
 
 
+@pytest.mark.parametrize("tail", [True, False], ids=["tail", "renorm"])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("V", [60, 40001])
+def test_loss_of_rows_as_wide_as_the_type(V, dtype, tail):
+    # a draft logit and the row's maximum whose difference passes the range,
+    # which a T above 1 brings back into it
+    T, K = 8.0, 6
+    ids, lp, z, w = pair(4, 1, V, dtype, K, T, seed=130)
+    low = torch.finfo(dtype).min
+    z[0], z[0, 0, int(ids[0, 0, 0])] = low, 3e38          # one listed token, the rest far below
+    z[1, 0, int(ids[1, 0, 1])] = low                      # a listed token far below an unlisted one
+    z[1, 0, next(x for x in range(V) if x not in ids[1, 0].tolist())] = 3e38
+    z[2, 0, int(ids[2, 0, 0])], z[2, 0, int(ids[2, 0, 1])] = -2e38, 2e38
+    kl, _, grad = (x.cpu().double().numpy() for x in svp.kd_top_loss(ids.to(DEV), lp.to(DEV), z.to(DEV), w.to(DEV), T, tail=tail))
+    for b in range(4):
+        ref, _, tol, _ = loss_reference(ids[b, 0], lp[b, 0], z[b, 0], float(w[b]), T, tail)
+        assert math.isfinite(ref) and abs(kl[b, 0] - ref) <= tol, (b, kl[b, 0], ref, tol)
+        # the others' shares about their own maximum: log q of -1e38 has no digits left for them
+        x, v = ids[b, 0].numpy(), z[b, 0].double().numpy()
+        p = np.exp(lp[b, 0].double().numpy())
+        r = 1 - p.sum() if tail else 0.0
+        p = p if tail else p / p.sum()
+        q, share = np.exp((v - v.max()) / T), np.exp(np.minimum(v - np.delete(v, x).max(), 0) / T)
+        q, share[x] = q / q.sum(), 0.0
+        share /= share.sum()
+        want, bound = q - r * share, 1e-5 * (q + r * share) + 2e-6 * share
+        want[x] -= p
+        bound[x] += 1e-5 * p
+        if dtype == torch.bfloat16:
+            bound = bound + np.abs(want) * 2.0 ** -7
+        s = float(w[b]) / T
+        assert (np.abs(grad[b, 0] - s * want) <= s * bound + 1e-30).all(), (b, (np.abs(grad[b, 0] - s * want) - s * bound).max())
+
+
 def test_rows_without_a_list_are_not_read():
     ids, lp, z, w = pair(4, 3, 2001, torch.bfloat16, 10, 1.0, seed=60)
     for b, n in enumerate((0, 1, 2, 3)):
