@@ -410,15 +410,26 @@ sv_status spec_kd_top(int n_seq, int t_len, int V, sv_dtype dtype, const void *t
  * -inf, an id >= V or one listed twice give a NaN KL, NaN gradient and NaN
  * loss for the rollout; a listed token with p_j > 0 (or, with r > 0, all
  * others) at draft logit -inf gives KL = +inf.  K and the rows as for
- * spec_kd_top, V * sizeof(dtype) <= 1 MiB.  Asynchronous on `stream`; no context, no workspace, no
- * allocation; every sum is taken in a fixed order.  Host-checkable errors
- * return SV_ERR_INVALID_ARG and launch nothing. */
+ * spec_kd_top, V * sizeof(dtype) <= 1 MiB.  Asynchronous on `stream`; no
+ * context, no workspace, no allocation; every sum is taken in a fixed order.
+ * A wait for staged logits that lasts longer than 1 s is given up.  There is
+ * no status for it: the row's KL, its gradients not yet taken and every later
+ * row (with a list) of the CTAs concerned are NaN, and so are the losses of
+ * their rollouts; no copy is left in flight and the next call is not
+ * affected.  Host-checkable errors return SV_ERR_INVALID_ARG and launch
+ * nothing. */
 typedef enum { SV_KD_TOP_TAIL = 0, SV_KD_TOP_RENORM = 1 } sv_kd_top_mode;
 
 sv_status spec_kd_top_loss(int n_seq, int t_len, int V, sv_dtype dtype, int K, const int32_t *ids,
                            const float *logp, const void *draft_logits, const float *weights,
                            float temperature, int mode, float *row_kl, float *loss, void *grad,
                            sv_stream_t stream);
+
+/* Test hook: the limit, in nanoseconds, of spec_kd_top_loss's waits for staged
+ * logits, in the calls of the whole process from here on (default 1 s).  0
+ * makes every such wait report expiry; rows short enough to stay in registers
+ * (32 KB) have none.  Negative restores the default. */
+sv_status spec_kd_set_wait_limit_ns(long long ns);
 
 /* Test hook: the limit, in nanoseconds, of each bounded wait for staged logits
  * (default 1 s).  0 makes every wait report expiry, so every sequence that

@@ -50,6 +50,7 @@ EXPORTED_SYMBOLS = (
     "spec_ctrl_create", "spec_ctrl_destroy", "spec_ctrl_set_cost", "spec_ctrl_set_params", "spec_ctrl_reset",
     "spec_ctrl_observe", "spec_ctrl_choose", "spec_ctrl_alpha", "spec_ctrl_status",
     "spec_verify_tree", "sv_process_logits", "spec_kd_top", "spec_kd_top_loss",
+    "spec_kd_set_wait_limit_ns",
 )
 
 
@@ -166,6 +167,8 @@ def load_library(path: str | None = None):
     lib.spec_kd_top_loss.restype = c.c_int
     lib.spec_kd_top_loss.argtypes = [c.c_int, c.c_int, c.c_int, c.c_int, c.c_int, P, P, P, P, c.c_float, c.c_int,
                                      P, P, P, P]
+    lib.spec_kd_set_wait_limit_ns.restype = c.c_int
+    lib.spec_kd_set_wait_limit_ns.argtypes = [c.c_longlong]
     lib.spec_verify_noalloc.restype = c.c_int
     lib.spec_verify_noalloc.argtypes = [c.c_int, c.c_int, c.c_int, c.c_int, P, P, P, P, P, c.c_float, P, P, P]
     if path is None:

@@ -7,6 +7,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <climits>
 #include <cmath>
 #include <cstdio>
@@ -15,6 +16,13 @@
 
 #include "../../include/specverify.h"
 #include "sv_internal.h"
+
+namespace sv {
+namespace {
+std::atomic<long long> g_kd_wait_limit_ns{kDrainLimitNs};
+}
+long long kd_wait_limit_ns() { return g_kd_wait_limit_ns.load(std::memory_order_relaxed); }
+}  // namespace sv
 
 struct sv_ctx {
   int max_B = 0, max_k = 0, V = 0;
@@ -510,6 +518,11 @@ sv_status sv_kernel_for(const sv_ctx* ctx, int B, int* kernel) {
 sv_status sv_set_wait_limit_ns(sv_ctx* ctx, long long ns) {
   if (!ctx) return SV_ERR_INVALID_ARG;
   ctx->wait_limit_ns = ns < 0 ? sv::kDrainLimitNs : ns;
+  return SV_OK;
+}
+
+sv_status spec_kd_set_wait_limit_ns(long long ns) {
+  sv::g_kd_wait_limit_ns.store(ns < 0 ? sv::kDrainLimitNs : ns, std::memory_order_relaxed);
   return SV_OK;
 }
 

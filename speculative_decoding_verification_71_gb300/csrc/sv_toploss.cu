@@ -26,6 +26,14 @@
 // a cluster exchange nothing but their (M, S), through distributed shared
 // memory; the listed tokens' gradients are stored after the row's.
 //
+// Every wait has a limit.  A consumer warp whose wait for a slot expires touches
+// no barrier of the ring again: its sums and gradients are NaN from there on, so
+// that every later row of its cluster is, and the row itself is set to NaN at the
+// end (its numbers may have been put together before).  The CTAs of a cluster go
+// on exchanging parts.  The producer, which then waits in vain for the slots'
+// release, leaves last, when its copies have landed: none is to reach shared
+// memory that a later CTA owns.
+//
 // 4096 rows of 151936 bf16 logits with their gradients: 455 us, 5.5 TB/s of
 // each logit read and each gradient written once; the loss alone 187 us, 6.7
 // TB/s.  With one CTA to a row the rows at work do not stay in L2 (452 MB read
@@ -62,6 +70,7 @@ struct TopLossParams {
   int renorm;
   int same_shift;              // draft and grad lie alike: 16-byte stores
   float c2, inv_T;             // log2(e) / T, 1 / T
+  long long wait_limit_ns;     // of a consumer's wait for a slot
 };
 
 // A part's sums: the unlisted tokens' about their maximum m, the listed ones'
@@ -171,6 +180,9 @@ constexpr int kTrHash = 1024;                         // places for a row's list
 constexpr int kTrGrid = 152 * kTrCtas;                // CTAs that fit at once
 constexpr long long kTrInL2 = 72LL << 20;             // bytes of rows at work that L2 keeps
 constexpr int kTrMinPart = 16 * 1024;                 // a part's bytes where a row is split for want of rows
+// A CTA's parts come within two expired waits for its slots.
+constexpr long long kTrJoinLimitNs = 4 * kDrainLimitNs;
+constexpr int kTrNoRow = 0x7fffffff;
 
 struct TrShared {
   uint64_t full[kTrSlots], ready[kTrSlots], empty[kTrSlots];
@@ -180,6 +192,7 @@ struct TrShared {
   double mass[2][kTrWarps];      // P in 64 bits: 1 - P keeps what the log-probabilities have
   float term[2][kTrWarps];
   TlRow row[2];
+  int failed;                    // the first row in which a wait expired, or kTrNoRow
   int ids[kTrHash];              // open addressing; -1: empty
 };
 constexpr int kTrRingAt = (static_cast<int>(sizeof(TrShared)) + 127) / 128 * 128;
@@ -249,6 +262,7 @@ __global__ void __launch_bounds__(kTrThreads, kTrCtas) toploss_kernel(const __gr
       mbar_init(&sh.ready[s], 1);
       mbar_init(&sh.empty[s], kTrWarps + 1);
     }
+    sh.failed = kTrNoRow;
     fence_mbar_init();
   }
   for (int w = tid; w < kTrHash; w += kTrThreads) sh.ids[w] = -1;
@@ -260,15 +274,19 @@ __global__ void __launch_bounds__(kTrThreads, kTrCtas) toploss_kernel(const __gr
     // ---- the producer: every row with a list once, for the gradient twice
     const uint64_t first_out = evict_first_policy();
     unsigned q = 0;
-    for (long long r = cluster; r < rows; r += clusters) {
+    bool given_up = false;
+    for (long long r = cluster; r < rows && !given_up; r += clusters) {
       if (!tr_has_list(P, r, lane)) continue;
       const TrRow row = TrRow::of<ELT>(P, r, ctas, rank);
-      for (int pass = 0; pass < (GRAD ? 2 : 1); ++pass)
+      for (int pass = 0; pass < (GRAD ? 2 : 1) && !given_up; ++pass)
         for (int v = 0; v < row.n; v += kTrSlotVecs, ++q) {
           const int s = q % kTrSlots;
           int ok = 1;
           if (lane == 0) ok = mbar_wait_bounded(&sh.empty[s], ((q / kTrSlots) & 1) ^ 1, kDrainLimitNs) ? 1 : 0;
-          if (!__shfl_sync(0xffffffffu, ok, 0)) return;   // the consumers give up as well
+          if (!__shfl_sync(0xffffffffu, ok, 0)) {
+            given_up = true;             // as a consumer or the marking warp has
+            break;
+          }
           if (lane == 0) {
             const uint32_t bytes = static_cast<uint32_t>(min(kTrSlotVecs, row.n - v)) * 16u;
             const unsigned char* src = row.at + static_cast<long long>(v) * 16;
@@ -279,6 +297,10 @@ __global__ void __launch_bounds__(kTrThreads, kTrCtas) toploss_kernel(const __gr
           }
         }
     }
+    // the last copy of every slot has landed, whether it was waited for or not
+    if (lane == 0)
+      for (unsigned i = q > kTrSlots ? q - kTrSlots : 0; i < q; ++i)
+        mbar_wait_bounded(&sh.full[i % kTrSlots], (i / kTrSlots) & 1u, kDrainLimitNs);
     return;
   }
 
@@ -322,17 +344,23 @@ __global__ void __launch_bounds__(kTrThreads, kTrCtas) toploss_kernel(const __gr
   // ---- the consumers
   const f2 cc = pack2(P.c2, P.c2);
   unsigned q = 0;
-  bool dead = false;             // a wait has expired: every row from then on is NaN
-  int turn = 0;
+  bool dead = false;             // a wait of this warp has expired: what it adds is NaN
+  bool alone = false;            // (warp 0) the others' parts did not come
+  int turn = 0, alone_turn = 0;
   // this lane's vectors of the slot, -inf past the row's; the slot is released
   // as soon as they are in registers
-  auto take = [&](uint4 (&w)[kTrPerLane], int n, bool marked) {
+  auto take = [&](uint4 (&w)[kTrPerLane], int n, bool marked, long long r) {
     const int s = q % kTrSlots;
     const uint32_t phase = (q / kTrSlots) & 1u;
-    bool ok = !dead && mbar_wait_bounded(&sh.full[s], phase, kDrainLimitNs);
-    if (marked) ok = ok && mbar_wait_bounded(&sh.ready[s], phase, kDrainLimitNs);
-    dead = !__all_sync(0xffffffffu, ok);
+    ++q;
+    if (!dead) {
+      bool ok = mbar_wait_bounded(&sh.full[s], phase, P.wait_limit_ns);
+      if (marked) ok = ok && mbar_wait_bounded(&sh.ready[s], phase, P.wait_limit_ns);
+      dead = !__all_sync(0xffffffffu, ok);
+      if (dead && lane == 0) atomicMin(&sh.failed, static_cast<int>(r));
+    }
     const uint4* src = reinterpret_cast<const uint4*>(ring + s * kTrSlotVecs * 16) + tid;
+    if (dead) n = 0;
     if (n >= kTrSlotVecs) {
 #pragma unroll
       for (int k = 0; k < kTrPerLane; ++k) w[k] = src[k * kTrConsumers];
@@ -341,8 +369,7 @@ __global__ void __launch_bounds__(kTrThreads, kTrCtas) toploss_kernel(const __gr
       for (int k = 0; k < kTrPerLane; ++k) w[k] = tid + k * kTrConsumers < n ? src[k * kTrConsumers] : VT::neg_inf();
     }
     __syncwarp();
-    if (lane == 0) mbar_arrive(&sh.empty[s]);
-    ++q;
+    if (lane == 0 && !dead) mbar_arrive(&sh.empty[s]);
   };
   // the next row's list is loaded while this one is at work
   int next_id = -1;
@@ -427,7 +454,7 @@ __global__ void __launch_bounds__(kTrThreads, kTrCtas) toploss_kernel(const __gr
     if (end >= 0) end_vec = load_row_vec<ELT>(start, P.V, shift, end);
     for (int v = 0; v < row.n; v += kTrSlotVecs) {
       uint4 w[kTrPerLane];
-      take(w, row.n - v, true);
+      take(w, row.n - v, true, r);
       if (row.n - v > kTrSlotVecs / 2) {
         add(w);
       } else {   // a last slot of half the vectors at most (10000 rows of 20000: 245 us, as a whole one 250)
@@ -463,21 +490,29 @@ __global__ void __launch_bounds__(kTrThreads, kTrCtas) toploss_kernel(const __gr
       const TlPart none{-INFINITY, 0.f, -INFINITY, 0.f};
       part = tl_combine(lane < kTrWarps ? sh.warp[par][lane] : none, P.c2, P.inv_T);
       if (ctas > 1) {
-        if (lane == 0) mbar_expect_tx(&sh.joined[par], static_cast<uint32_t>(ctas) * 16u);
-        if (lane < ctas)
-          st_async(peer(&sh.part[par][rank], lane), make_uint4(__float_as_uint(part.m), __float_as_uint(part.s), 0u, 0u),
-                   peer(&sh.joined[par], lane));
-        const bool ok = !dead && mbar_wait_bounded(&sh.joined[par], static_cast<uint32_t>(phase), kDrainLimitNs);
-        dead = !__all_sync(0xffffffffu, ok);
         TlPart other = none;
-        if (lane < ctas && !dead) {
-          const uint4 x = sh.part[par][lane];
-          other.m = __uint_as_float(x.x);
-          other.s = __uint_as_float(x.y);
+        if (!alone) {
+          if (lane == 0) mbar_expect_tx(&sh.joined[par], static_cast<uint32_t>(ctas) * 16u);
+          if (lane < ctas)
+            st_async(peer(&sh.part[par][rank], lane), make_uint4(__float_as_uint(part.m), __float_as_uint(part.s), 0u, 0u),
+                     peer(&sh.joined[par], lane));
+          alone = !__all_sync(0xffffffffu, mbar_wait_bounded(&sh.joined[par], static_cast<uint32_t>(phase), kTrJoinLimitNs));
+          if (alone && lane == 0) {
+            // another CTA may still get here and on to the next row, where it
+            // waits in vain: what it sends until then is waited for at the end
+            mbar_expect_tx(&sh.joined[par ^ 1], static_cast<uint32_t>(ctas) * 16u);
+            atomicMin(&sh.failed, static_cast<int>(r));
+          }
+          if (alone) alone_turn = turn - 1;
+          if (lane < ctas && !alone) {
+            const uint4 x = sh.part[par][lane];
+            other.m = __uint_as_float(x.x);
+            other.s = __uint_as_float(x.y);
+          }
         }
         other = tl_combine(other, P.c2, P.inv_T);
         part.m = other.m;
-        part.s = dead ? NAN : other.s;
+        part.s = alone ? NAN : other.s;
       }
       mass = sh.mass[par][lane % kTrWarps];
 #pragma unroll
@@ -490,7 +525,8 @@ __global__ void __launch_bounds__(kTrThreads, kTrCtas) toploss_kernel(const __gr
 
     // ---- the gradient
     if (GRAD) {
-      const f2 bb = pack2(R.base, R.base), aa = pack2(R.a, R.a);
+      const f2 bb = pack2(R.base, R.base);
+      f2 aa = pack2(R.a, R.a);
       auto gradient = [&](const uint4& x) {
         f2 z[N / 2];
         float g[N];
@@ -502,7 +538,8 @@ __global__ void __launch_bounds__(kTrThreads, kTrCtas) toploss_kernel(const __gr
       unsigned char* out = grad + (static_cast<long long>(row.first) * N - shift) * ELT;
       for (int v = 0; v < row.n; v += kTrSlotVecs) {
         uint4 w[kTrPerLane];
-        take(w, row.n - v, false);
+        take(w, row.n - v, false, r);
+        if (dead) aa = pack2(NAN, NAN);
         unsigned char* at = out + static_cast<long long>(v + tid) * 16;
         if (P.same_shift && row.n - v >= kTrSlotVecs) {
 #pragma unroll
@@ -540,7 +577,16 @@ __global__ void __launch_bounds__(kTrThreads, kTrCtas) toploss_kernel(const __gr
       P.row_kl[r] = valid ? kl : NAN;
     }
   }
-  if (ctas > 1) cluster_sync();   // nothing is on its way to a CTA that has left
+  if (ctas > 1) {
+    cluster_sync();              // nothing will be sent to a CTA that has left, nor is it on its way:
+    if (alone)
+      for (int t = alone_turn; t < alone_turn + 2; ++t)
+        mbar_wait_bounded(&sh.joined[t & 1], static_cast<uint32_t>(t >> 1 & 1), kDrainLimitNs);
+  } else {
+    named_barrier_sync(1, kTrConsumers);
+  }
+  // the row in which a wait expired, its divergence perhaps stored before
+  if (tid == 0 && sh.failed != kTrNoRow) P.row_kl[sh.failed] = NAN;
 }
 
 // ---- short rows: a CTA to a row, which stays in its registers
@@ -791,7 +837,7 @@ extern "C" sv_status spec_kd_top_loss(int n_seq, int t_len, int V, sv_dtype dtyp
   if (!(c2 < 1e30)) return SV_ERR_INVALID_ARG;
   TopLossParams p{ids, logp, static_cast<const unsigned char*>(draft_logits), weights, row_kl,
                   static_cast<unsigned char*>(grad), t_len, V, K, mode == SV_KD_TOP_RENORM, (a % 16) == (g % 16),
-                  static_cast<float>(c2), 1.f / temperature};
+                  static_cast<float>(c2), 1.f / temperature, kd_wait_limit_ns()};
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   NvtxRange range("spec_kd_top_loss");
   const int rows = n_seq * t_len;

@@ -541,6 +541,57 @@ def test_loss_is_deterministic_and_stream_ordered():
         assert all(torch.equal(x, y) for x, y in zip(got, want))
 
 
+@pytest.fixture
+def wait_limit():
+    lib = svp.load_library()
+    yield lambda ns: lib.spec_kd_set_wait_limit_ns(ns)
+    lib.spec_kd_set_wait_limit_ns(-1)
+
+
+# rows of 8, 2 and 1 CTAs
+@pytest.mark.parametrize("n_seq,t_len,V,dtype", [(3, 5, 140001, torch.bfloat16), (50, 8, 140001, torch.bfloat16),
+                                                 (130, 3, 9001, torch.float32)])
+@pytest.mark.parametrize("grad", [True, False], ids=["grad", "loss"])
+def test_loss_where_every_wait_expires(n_seq, t_len, V, dtype, grad, wait_limit):
+    g = torch.Generator(device=DEV).manual_seed(140)
+    z = (torch.randn(n_seq, t_len, V, generator=g, device=DEV) * 3).to(dtype)
+    ids, lp, _ = svp.kd_top(z.flip(2).contiguous(), 12)
+    ids[1, 0], lp[1, 0] = -1, -INF                       # no list: nothing is waited for
+    w = torch.ones(n_seq, device=DEV)
+    want = svp.kd_top_loss(ids, lp, z, w, grad=grad)
+    wait_limit(0)
+    kl, loss, gr = svp.kd_top_loss(ids, lp, z, w, grad=grad)
+    wait_limit(-1)
+    again = svp.kd_top_loss(ids, lp, z, w, grad=grad)
+    torch.cuda.synchronize()
+    assert kl[1, 0] == 0 and loss.isnan().all()
+    kl[1, 0] = math.nan
+    assert kl.isnan().all()
+    if grad:
+        assert (gr[1, 0] == 0).all()
+        gr[1, 0] = math.nan
+        assert gr.isnan().all()
+    assert all(x is y is None or torch.equal(x, y) for x, y in zip(again, want))
+
+
+@pytest.mark.parametrize("ns", [1, 3000, 20000])
+@pytest.mark.parametrize("n_seq,t_len,V,dtype", [(3, 5, 140001, torch.bfloat16), (130, 3, 70001, torch.bfloat16)])
+def test_loss_where_some_waits_expire(n_seq, t_len, V, dtype, ns, wait_limit):
+    # which ones is not known; what is not NaN is right
+    g = torch.Generator(device=DEV).manual_seed(150)
+    z = (torch.randn(n_seq, t_len, V, generator=g, device=DEV) * 3).to(dtype)
+    ids, lp, _ = svp.kd_top(z.flip(2).contiguous(), 12)
+    w = torch.ones(n_seq, device=DEV)
+    want = svp.kd_top_loss(ids, lp, z, w)
+    wait_limit(ns)
+    kl, loss, gr = svp.kd_top_loss(ids, lp, z, w)
+    torch.cuda.synchronize()
+    assert (kl.isnan() | (kl == want[0])).all()
+    assert torch.equal(loss.isnan(), kl.isnan().any(1)) and (loss.isnan() | (loss == want[1])).all()
+    assert (gr.isnan() | (gr == want[2])).all()
+    assert not gr[~kl.isnan()].isnan().any()
+
+
 def test_captured_calls_replay():
     ids, lp, z, w = (x.to(DEV) for x in pair(2, 2, 3000, torch.float32, 16, 1.0, seed=110))
     want = svp.kd_top(z, 16) + svp.kd_top_loss(ids, lp, z, w)
