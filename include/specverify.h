@@ -296,7 +296,11 @@ sv_status sv_set_early_exit(sv_ctx *ctx, int on);
  * per SM takes whole row pairs; with the gradient each pair is streamed twice,
  * the second time from L2.  Rows whose V * sizeof(dtype) is a multiple of 16
  * with 16-byte aligned bases (and gradient) are staged with bulk copies,
- * others with plain loads.  Rows of more than 1 GiB are SV_ERR_INVALID_ARG. */
+ * others with plain loads.  A wait for staged logits that lasts longer than
+ * 1 s is given up.  There is no status for it: the row's KL, its gradients not
+ * yet taken and the CTA's later rows are NaN, and so are the losses of their
+ * rollouts; no copy is left in flight and the next call is not affected.
+ * Rows of more than 1 GiB are SV_ERR_INVALID_ARG. */
 sv_status spec_kd_loss(int n_seq, int t_len, int V, sv_dtype dtype, const void *target_logits,
                        const void *draft_logits, const float *weights, float temperature,
                        float *row_kl, float *loss, void *grad, sv_stream_t stream);
@@ -425,10 +429,11 @@ sv_status spec_kd_top_loss(int n_seq, int t_len, int V, sv_dtype dtype, int K, c
                            float temperature, int mode, float *row_kl, float *loss, void *grad,
                            sv_stream_t stream);
 
-/* Test hook: the limit, in nanoseconds, of spec_kd_top_loss's waits for staged
- * logits, in the calls of the whole process from here on (default 1 s).  0
- * makes every such wait report expiry; rows short enough to stay in registers
- * (32 KB) have none.  Negative restores the default. */
+/* Test hook: the limit, in nanoseconds, of spec_kd_loss's and
+ * spec_kd_top_loss's waits for staged logits, in the calls of the whole process
+ * from here on (default 1 s).  0 makes every such wait report expiry;
+ * spec_kd_top_loss's rows that stay in registers (32 KB) have none.  Negative
+ * restores the default. */
 sv_status spec_kd_set_wait_limit_ns(long long ns);
 
 /* Test hook: the limit, in nanoseconds, of each bounded wait for staged logits

@@ -25,6 +25,11 @@
 // the row in L2 (it was read a few microseconds before) and are marked first
 // out of it, and the gradient leaves with streaming stores.  Each logit
 // crosses HBM once and each gradient value once; no CTA waits for another.
+//
+// Every wait has a limit.  A consumer warp whose wait expires touches the ring
+// no more: its parts and gradients are NaN from there on, and with them the
+// CTA's later rows; the KL of the row itself, perhaps stored before, is set to
+// NaN at the end.  The producer leaves last, when its copies have landed.
 
 #include <cuda_runtime.h>
 
@@ -73,6 +78,7 @@ struct KdParams {
   float inv_T;
   int nchunks;                 // slots per row and pass: ceil(V * elt / kKdHalf)
   int bulk;                    // rows 16-byte aligned: cp.async.bulk; else plain loads
+  long long wait_limit_ns;     // of a consumer's wait for a slot
 };
 
 // A part's numbers rescaled onto the common maxima of the parts in lanes
@@ -151,10 +157,11 @@ struct KdRows {
     const uint64_t first_out = evict_first_policy();
     const int passes = GRAD ? 2 : 1;
     int q = 0;
-    for (int r = blockIdx.x; r < P.rows; r += gridDim.x) {
+    bool given_up = false;
+    for (int r = blockIdx.x; r < P.rows && !given_up; r += gridDim.x) {
       const unsigned char* rt = static_cast<const unsigned char*>(P.target) + static_cast<size_t>(r) * row_bytes;
       const unsigned char* rd = static_cast<const unsigned char*>(P.draft) + static_cast<size_t>(r) * row_bytes;
-      for (int pass = 0; pass < passes; ++pass) {
+      for (int pass = 0; pass < passes && !given_up; ++pass) {
         // a pass read again keeps its lines in L2; the last read of a row
         // marks them first out
         const bool last_read = pass == passes - 1;
@@ -164,7 +171,8 @@ struct KdRows {
           if (lane == 0) ok = mbar_wait_bounded(&C.empty[s], ((q / kKdStages) & 1) ^ 1, kDrainLimitNs) ? 1 : 0;
           if (!__shfl_sync(0xffffffffu, ok, 0)) {
             if (lane == 0) atomicOr(failed, 1u);
-            return;
+            given_up = true;
+            break;
           }
           const long long off = static_cast<long long>(c) * kKdHalf;
           const int bytes = chunk_bytes(c);
@@ -195,20 +203,21 @@ struct KdRows {
         }
       }
     }
+    // the last copy of every slot has landed, whether it was waited for or not
+    if (P.bulk && lane == 0)
+      for (int i = q > kKdStages ? q - kKdStages : 0; i < q; ++i)
+        mbar_wait_bounded(&C.full[i % kKdStages], static_cast<uint32_t>(i / kKdStages) & 1u, kDrainLimitNs);
   }
 
   // ---- consumer warps --------------------------------------------------------
 
   // This lane's vectors of slot s (target, draft), -inf past the chunk; the
-  // slot is released as soon as they are in registers.  False if the wait
-  // gave up (every later wait is then skipped: the rows turn NaN).
-  __device__ bool take(int s, int q, int c, bool& dead, uint4 (&tv)[kKdVecsPerLane], uint4 (&dv)[kKdVecsPerLane]) {
-    bool ok = !dead && mbar_wait_bounded(&C.full[s], static_cast<uint32_t>(q / kKdStages) & 1u, kDrainLimitNs);
+  // slot is released as soon as they are in registers.  Once a wait has given
+  // up (`dead`, in row `dead_row`) the ring is left alone and the vectors are NaN.
+  __device__ void take(int s, int q, int c, int r, bool& dead, int& dead_row, uint4 (&tv)[kKdVecsPerLane],
+                       uint4 (&dv)[kKdVecsPerLane]) {
+    bool ok = !dead && mbar_wait_bounded(&C.full[s], static_cast<uint32_t>(q / kKdStages) & 1u, P.wait_limit_ns);
     ok = __all_sync(0xffffffffu, ok);
-    if (!ok && !dead) {
-      dead = true;
-      if (lane == 0) atomicOr(failed, 2u);
-    }
     const int nvec = (chunk_bytes(c) + 15) / 16;
     const unsigned char* src = slot(s);
 #pragma unroll
@@ -218,9 +227,19 @@ struct KdRows {
       tv[j] = in ? *reinterpret_cast<const uint4*>(src + static_cast<size_t>(v) * 16) : V::neg_inf();
       dv[j] = in ? *reinterpret_cast<const uint4*>(src + kKdHalf + static_cast<size_t>(v) * 16) : V::neg_inf();
     }
+    if (!ok) {               // (a branch: with the vectors chosen above the gradients take 3 % longer)
+      if (!dead) {
+        dead = true;
+        dead_row = r;
+        if (lane == 0) atomicOr(failed, 2u);
+      }
+      const uint32_t x = 0x7fc07fc0u;   // NaN in either type
+#pragma unroll
+      for (int j = 0; j < kKdVecsPerLane; ++j) tv[j] = dv[j] = make_uint4(x, x, x, x);
+      return;
+    }
     __syncwarp();
     if (lane == 0) mbar_arrive(&C.empty[s]);
-    return ok;
   }
 
   __device__ void consume() {
@@ -228,14 +247,14 @@ struct KdRows {
     const f2 cc = pack2(c2, c2);
     int q = 0, row_i = 0;
     bool dead = false;
+    int dead_row = 0;
     for (int r = blockIdx.x; r < P.rows; r += gridDim.x, ++row_i) {
       // ---- first pass: per lane, running maxima and sums against K = fl(M c)
       float mt = -INFINITY, md = -INFINITY, kt = 0.f, kd = 0.f;
       f2 st2 = 0ull, sd2 = 0ull, a2 = 0ull, unused = 0ull;
-      bool lost = false;
       for (int c = 0; c < P.nchunks; ++c, ++q) {
         uint4 tv[kKdVecsPerLane], dv[kKdVecsPerLane];
-        if (!take(q % kKdStages, q, c, dead, tv, dv)) lost = true;
+        take(q % kKdStages, q, c, r, dead, dead_row, tv, dv);
         // NaN is passed over by the maxima and kept by the sums
         const float vt = V::vmax(tv), vd = V::vmax(dv);
         if (vt > mt) raise_max(vt, c2, mt, kt, st2, a2);
@@ -269,8 +288,8 @@ struct KdRows {
       unpack2(sd2, x0, x1); mine.sd = x0 + x1;
       // a NaN sum is carried by the maximum (a lane whose maximum stayed
       // -inf would otherwise drop it in the combine); so is a lost wait
-      mine.mt = (mine.st != mine.st || lost) ? NAN : mt;
-      mine.md = (mine.sd != mine.sd || lost) ? NAN : md;
+      mine.mt = (mine.st != mine.st || dead) ? NAN : mt;
+      mine.md = (mine.sd != mine.sd || dead) ? NAN : md;
       mine.pad0 = mine.pad1 = mine.pad2 = 0.f;
       const KdPart w = combine_parts(mine, true, 32, c2);
       if (lane == 0) C.wpart[row_i & 1][warp] = w;
@@ -279,8 +298,10 @@ struct KdRows {
       const bool valid = isfinite(row.mt) && isfinite(row.md) && isfinite(row.st) && isfinite(row.sd) &&
                          row.st > 0.f && row.sd > 0.f && !isnan(row.a);
       if (warp == 0 && lane == 0) P.row_kl[r] = row_kl(row, valid);
-      if (GRAD) gradient(r, row, valid, q, dead);
+      if (GRAD) gradient(r, row, valid, q, dead, dead_row);
     }
+    named_barrier_sync(kKdBarCompute, kKdWarps * 32);
+    if (dead && lane == 0) P.row_kl[dead_row] = NAN;
   }
 
   // KL / ln 2 = c A / S^t - (K^t - K^d) - log2(S^t / S^d), with the very
@@ -303,7 +324,7 @@ struct KdRows {
   }
 
   // ---- second pass: w (q - p) / T for every logit of the row pair
-  __device__ void gradient(int r, const KdPart& row, bool valid, int& q, bool& dead) {
+  __device__ void gradient(int r, const KdPart& row, bool valid, int& q, bool& dead, int& dead_row) {
     const float c2 = P.c2;
     const float kt = __fmul_rn(row.mt, c2), kd = __fmul_rn(row.md, c2);
     float lt, ld;
@@ -316,7 +337,7 @@ struct KdRows {
     unsigned char* out_row = static_cast<unsigned char*>(P.grad) + static_cast<size_t>(r) * row_bytes;
     for (int c = 0; c < P.nchunks; ++c, ++q) {
       uint4 tv[kKdVecsPerLane], dv[kKdVecsPerLane];
-      take(q % kKdStages, q, c, dead, tv, dv);
+      take(q % kKdStages, q, c, r, dead, dead_row, tv, dv);
       const int nvec = (chunk_bytes(c) + 15) / 16;
       unsigned char* out = out_row + static_cast<size_t>(c) * kKdHalf;
 #pragma unroll
@@ -458,6 +479,7 @@ extern "C" sv_status spec_kd_loss(int n_seq, int t_len, int V, sv_dtype dtype, c
   p.weights = weights;
   p.row_kl = row_kl;
   p.grad = grad;
+  p.wait_limit_ns = kd_wait_limit_ns();
   p.rows = rows;
   p.t_len = t_len;
   p.V = V;

@@ -165,3 +165,43 @@ def test_full_size_batch_on_sampled_rollouts():
         check(t[b:b + 1].cpu(), d[b:b + 1].cpu(), w[b:b + 1].cpu(), 1.0)
         torch.testing.assert_close(kl[b:b + 1], svp.kd_loss(t[b:b + 1].contiguous(), d[b:b + 1].contiguous(),
                                                             w[b:b + 1].contiguous(), 1.0)[0], rtol=0, atol=0)
+
+
+@pytest.fixture
+def wait_limit():
+    lib = svp.load_library()
+    yield lambda ns: lib.spec_kd_set_wait_limit_ns(ns)
+    lib.spec_kd_set_wait_limit_ns(-1)
+
+
+@pytest.mark.parametrize("grad", [True, False], ids=["grad", "loss"])
+@pytest.mark.parametrize("n_seq,t_len,V,dtype", [(2, 3, 40000, torch.bfloat16), (90, 4, 20008, torch.float32),
+                                                 (3, 2, 5003, torch.bfloat16)])
+def test_where_every_wait_expires(n_seq, t_len, V, dtype, grad, wait_limit):
+    g = torch.Generator(device="cuda").manual_seed(160)
+    t, d = ((torch.randn(n_seq, t_len, V, generator=g, device="cuda") * 3).to(dtype) for _ in range(2))
+    w = torch.ones(n_seq, device="cuda")
+    want = svp.kd_loss(t, d, w, grad=grad)
+    wait_limit(0)
+    got = svp.kd_loss(t, d, w, grad=grad)
+    wait_limit(-1)
+    again = svp.kd_loss(t, d, w, grad=grad)
+    torch.cuda.synchronize()
+    assert all(x is None or x.isnan().all() for x in got)
+    assert all(x is y is None or torch.equal(x, y) for x, y in zip(again, want))
+
+
+@pytest.mark.parametrize("ns", [1, 3000, 20000])
+def test_where_some_waits_expire(ns, wait_limit):
+    # which ones is not known; what is not NaN is right
+    g = torch.Generator(device="cuda").manual_seed(170)
+    t, d = ((torch.randn(100, 4, 60000, generator=g, device="cuda") * 3).to(torch.bfloat16) for _ in range(2))
+    w = torch.ones(100, device="cuda")
+    want = svp.kd_loss(t, d, w)
+    wait_limit(ns)
+    kl, loss, gr = svp.kd_loss(t, d, w)
+    torch.cuda.synchronize()
+    assert (kl.isnan() | (kl == want[0])).all()
+    assert torch.equal(loss.isnan(), kl.isnan().any(1)) and (loss.isnan() | (loss == want[1])).all()
+    assert (gr.isnan() | (gr == want[2])).all()
+    assert not gr[~kl.isnan()].isnan().any()
