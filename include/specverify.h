@@ -315,10 +315,13 @@ sv_status spec_kd_launch_shape(int V, sv_dtype dtype, int with_grad, int *cluste
 /* Penalties for repeated tokens, biases and grammar masks on logit rows: what
  * a rollout applies to the target's (and the drafter's) rows before
  * spec_verify, so that verification runs on the distribution that is sampled.
- * No page defines these; the rule is the usual one.  Row i of sequence b
- * follows its history and its drafts x_{b,0..i-1}.  With n(v) the times v was
- * generated (the history after the prompt, and those drafts) and seen(v)
- * whether v was generated or stands in the prompt, in this order:
+ * No page defines these, and programs differ in the order.  Here the bias is
+ * added after the penalties, so the repetition penalty does not scale it; a
+ * sampler that adds its biases first gives tokens both biased and seen another
+ * probability.  Row i of sequence b follows its history and its drafts
+ * x_{b,0..i-1}.  With n(v) the times v was generated (the history after the
+ * prompt, and those drafts) and seen(v) whether v was generated or stands in
+ * the prompt, in this order:
  *   z <- z > 0 ? z / r_b : z r_b     where seen(v)     (repetition)
  *   z <- z - f_b n(v) - p_b          where n(v) > 0    (frequency, presence)
  *   z <- z + bias_b(v)
@@ -333,11 +336,11 @@ sv_status spec_kd_launch_shape(int V, sv_dtype dtype, int with_grad, int *cluste
  *                 history_max), the first prompt_len[b] of them (NULL: 0)
  *                 the prompt.  history_max = 0: none
  *   tokens        [B, k] int32 device, the drafts, or NULL: none counted
- *   draft_len     [B] int32 device or NULL.  With it R is k + 1 (target
- *                 rows, i <= k_b) or k (draft rows, i < k_b), and the rows
- *                 past these are neither used nor written; a length outside
- *                 [0, k] leaves its whole sequence so (spec_verify reports
- *                 it).  NULL: every row
+ *   draft_len     [B] int32 device or NULL, with or without tokens.  With
+ *                 it R is k + 1 (target rows, i <= k_b) or k (draft rows,
+ *                 i < k_b), and the rows past these are neither used nor
+ *                 written; a length outside [0, k] leaves its whole sequence
+ *                 so (spec_verify reports it).  NULL: every row
  *   repetition, presence, frequency   [B] fp32 device or NULL (1, 0, 0);
  *                 repetition > 0
  *   bias_ids, bias_values   [B, n_bias] int32 / fp32 device; of entries with

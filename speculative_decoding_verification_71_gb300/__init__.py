@@ -554,8 +554,8 @@ def process_logits(logits, history=None, prompt_len=None, history_len=None, toke
     [0, k].  ``k`` is taken from tokens; without tokens draft_len is read as
     that of target rows, k = R - 1, so pass ``k=R`` for draft rows.
     repetition, presence, frequency [B] float32;
-    bias_ids [B, M] int32 with bias_values [B, M] float32; mask
-    [B, R, ceil(V / 32)] int32, a set bit allows its token.  ``out=logits``
+    bias_ids [B, M] int32 with bias_values [B, M] float32, added after the
+    penalties; mask [B, R, ceil(V / 32)] int32, a set bit allows its token.  ``out=logits``
     works in place; without ``out`` the result is a new tensor (whose rows
     past the drafts are not set).  Returns the result."""
     lib = load_library()

@@ -294,6 +294,14 @@ def test_the_last_of_a_tokens_biases_counts():
     assert got[0, 0, 7] == 299.0 and got[0, 0, 8] == 200.0
 
 
+def test_the_bias_is_added_after_the_penalties():
+    z = torch.tensor([[[2.0, -2.0, 2.0]]])
+    a = {"history": torch.tensor([[0, 1]], dtype=torch.int32), "prompt_len": torch.tensor([2], dtype=torch.int32),
+         "repetition": torch.tensor([2.0]), "bias_ids": torch.tensor([[0, 1, 2]], dtype=torch.int32),
+         "bias_values": torch.tensor([[3.0, 3.0, 3.0]])}
+    assert check(z, a, 0)[0, 0].tolist() == [4.0, -1.0, 5.0]
+
+
 def test_counts_beyond_16_bits():
     z = torch.full((1, 1, 40), 1.0)
     h = torch.full((1, 70001), 11, dtype=torch.int32)
