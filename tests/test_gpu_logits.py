@@ -184,6 +184,31 @@ def test_matches_the_rule(B, k, V, dtype, r, in_place):
     check(logits(B, k + 1, V, dtype, V), a, k, in_place=in_place)
 
 
+# How a call is cut depends on the numbers of CTAs that its slices make: vectors
+# a thread (2, 4), passes a slice (2, for fp32), rows a CTA (all of them, or two).
+MANY = [  # B, k, V, dtype, rules
+    (130, 7, 5001, torch.bfloat16, dict(H=50, n_bias=3)),       # 2 vectors
+    (120, 3, 9001, torch.float32, dict(H=64)),                  # 2
+    (256, 3, 9001, torch.bfloat16, dict(H=64, n_bias=2)),       # 4
+    (256, 3, 9001, torch.float32, dict(H=64, n_bias=2)),        # 4
+    (600, 0, 10001, torch.float32, dict(H=64)),                 # 4, two passes, the second with tokens
+    (500, 1, 9001, torch.float32, dict(H=64, n_bias=3)),        # 4, two passes, two rows
+    (620, 4, 8300, torch.bfloat16, dict(H=20)),                 # 4, five rows to a CTA
+    (256, 3, 9001, torch.bfloat16, dict(H=9000)),               # a list of thousands, above 48 KB of shared memory
+    (512, 1, 9001, torch.float32, dict(H=9000)),                # ... and two passes
+]
+
+
+@pytest.mark.parametrize("mask", [None, 0.6], ids=["no_mask", "mask"])
+@pytest.mark.parametrize("B,k,V,dtype,r", MANY, ids=[f"{c[0]}x{c[1] + 1}x{c[2]}-{str(c[3])[6:]}-{c[4]['H']}" for c in MANY])
+def test_batches_of_many_sequences(B, k, V, dtype, r, mask):
+    a = rules(B, k + 1, k, V, seed=V + B, mask=mask, **r)
+    if r["H"] > 1000:      # a few whole histories, the others short: the reference goes token by token
+        a["history_len"][3:] %= 60
+        a["prompt_len"] = a["history_len"] // 3
+    check(logits(B, k + 1, V, dtype, V), a, k, in_place=mask is not None and B % 4 == 0)
+
+
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_draft_rows(dtype):
     # R = k: row i follows i drafts, rows i >= k_b are the padding
