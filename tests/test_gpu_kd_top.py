@@ -109,6 +109,12 @@ def test_top_of_long_rows_that_are_split(V, dtype, K, rows):
     check_top(randn(rows, 1, V, seed=V + K, dtype=dtype), K)
 
 
+@pytest.mark.parametrize("V,dtype,K", [(262147, torch.float32, 256), (262147, torch.float32, 65), (140001, torch.float32, 200),
+                                       (200003, torch.bfloat16, 256), (200003, torch.bfloat16, 64)])
+def test_top_of_more_long_rows_than_are_split(V, dtype, K):
+    check_top_rows(randn(7, V, seed=V + K, dtype=dtype), K, 1.0, times=23)
+
+
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("K", [129, 200, 256])
 @pytest.mark.parametrize("V", [257, 1100, 4001, 8190])
@@ -413,6 +419,15 @@ def test_loss_matches_the_definition(n_seq, t_len, V, dtype, K, T, tail):
 @pytest.mark.parametrize("dtype,V", [(torch.bfloat16, V) for V in (4072, 4073, 8175, 8177, 16360, 16367, 16369)] +
                          [(torch.float32, V) for V in (2035, 2041, 4085, 4091, 8181, 8185)])
 def test_loss_where_the_row_length_changes_the_kernel(dtype, V, tail):
+    check_loss(*pair(3, 3, V, dtype, 70, 0.9, seed=V), 0.9, tail)
+
+
+# the longest rows of a kernel and the shortest of the next: 512, 1024 and 2048
+# vectors with the two that a row off the 16-byte boundary takes more
+@pytest.mark.parametrize("tail", [True, False], ids=["tail", "renorm"])
+@pytest.mark.parametrize("dtype,V", [(torch.bfloat16, V) for V in (4087, 4088, 8183, 8184, 16375, 16376, 16377)] +
+                         [(torch.float32, V) for V in (2043, 2044, 4091, 4092, 8187, 8188, 8189)])
+def test_loss_on_both_sides_of_a_change_of_kernel(dtype, V, tail):
     check_loss(*pair(3, 3, V, dtype, 70, 0.9, seed=V), 0.9, tail)
 
 
