@@ -235,6 +235,23 @@ struct TrRow {
   }
 };
 
+// mbar_wait_bounded for a limit above 0.
+__device__ __forceinline__ bool tr_wait(uint64_t* bar, uint32_t parity, long long limit_ns) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const unsigned long long t0 = global_ns();
+  while (!mbar_try_wait(bar, parity))
+    if (static_cast<long long>(global_ns() - t0) >= limit_ns) return false;
+  return true;
+}
+
+// NaN in place of this thread's gradients of a part.
+template <int ELT>
+__device__ __noinline__ void tr_nan_gradient(unsigned char* grad, int V, int first, int n, int shift, int same_shift) {
+  const uint32_t x = 0x7fc07fc0u;   // in either type
+  for (int v = threadIdx.x; v < n; v += kTrConsumers)
+    store_edge<ELT>(grad, V, (first + v) * Vec<ELT>::N - shift, same_shift, make_uint4(x, x, x, x));
+}
+
 // Whether a row has a list, and whether anything is wrong with it, by one warp.
 __device__ __forceinline__ bool tr_has_list(const TopLossParams& P, long long r, int lane) {
   bool any = false;
@@ -344,23 +361,23 @@ __global__ void __launch_bounds__(kTrThreads, kTrCtas) toploss_kernel(const __gr
   // ---- the consumers
   const f2 cc = pack2(P.c2, P.c2);
   unsigned q = 0;
-  bool dead = false;             // a wait of this warp has expired: what it adds is NaN
+  // a wait of this warp has expired: what it adds is NaN (a limit of 0, at which
+  // every wait expires, is looked at here once: at each wait it took 1 % of rows
+  // of 40 KB)
+  bool dead = P.wait_limit_ns <= 0;
   bool alone = false;            // (warp 0) the others' parts did not come
   int turn = 0, alone_turn = 0;
   // this lane's vectors of the slot, -inf past the row's; the slot is released
-  // as soon as they are in registers
-  auto take = [&](uint4 (&w)[kTrPerLane], int n, bool marked, long long r) {
+  // as soon as they are in registers.  After an expired wait they are whatever
+  // lies there, and the caller makes NaN of it once a row (at each slot it took
+  // 2 % of rows of 64 KB).
+  auto take = [&](uint4 (&w)[kTrPerLane], int n, bool marked) {
     const int s = q % kTrSlots;
     const uint32_t phase = (q / kTrSlots) & 1u;
-    ++q;
-    if (!dead) {
-      bool ok = mbar_wait_bounded(&sh.full[s], phase, P.wait_limit_ns);
-      if (marked) ok = ok && mbar_wait_bounded(&sh.ready[s], phase, P.wait_limit_ns);
-      dead = !__all_sync(0xffffffffu, ok);
-      if (dead && lane == 0) atomicMin(&sh.failed, static_cast<int>(r));
-    }
+    bool ok = !dead && tr_wait(&sh.full[s], phase, P.wait_limit_ns);
+    if (marked) ok = ok && tr_wait(&sh.ready[s], phase, P.wait_limit_ns);
+    dead = !__all_sync(0xffffffffu, ok);
     const uint4* src = reinterpret_cast<const uint4*>(ring + s * kTrSlotVecs * 16) + tid;
-    if (dead) n = 0;
     if (n >= kTrSlotVecs) {
 #pragma unroll
       for (int k = 0; k < kTrPerLane; ++k) w[k] = src[k * kTrConsumers];
@@ -370,6 +387,7 @@ __global__ void __launch_bounds__(kTrThreads, kTrCtas) toploss_kernel(const __gr
     }
     __syncwarp();
     if (lane == 0 && !dead) mbar_arrive(&sh.empty[s]);
+    ++q;
   };
   // the next row's list is loaded while this one is at work
   int next_id = -1;
@@ -454,7 +472,7 @@ __global__ void __launch_bounds__(kTrThreads, kTrCtas) toploss_kernel(const __gr
     if (end >= 0) end_vec = load_row_vec<ELT>(start, P.V, shift, end);
     for (int v = 0; v < row.n; v += kTrSlotVecs) {
       uint4 w[kTrPerLane];
-      take(w, row.n - v, true, r);
+      take(w, row.n - v, true);
       if (row.n - v > kTrSlotVecs / 2) {
         add(w);
       } else {   // a last slot of half the vectors at most (10000 rows of 20000: 245 us, as a whole one 250)
@@ -525,8 +543,7 @@ __global__ void __launch_bounds__(kTrThreads, kTrCtas) toploss_kernel(const __gr
 
     // ---- the gradient
     if (GRAD) {
-      const f2 bb = pack2(R.base, R.base);
-      f2 aa = pack2(R.a, R.a);
+      const f2 bb = pack2(R.base, R.base), aa = pack2(R.a, R.a);
       auto gradient = [&](const uint4& x) {
         f2 z[N / 2];
         float g[N];
@@ -538,8 +555,7 @@ __global__ void __launch_bounds__(kTrThreads, kTrCtas) toploss_kernel(const __gr
       unsigned char* out = grad + (static_cast<long long>(row.first) * N - shift) * ELT;
       for (int v = 0; v < row.n; v += kTrSlotVecs) {
         uint4 w[kTrPerLane];
-        take(w, row.n - v, false, r);
-        if (dead) aa = pack2(NAN, NAN);
+        take(w, row.n - v, false);
         unsigned char* at = out + static_cast<long long>(v + tid) * 16;
         if (P.same_shift && row.n - v >= kTrSlotVecs) {
 #pragma unroll
@@ -552,7 +568,9 @@ __global__ void __launch_bounds__(kTrThreads, kTrCtas) toploss_kernel(const __gr
         }
       }
       if (end >= 0) store_edge<ELT>(grad, P.V, end * N - shift, P.same_shift, gradient(end_vec));
+      if (dead) tr_nan_gradient<ELT>(grad, P.V, row.first, row.n, shift, P.same_shift);
     }
+    if (dead && lane == 0) atomicMin(&sh.failed, static_cast<int>(r));
 
     // ---- the listed tokens: their gradients after the row's, and the divergence
     const float lj = tl_below(zj, R.Ma, P.inv_T);
