@@ -87,11 +87,12 @@ struct TlRow {
   int valid;
 };
 
-// (z - m) / T: by difference, as the logits may be large and alike; apart where
-// the difference passes the range, which a T above 1 may undo.
-__device__ __forceinline__ float tl_below(float z, float m, float inv_T) {
-  const float d = __fsub_rn(z, m);
-  return d > -INFINITY ? __fmul_rn(d, inv_T) : __fsub_rn(__fmul_rn(z, inv_T), __fmul_rn(m, inv_T));
+// p (m - z) / T where (z - m) / T is past the range (the type's lowest value for
+// a mask, at a T below 1 or under a maximum of 1e32): p may bring it back.
+__device__ __forceinline__ float tl_far(float p, float m, float z, float inv_T) {
+  if (!(z > -INFINITY)) return INFINITY;
+  const float s = __fmul_rn(p, inv_T), d = __fsub_rn(m, z);
+  return d < INFINITY ? __fmul_rn(s, d) : __fsub_rn(__fmul_rn(s, m), __fmul_rn(s, z));
 }
 
 // The parts of all lanes on their common maxima, the same in every lane and in
@@ -112,7 +113,7 @@ __device__ __forceinline__ TlRow tl_row(const TlPart& part, double mass, float s
   R.Ma = fmaxf(part.m, part.ml);
   R.valid = part.s == part.s && R.Ma > -INFINITY && R.Ma < INFINITY;
   // the listed tokens carry most of Z: full-precision exponentials for them
-  const float lt = tl_below(part.m, R.Ma, P.inv_T);
+  const float lt = __fmul_rn(__fsub_rn(part.m, R.Ma), P.inv_T);
   const float ft = part.m > -INFINITY ? expf(lt) : 0.f;
   const float fl = part.ml > -INFINITY ? expf(__fmul_rn(__fsub_rn(part.ml, R.Ma), P.inv_T)) : 0.f;
   const float tail = __fmul_rn(part.s, ft);   // of Z
@@ -127,9 +128,10 @@ __device__ __forceinline__ TlRow tl_row(const TlPart& part, double mass, float s
   // written: r and 1 - Q are alike, and their logarithms' roundings are not
   R.kl = 0.f;
   if (rest > 0.f)
-    R.kl = tail > 1e-30f   ? rest * logf(__fdiv_rn(__fmul_rn(rest, R.Z), tail))
-           : part.s > 0.f ? rest * (logf(rest) - __fsub_rn(__fadd_rn(lt, logf(part.s)), R.LZ))
-                          : INFINITY;
+    R.kl = tail > 1e-30f         ? rest * logf(__fdiv_rn(__fmul_rn(rest, R.Z), tail))
+           : !(part.s > 0.f)     ? INFINITY
+           : lt > -INFINITY      ? rest * (logf(rest) - __fsub_rn(__fadd_rn(lt, logf(part.s)), R.LZ))
+                                 : tl_far(rest, R.Ma, part.m, P.inv_T);
   return R;
 }
 
@@ -573,12 +575,14 @@ __global__ void __launch_bounds__(kTrThreads, kTrCtas) toploss_kernel(const __gr
     if (dead && lane == 0) atomicMin(&sh.failed, static_cast<int>(r));
 
     // ---- the listed tokens: their gradients after the row's, and the divergence
-    const float lj = tl_below(zj, R.Ma, P.inv_T);
+    const float lj = __fmul_rn(__fsub_rn(zj, R.Ma), P.inv_T);
     if (P.renorm) {
       lp = R.mass > 0.f ? __fsub_rn(lp, logf(R.mass)) : -INFINITY;
       p = R.mass > 0.f ? __fdiv_rn(p, R.mass) : 0.f;
     }
-    float term = id >= 0 && p > 0.f ? __fmul_rn(p, __fsub_rn(lp, __fsub_rn(lj, R.LZ))) : 0.f;
+    float term = 0.f;
+    if (id >= 0 && p > 0.f)
+      term = lj > -INFINITY ? __fmul_rn(p, __fsub_rn(lp, __fsub_rn(lj, R.LZ))) : tl_far(p, R.Ma, zj, P.inv_T);
     term = warp_sum(term);
     if (lane == 0) sh.term[par][warp] = term;
     named_barrier_sync(1, kTrConsumers);
@@ -727,12 +731,14 @@ __global__ void __launch_bounds__(kTsThreads, U > 4 ? 3 : 4) toploss_short_kerne
       else if (v < nvec) store_edge<ELT>(grad, P.V, t0, P.same_shift, VT::pack(g));
     }
   }
-  const float lj = tl_below(zj, R.Ma, P.inv_T);
+  const float lj = __fmul_rn(__fsub_rn(zj, R.Ma), P.inv_T);
   if (P.renorm) {
     lp = R.mass > 0.f ? __fsub_rn(lp, logf(R.mass)) : -INFINITY;
     p = R.mass > 0.f ? __fdiv_rn(p, R.mass) : 0.f;
   }
-  float term = id >= 0 && p > 0.f ? __fmul_rn(p, __fsub_rn(lp, __fsub_rn(lj, R.LZ))) : 0.f;
+  float term = 0.f;
+  if (id >= 0 && p > 0.f)
+    term = lj > -INFINITY ? __fmul_rn(p, __fsub_rn(lp, __fsub_rn(lj, R.LZ))) : tl_far(p, R.Ma, zj, P.inv_T);
   term = warp_sum(term);
   if (lane == 0) terms[warp] = term;
   __syncthreads();

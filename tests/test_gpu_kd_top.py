@@ -499,6 +499,35 @@ def test_loss_of_rows_as_wide_as_the_type(V, dtype, tail):
         assert (np.abs(grad[b, 0] - s * want) <= s * bound + 1e-30).all(), (b, (np.abs(grad[b, 0] - s * want) - s * bound).max())
 
 
+@pytest.mark.parametrize("tail", [True, False], ids=["tail", "renorm"])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("T", [0.3, 0.6, 1.0, 2.0])
+@pytest.mark.parametrize("V", [60, 40001])
+def test_loss_of_a_draft_masked_with_the_lowest_value(V, T, dtype, tail):
+    # (z - m) / T passes the range where T is below 1, its share of the KL does not
+    K = 12
+    ids, lp, z, w = pair(4, 1, V, dtype, K, 1.0, seed=180)
+    lp = torch.log_softmax(torch.arange(K, 0, -1) * 0.9, 0).expand_as(lp).contiguous() - 0.1   # a tail of 0.1
+    low = torch.finfo(dtype).min
+    z[0, 0, ids[0, 0, 4:].long()] = low                   # some of the listed, with 0.03 of the mass
+    z[1, 0, int(ids[1, 0, K - 1])] = low
+    z[1, 0, int(ids[1, 0, K - 2])] = -INF                 # ... where nothing helps
+    others = torch.ones(V, dtype=torch.bool)
+    others[ids[2, 0].long()] = False
+    z[2, 0, others] = low                                 # all the others, with a tenth of it
+    lp[3, 0, 6:] = -300.0                                 # probability 0 in float32
+    z[3, 0, ids[3, 0, 6:].long()] = low
+    if T < 1:
+        z[3, 0, ids[3, 0].long()] = 3e38                  # both far above 0
+        z[3, 0, int(ids[3, 0, 5])] = 1.5e38               # probability 0.004
+    kl, _, _ = (x.cpu().double().numpy() for x in svp.kd_top_loss(ids.to(DEV), lp.to(DEV), z.to(DEV), w.to(DEV), T, tail=tail))
+    for b in range(4):
+        with np.errstate(over="ignore"):
+            ref, _, tol, _ = loss_reference(ids[b, 0], lp[b, 0], z[b, 0], float(w[b]), T, tail)
+        assert math.isfinite(ref) == (b != 1)
+        assert kl[b, 0] == ref if b == 1 else abs(kl[b, 0] - ref) <= tol, (b, kl[b, 0], ref, tol)
+
+
 def test_rows_without_a_list_are_not_read():
     ids, lp, z, w = pair(4, 3, 2001, torch.bfloat16, 10, 1.0, seed=60)
     for b, n in enumerate((0, 1, 2, 3)):
