@@ -30,7 +30,7 @@ def _nvcc():
 def _inputs():
     files = [os.path.join(CSRC, s) for s in SOURCES]
     files += [os.path.join(CSRC, "sv_internal.h"), os.path.join(CSRC, "sv_device.cuh"),
-              os.path.join(CSRC, "sv_rowvec.cuh"),
+              os.path.join(CSRC, "sv_rowvec.cuh"), os.path.join(CSRC, "sv_kd.h"),
               os.path.join(INCLUDE, "specverify.h"), __file__]
     return files
 

@@ -16,6 +16,7 @@
 
 #include "../../include/specverify.h"
 #include "sv_internal.h"
+#include "sv_kd.h"
 
 namespace sv {
 namespace {

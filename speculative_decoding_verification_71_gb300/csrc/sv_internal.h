@@ -108,10 +108,6 @@ struct VerifyParams {
   PiecesWs pw;
 };
 
-// The limit of the distillation kernels' waits for staged logits, a call's at
-// the time of the call (sv_api.cu: spec_kd_set_wait_limit_ns).
-long long kd_wait_limit_ns();
-
 // Launchers (sv_kernels.cu).
 cudaError_t launch_verify(const VerifyParams& p, int ctas, int smem_bytes, cudaStream_t s);
 cudaError_t prepare_verify_kernel(int smem_bytes);

@@ -40,6 +40,7 @@
 
 #include "../../include/specverify.h"
 #include "sv_internal.h"
+#include "sv_kd.h"
 #include "sv_device.cuh"
 
 namespace sv {

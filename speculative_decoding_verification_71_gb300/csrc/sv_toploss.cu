@@ -49,6 +49,7 @@
 
 #include "../../include/specverify.h"
 #include "sv_internal.h"
+#include "sv_kd.h"
 #include "sv_rowvec.cuh"
 
 namespace sv {
