@@ -404,7 +404,7 @@ sv_status spec_kd_top(int n_seq, int t_len, int V, sv_dtype dtype, const void *t
  *     KL = sum_j p_j (log p_j - log q(id_j)),
  *     grad(x) = w (q(x) - p_j) / T for a listed x, w q(x) / T for the others.
  *   ids, logp     [n_seq, t_len, K] int32 / fp32 device; entries with id < 0
- *                 are passed over (whatever their logp, NaN apart)
+ *                 are passed over (whatever their logp, NaN and +inf apart)
  *   draft_logits  [n_seq, t_len, V] dtype device, contiguous
  *   weights       [n_seq] fp32 device
  *   row_kl, loss  [n_seq, t_len], [n_seq] fp32 device, out:

@@ -21,7 +21,7 @@
 //     are under way while the history is counted;
 //   - the tokens of the bitmap, a thread for each token of each row.
 // On 256 sequences of up to four rows of 128256 bf16 logits with histories of
-// up to 4096 tokens: 71 us (4.7 TB/s of what has to be read and written), the
+// up to 4096 tokens: 70 us (4.7 TB/s of what has to be read and written), the
 // copy alone 53 us.  Bound by the chain of short phases that each CTA goes
 // through besides its copy (count, list, correct: they move little, and grow
 // with the distinct tokens, from 57 us at histories of 64 tokens to 71 us at
@@ -52,7 +52,9 @@ namespace sv {
 namespace {
 
 constexpr int kLgThreads = 256;
-constexpr int kLgCtas = 4;                // resident per SM (with 3 the ragged rows take 77 us, with 5 94: registers spill)
+// Resident CTAs per SM: with 3 the ragged rows take 77 us, with 5 94, as registers
+// spill (at 4 only the masked kernels of four vectors do, 40 bytes).
+constexpr int kLgCtas = 4;
 constexpr int kLgEnough = 912, kLgMost = 2432;   // CTAs: one and a half times those resident, and four times
 constexpr int kLgMaxDrafts = 32;
 // A table word: in the prompt, among the drafts, the last bias's entry + 1

@@ -27,8 +27,8 @@
 // tile hold a value of at least t notes them, with one ballot and one addition
 // a warp, and their largest value; once t is final, those that still pass are
 // read again, from L2, and their tokens at or above t kept.
-// On 1024 ragged rows of 128256 bf16 logits, K = 64: 46 us; appending token by
-// token while streaming 116 us.
+// On 1024 ragged rows of 128256 bf16 logits, K = 64: 44 us; appending token by
+// token while streaming 116 us.  A row that takes its sum again, 24 us for 9.
 //
 // The CTAs hand their tokens at or above t, and their M and S, to the
 // cluster's first one and leave; it sorts them, after a selection by

@@ -34,8 +34,8 @@
 // release, leaves last, when its copies have landed: none is to reach shared
 // memory that a later CTA owns.
 //
-// 4096 rows of 151936 bf16 logits with their gradients: 455 us, 5.5 TB/s of
-// each logit read and each gradient written once; the loss alone 187 us, 6.7
+// 4096 rows of 151936 bf16 logits with their gradients: 460 us, 5.4 TB/s of
+// each logit read and each gradient written once; the loss alone 189 us, 6.6
 // TB/s.  With one CTA to a row the rows at work do not stay in L2 (452 MB read
 // for 311 MB of rows) and the gradients take 523 us.  Kept in the registers of
 // a cluster's CTAs in place of read twice: 742 us, each CTA idle while the
@@ -478,7 +478,7 @@ __global__ void __launch_bounds__(kTrThreads, kTrCtas) toploss_kernel(const __gr
       take(w, row.n - v, true);
       if (row.n - v > kTrSlotVecs / 2) {
         add(w);
-      } else {   // a last slot of half the vectors at most (10000 rows of 20000: 245 us, as a whole one 250)
+      } else {   // a last slot of half the vectors at most (10000 rows of 20000: 2 % less than as a whole one)
         uint4 half[kTrPerLane / 2];
 #pragma unroll
         for (int k = 0; k < kTrPerLane / 2; ++k) half[k] = w[k];
@@ -619,7 +619,8 @@ __global__ void __launch_bounds__(kTrThreads, kTrCtas) toploss_kernel(const __gr
 // time on the wire; here twice the CTAs work at once and the row is read once.
 // Bound by its instructions: the list and the row's numbers cost as much as
 // 8000 logits (with every warp working out the row's numbers for itself 50000
-// rows of 4000 took 391 us).
+// rows of 4000 took 391 us where they take 359, with lists of 64).  Eight
+// vectors of bf16 with the gradient spill 48 bytes at three CTAs an SM.
 constexpr int kTsThreads = 256, kTsWarps = kTsThreads / 32;
 static_assert(kTsThreads >= SV_KD_TOP_MAX && kTsWarps == kTrWarps, "a thread for each entry of the list");
 
@@ -794,7 +795,7 @@ cudaError_t launch_toploss(const TopLossParams& p, int rows, cudaStream_t s) {
   const long long row_bytes = static_cast<long long>(p.V) * ELT;
   // Rows that fit in a CTA's registers, up to 32 KB, the lists' bits with them
   // (two vectors more for a row off the 16-byte boundary): 50000 bf16 rows of
-  // 4000 logits with gradients 358 us, streamed 790; 25000 of 8000 259 and 427;
+  // 4000 logits with gradients 359 us, streamed 790; 25000 of 8000 256 and 427;
   // 12500 of 16000 249 and 263; 16 of 16000 8.6 and 9.2.
   const int vecs = static_cast<int>(row_bytes / 16) + 2;
   if (vecs <= 8 * kTsThreads) {
