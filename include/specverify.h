@@ -347,7 +347,10 @@ sv_status spec_kd_launch_shape(int V, sv_dtype dtype, int with_grad, int *cluste
  *                 the same token the last counts.  n_bias = 0: none
  *   mask          [B, R, ceil(V / 32)] int32 device or NULL: bit v % 32 of
  *                 word v / 32 set allows token v.  A row that allows nothing
- *                 becomes all -inf, which spec_verify reports
+ *                 becomes all -inf, which spec_verify reports (it, and
+ *                 spec_kd_loss by NaN, may also report rows that hold finite
+ *                 logits with |z| / T above 2.9e9: forbid by the mask, not by
+ *                 -1e30, and force a token by it, not by a bias of 1e10)
  * Token ids outside [0, V) (history, drafts, biases) are passed over.  NaN
  * and infinities go through the arithmetic above; what the mask forbids is
  * -inf whatever it held.  k < 32, n_bias <= SV_MAX_BIASES, history_max <
