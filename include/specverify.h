@@ -48,6 +48,7 @@
 #ifndef SPECVERIFY_H
 #define SPECVERIFY_H
 
+#include <stddef.h>
 #include <stdint.h>
 
 #ifdef __cplusplus
@@ -434,6 +435,136 @@ sv_status spec_kd_top_loss(int n_seq, int t_len, int V, sv_dtype dtype, int K, c
                            const float *logp, const void *draft_logits, const float *weights,
                            float temperature, int mode, float *row_kl, float *loss, void *grad,
                            sv_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * The policy's own update on verified rollouts.
+ *
+ * The pages train the policy on the rollouts that verification keeps exact
+ * ("Accelerating RL Post-Training Rollouts via System-Integrated Speculative
+ * Decoding") and leave its loss open; these are the operators on logit rows
+ * that such a trainer needs beside spec_kd_loss, and what it does with the
+ * gradients before its step.
+ *
+ * Common to them: a row of logits z has a token x, p = softmax(z / T);
+ *   logits        [n_seq, t_len, V] dtype device, contiguous
+ *   tokens        [n_seq, t_len] int32 device; spec_verify's out_tokens will
+ *                 do.  A row whose token is negative (padding, a prompt) is not
+ *                 read: log-probability, entropy and losses 0, lse -inf,
+ *                 gradient 0
+ *   grad          [n_seq, t_len, V] dtype device, out (bf16: rounded to
+ *                 nearest even); may be the logits themselves, and may not
+ *                 overlap them otherwise
+ * A row holding NaN or +inf, one that is all -inf, and a token >= V give NaN
+ * in all the row's outputs (its gradient among them) and in the losses that it
+ * enters.  So does a derivative past float32's range in the gradient.  A token at
+ * logit -inf has log-probability -inf.  At most 2^28 rows, V * sizeof(dtype) <=
+ * 1 MiB, temperature as for spec_kd_loss.  Asynchronous on `stream`; no context,
+ * no allocation; every sum is taken in a fixed order.  Host-checkable errors
+ * return SV_ERR_INVALID_ARG and launch nothing.
+ * ------------------------------------------------------------------------ */
+
+/* Log-probabilities of the tokens, the rows' entropies and log-sum-exps:
+ *   logp    [n_seq, t_len] fp32 device, out: log p(x)
+ *   entropy [n_seq, t_len] fp32 device, out, or NULL: -sum p log p
+ *   lse     [n_seq, t_len] fp32 device, out: log sum exp(z / T) */
+sv_status sv_token_logp(int n_seq, int t_len, int V, sv_dtype dtype, const void *logits,
+                        const int32_t *tokens, float temperature, float *logp, float *entropy,
+                        float *lse, sv_stream_t stream);
+
+/* Their gradient in the logits, for a loss of the caller's own:
+ *   grad(v) = (d_logp (1[v = x] - p(v)) - d_entropy p(v) (log p(v) + entropy)) / T
+ *   logp, lse     [n_seq, t_len] fp32 device: sv_token_logp's for these rows
+ *   entropy       [n_seq, t_len] fp32 device: sv_token_logp's; with d_entropy,
+ *                 or both NULL
+ *   d_logp, d_entropy [n_seq, t_len] fp32 device: the loss's derivatives
+ * Probabilities are taken from z - z(x) and logp, so they keep their digits at
+ * any level of the logits; for a token with logp <= -32 from lse, whose
+ * rounding they then share.  A row whose derivatives are 0 has gradient 0 and
+ * is not read but for its token's logit. */
+sv_status sv_token_logp_grad(int n_seq, int t_len, int V, sv_dtype dtype, const void *logits,
+                             const int32_t *tokens, const float *logp, const float *lse,
+                             const float *entropy, const float *d_logp, const float *d_entropy,
+                             float temperature, void *grad, sv_stream_t stream);
+
+/* The clipped policy loss, with a divergence from a reference policy and an
+ * entropy bonus, and its gradient in the logits.  With r = exp(log p(x) - old)
+ * and d = ref - log p(x), a row's loss is
+ *   -min(r A, clip(r, 1 - clip_low, 1 + clip_high) A)
+ *   (where A < 0 and dual_clip > 0, at most -dual_clip A)
+ *   + kl_coef (e^d - d - 1) - entropy_coef H.
+ * Its derivative in log p(x) is -r A + kl_coef (1 - e^d), without the first
+ * term where clipping holds.
+ *   advantages    [n_seq] fp32 device, or [n_seq, t_len] with per_token = 1
+ *   weights       [n_seq] fp32 device (1 / tokens, a mask of sequences, ...)
+ *   old_logp      [n_seq, t_len] fp32 device, or NULL: the policy is the old
+ *                 one, r = 1 (its derivative stays)
+ *   ref_logp      [n_seq, t_len] fp32 device; may be NULL where kl_coef is 0
+ *   clip_low      in [0, 1], clip_high >= 0; dual_clip > 1, or 0 for none
+ *   logp          [n_seq, t_len] fp32 device, out
+ *   entropy       [n_seq, t_len] fp32 device, out, or NULL
+ *   row_loss, loss [n_seq, t_len], [n_seq] fp32 device, out:
+ *                 loss[b] = weights[b] sum_t row_loss[b, t]
+ *   grad          of sum_b loss[b], or NULL for the losses alone */
+sv_status sv_policy_loss(int n_seq, int t_len, int V, sv_dtype dtype, const void *logits,
+                         const int32_t *tokens, const float *advantages, int per_token,
+                         const float *weights, const float *old_logp, const float *ref_logp,
+                         float temperature, float clip_low, float clip_high, float dual_clip,
+                         float kl_coef, float entropy_coef, float *logp, float *entropy,
+                         float *row_loss, float *loss, void *grad, sv_stream_t stream);
+
+/* A loss of pairs of sequences, one preferred to the other, and its gradient
+ * in the logits.  Sequence 2 i is the preferred one of pair i, 2 i + 1 the
+ * other.  With s_b the sum of a sequence's log-probabilities (`average`: their
+ * mean), h = (s_2i - s_2i+1) - (ref_2i - ref_2i+1) and m = beta h:
+ *   SV_PREF_SIGMOID  (1 - smoothing) log(1 + e^-m) + smoothing log(1 + e^m)
+ *   SV_PREF_HINGE    max(0, 1 - m)
+ *   SV_PREF_IPO      (h - 1 / (2 beta))^2
+ *   logits, tokens [2 n_pair, t_len, V], [2 n_pair, t_len]
+ *   ref_logp      [2 n_pair] fp32 device: s_b under the reference policy
+ *   weights       [n_pair] fp32 device
+ *   beta          > 0; smoothing in [0, 1/2), 0 for the other kinds
+ *   logp          [2 n_pair, t_len] fp32 device, out
+ *   margin, loss  [n_pair] fp32 device, out: m, and weights[i] times the loss
+ *   grad          of sum_i loss[i], or NULL for the losses alone
+ *   work          sv_preference_work(n_pair, t_len) floats of device memory,
+ *                 16-byte aligned, for this call alone while it runs
+ * A sequence without tokens has s = 0. */
+typedef enum { SV_PREF_SIGMOID = 0, SV_PREF_HINGE = 1, SV_PREF_IPO = 2 } sv_pref_kind;
+
+size_t sv_preference_work(int n_pair, int t_len);
+
+sv_status sv_preference_loss(int n_pair, int t_len, int V, sv_dtype dtype, const void *logits,
+                             const int32_t *tokens, const float *ref_logp, const float *weights,
+                             float temperature, float beta, int kind, float smoothing, int average,
+                             float *logp, float *margin, float *loss, void *grad, float *work,
+                             sv_stream_t stream);
+
+/* The norm of n gradients together, and their scaling to a largest norm:
+ *   SV_NORM_L2  norm = sqrt(sum g^2) over all elements of all tensors
+ *   SV_NORM_MAX norm = max |g|
+ *   g <- g min(1, max_norm / (norm + 1e-6)), rounded to nearest even
+ *   grads, sizes, dtypes  [n] host: each tensor's device address, its number
+ *                 of elements (0 is allowed) and its type
+ *   max_norm      > 0; INFINITY for the norm alone
+ *   outs, out_dtypes [n] host, or both NULL.  With them the scaled gradients go
+ *                 there (also where nothing has to be scaled) and the gradients
+ *                 stay as they are; without them the gradients themselves are
+ *                 scaled, and not written where the factor is 1
+ *   norm          [1] fp32 device, out
+ *   work          [SV_CLIP_WORK] fp64 of device memory for this call alone
+ *                 while it runs
+ * A norm that is not finite scales nothing (the factor is 1): the caller reads
+ * it where it decides on the step.  n = 0 gives norm 0.  What is written may
+ * not overlap anything else that is read or written, outs[i] = grads[i] with
+ * one type apart.  Squares are summed in fp32 by threads where that loses
+ * nothing, else in fp64, and joined in fp64, in a fixed order that depends on
+ * the sizes alone.  The host arrays are read during the call. */
+typedef enum { SV_NORM_L2 = 0, SV_NORM_MAX = 1 } sv_norm_kind;
+#define SV_CLIP_WORK 608
+
+sv_status sv_clip_gradients(int n, const void *const *grads, const long long *sizes, const int *dtypes,
+                            int kind, float max_norm, void *const *outs, const int *out_dtypes,
+                            float *norm, double *work, sv_stream_t stream);
 
 /* Test hook: the limit, in nanoseconds, of spec_kd_loss's and
  * spec_kd_top_loss's waits for staged logits, in the calls of the whole process

@@ -16,6 +16,7 @@ context for convenient use from PyTorch.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 
 import torch
@@ -26,6 +27,7 @@ __all__ = [
     "SV_ERR_NONFINITE", "SV_ERR_TIMEOUT", "SV_ERR_CUDA", "SV_ERR_UNSUPPORTED",
     "SV_F32", "SV_BF16", "EXPORTED_SYMBOLS", "DraftController", "verify_tree", "SV_CTRL_BATCH", "SV_CTRL_PER_SEQUENCE",
     "measure_ex2", "process_logits", "kd_top", "kd_top_loss", "SV_KD_TOP_MAX",
+    "token_logp", "token_logp_grad", "policy_loss", "preference_loss", "clip_gradients",
 ]
 
 SV_OK, SV_ERR_INVALID_ARG, SV_ERR_BAD_DRAFT_LEN, SV_ERR_BAD_TOKEN = 0, 1, 2, 3
@@ -36,6 +38,9 @@ SV_KERNEL_AUTO, SV_KERNEL_CLUSTER, SV_KERNEL_PIECES = 0, 1, 2
 SV_CTRL_MAX_POINTS = 12
 SV_KD_TOP_TAIL, SV_KD_TOP_RENORM = 0, 1
 SV_KD_TOP_MAX = 256
+SV_PREF_SIGMOID, SV_PREF_HINGE, SV_PREF_IPO = 0, 1, 2
+SV_NORM_L2, SV_NORM_MAX = 0, 1
+SV_CLIP_WORK = 608
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_PKG, "libspecverify.so")
@@ -51,6 +56,8 @@ EXPORTED_SYMBOLS = (
     "spec_ctrl_observe", "spec_ctrl_choose", "spec_ctrl_alpha", "spec_ctrl_status",
     "spec_verify_tree", "sv_process_logits", "spec_kd_top", "spec_kd_top_loss",
     "spec_kd_set_wait_limit_ns",
+    "sv_token_logp", "sv_token_logp_grad", "sv_policy_loss", "sv_preference_work", "sv_preference_loss",
+    "sv_clip_gradients",
 )
 
 
@@ -167,6 +174,20 @@ def load_library(path: str | None = None):
     lib.spec_kd_top_loss.restype = c.c_int
     lib.spec_kd_top_loss.argtypes = [c.c_int, c.c_int, c.c_int, c.c_int, c.c_int, P, P, P, P, c.c_float, c.c_int,
                                      P, P, P, P]
+    lib.sv_token_logp.restype = c.c_int
+    lib.sv_token_logp.argtypes = [c.c_int, c.c_int, c.c_int, c.c_int, P, P, c.c_float, P, P, P, P]
+    lib.sv_token_logp_grad.restype = c.c_int
+    lib.sv_token_logp_grad.argtypes = [c.c_int, c.c_int, c.c_int, c.c_int] + [P] * 7 + [c.c_float, P, P]
+    lib.sv_policy_loss.restype = c.c_int
+    lib.sv_policy_loss.argtypes = ([c.c_int, c.c_int, c.c_int, c.c_int, P, P, P, c.c_int, P, P, P]
+                                   + [c.c_float] * 6 + [P] * 6)
+    lib.sv_preference_work.restype = c.c_size_t
+    lib.sv_preference_work.argtypes = [c.c_int, c.c_int]
+    lib.sv_preference_loss.restype = c.c_int
+    lib.sv_preference_loss.argtypes = [c.c_int, c.c_int, c.c_int, c.c_int, P, P, P, P, c.c_float, c.c_float, c.c_int,
+                                       c.c_float, c.c_int, P, P, P, P, P, P]
+    lib.sv_clip_gradients.restype = c.c_int
+    lib.sv_clip_gradients.argtypes = [c.c_int, P, P, P, c.c_int, c.c_float, P, P, P, P, P]
     lib.spec_kd_set_wait_limit_ns.restype = c.c_int
     lib.spec_kd_set_wait_limit_ns.argtypes = [c.c_longlong]
     lib.spec_verify_noalloc.restype = c.c_int
@@ -665,6 +686,245 @@ def kd_top_loss(ids, logp, draft, weights, temperature=1.0, tail=True, grad=True
         if st != SV_OK:
             raise SpecVerifyError(st, "spec_kd_top_loss")
         return row_kl, loss, g
+
+    return _launch(dev, stream, call)
+
+
+def _gradient_of(logits, grad, out):
+    """The tensor that takes a gradient in the logits: ``out`` (which may be
+    the logits), a new one, or None where none is asked for."""
+    if not grad:
+        return None
+    return torch.empty_like(logits) if out is None else out
+
+
+def _check_out(logits, grad, out):
+    if out is not None and not grad:
+        raise ValueError("out takes the gradient, which grad=False leaves out")
+    _address("out", out, logits.dtype, logits.shape, logits.device)
+
+
+def token_logp(logits, tokens, temperature=1.0, entropy=False, stream=None):
+    """Log-probabilities of the rows' tokens (``sv_token_logp`` in
+    include/specverify.h): a rollout's under the policy that drew it, or under
+    the reference.  logits [n_seq, t_len, V] float32 or bfloat16; tokens
+    [n_seq, t_len] int32, negative where a row has none (``verify``'s
+    out_tokens will do).  Returns (logp, entropy or None, lse), each [n_seq,
+    t_len] float32; 0, 0 and -inf where there is no token."""
+    lib = load_library()
+    (n_seq, t_len, V), dev, code = _logit_rows("logits", logits)
+    tokens_at = _address("tokens", tokens, torch.int32, (n_seq, t_len), dev)
+
+    def call(handle):
+        logp = torch.empty((n_seq, t_len), dtype=torch.float32, device=dev)
+        lse = torch.empty_like(logp)
+        H = torch.empty_like(logp) if entropy else None
+        st = lib.sv_token_logp(n_seq, t_len, V, code, logits.data_ptr(), tokens_at, temperature, logp.data_ptr(),
+                               H.data_ptr() if entropy else None, lse.data_ptr(), handle)
+        if st != SV_OK:
+            raise SpecVerifyError(st, "sv_token_logp")
+        return logp, H, lse
+
+    return _launch(dev, stream, call)
+
+
+def token_logp_grad(logits, tokens, logp, lse, d_logp, entropy=None, d_entropy=None, temperature=1.0, out=None,
+                    stream=None):
+    """The gradient in the logits of a loss of the tokens' log-probabilities
+    and the rows' entropies (``sv_token_logp_grad`` in include/specverify.h):
+    logp, lse and entropy as ``token_logp`` gave them, d_logp and d_entropy
+    [n_seq, t_len] float32 the loss's derivatives.  ``out=logits`` overwrites
+    the logits.  Returns the gradient, in the logits' shape and type."""
+    lib = load_library()
+    (n_seq, t_len, V), dev, code = _logit_rows("logits", logits)
+    if (entropy is None) != (d_entropy is None):
+        raise ValueError("entropy and d_entropy go together")
+    per = (n_seq, t_len)
+    tokens_at = _address("tokens", tokens, torch.int32, per, dev)
+    args = [_address(name, t, torch.float32, per, dev) for name, t in
+            (("logp", logp), ("lse", lse), ("entropy", entropy), ("d_logp", d_logp), ("d_entropy", d_entropy))]
+    _check_out(logits, True, out)
+
+    def call(handle):
+        g = _gradient_of(logits, True, out)
+        st = lib.sv_token_logp_grad(n_seq, t_len, V, code, logits.data_ptr(), tokens_at, *args, temperature,
+                                    g.data_ptr(), handle)
+        if st != SV_OK:
+            raise SpecVerifyError(st, "sv_token_logp_grad")
+        return g
+
+    return _launch(dev, stream, call)
+
+
+def policy_loss(logits, tokens, advantages, weights, old_logp=None, ref_logp=None, temperature=1.0, clip_low=0.2,
+                clip_high=0.2, dual_clip=None, kl_coef=0.0, entropy_coef=0.0, entropy=False, grad=True, out=None,
+                stream=None):
+    """The clipped policy loss with a divergence from a reference and an
+    entropy bonus, and its gradient in the logits (``sv_policy_loss`` in
+    include/specverify.h).  logits [n_seq, t_len, V] float32 or bfloat16;
+    tokens [n_seq, t_len] int32, negative where nothing is learnt; advantages
+    [n_seq] or [n_seq, t_len] float32; weights [n_seq] float32; old_logp,
+    ref_logp [n_seq, t_len] float32 (``token_logp``'s; without old_logp the
+    ratio is 1).  ``out=logits`` overwrites the logits with the gradient.
+    Returns (logp [n_seq, t_len], entropy [n_seq, t_len] or None, row_loss
+    [n_seq, t_len], loss [n_seq], grad [n_seq, t_len, V] or None); the entropy
+    is there where it is asked for or has a coefficient."""
+    lib = load_library()
+    (n_seq, t_len, V), dev, code = _logit_rows("logits", logits)
+    f32, per = torch.float32, (n_seq, t_len)
+    tokens_at = _address("tokens", tokens, torch.int32, per, dev)
+    per_token = isinstance(advantages, torch.Tensor) and advantages.dim() == 2
+    adv_at = _address("advantages", advantages, f32, per if per_token else (n_seq,), dev)
+    weights_at = _address("weights", weights, f32, (n_seq,), dev)
+    old_at = _address("old_logp", old_logp, f32, per, dev)
+    ref_at = _address("ref_logp", ref_logp, f32, per, dev)
+    if kl_coef and ref_logp is None:
+        raise ValueError("kl_coef needs ref_logp")
+    _check_out(logits, grad, out)
+    entropy = bool(entropy or entropy_coef)
+
+    def call(handle):
+        logp = torch.empty(per, dtype=f32, device=dev)
+        row_loss = torch.empty_like(logp)
+        H = torch.empty_like(logp) if entropy else None
+        loss = torch.empty((n_seq,), dtype=f32, device=dev)
+        g = _gradient_of(logits, grad, out)
+        st = lib.sv_policy_loss(n_seq, t_len, V, code, logits.data_ptr(), tokens_at, adv_at, int(per_token), weights_at,
+                                old_at, ref_at, temperature, clip_low, clip_high, dual_clip or 0.0, kl_coef,
+                                entropy_coef, logp.data_ptr(), H.data_ptr() if entropy else None, row_loss.data_ptr(),
+                                loss.data_ptr(), g.data_ptr() if grad else None, handle)
+        if st != SV_OK:
+            raise SpecVerifyError(st, "sv_policy_loss")
+        return logp, H, row_loss, loss, g
+
+    return _launch(dev, stream, call)
+
+
+_PREFERENCES = {"sigmoid": SV_PREF_SIGMOID, "hinge": SV_PREF_HINGE, "ipo": SV_PREF_IPO}
+
+
+def preference_loss(logits, tokens, ref_logp, weights, beta=0.1, temperature=1.0, kind="sigmoid", smoothing=0.0,
+                    average=False, grad=True, out=None, stream=None):
+    """A loss of pairs of sequences, one preferred to the other, and its
+    gradient in the logits (``sv_preference_loss`` in include/specverify.h).
+    logits [2 n, t_len, V] float32 or bfloat16, sequence 2 i preferred to
+    2 i + 1; tokens [2 n, t_len] int32, negative on prompts and padding;
+    ref_logp [2 n] float32, the sequences' log-probabilities under the
+    reference (``token_logp(...)[0].sum(1)``, their mean over the tokens with
+    ``average``); weights [n] float32; kind "sigmoid", "hinge" or "ipo".
+    ``out=logits`` overwrites the logits with the gradient.  Returns (logp
+    [2 n, t_len], margin [n], loss [n], grad [2 n, t_len, V] or None)."""
+    lib = load_library()
+    (n_seq, t_len, V), dev, code = _logit_rows("logits", logits)
+    if n_seq % 2:
+        raise ValueError(f"logits hold {n_seq} sequences, expected pairs")
+    if kind not in _PREFERENCES:
+        raise ValueError(f"kind is {kind!r}, expected one of {', '.join(_PREFERENCES)}")
+    n = n_seq // 2
+    f32, per = torch.float32, (n_seq, t_len)
+    tokens_at = _address("tokens", tokens, torch.int32, per, dev)
+    ref_at = _address("ref_logp", ref_logp, f32, (n_seq,), dev)
+    weights_at = _address("weights", weights, f32, (n,), dev)
+    _check_out(logits, grad, out)
+
+    def call(handle):
+        logp = torch.empty(per, dtype=f32, device=dev)
+        margin = torch.empty((n,), dtype=f32, device=dev)
+        loss = torch.empty_like(margin)
+        work = torch.empty((lib.sv_preference_work(n, t_len),), dtype=f32, device=dev)
+        g = _gradient_of(logits, grad, out)
+        st = lib.sv_preference_loss(n, t_len, V, code, logits.data_ptr(), tokens_at, ref_at, weights_at, temperature, beta,
+                                    _PREFERENCES[kind], smoothing, int(bool(average)), logp.data_ptr(),
+                                    margin.data_ptr(), loss.data_ptr(), g.data_ptr() if grad else None,
+                                    work.data_ptr(), handle)
+        if st != SV_OK:
+            raise SpecVerifyError(st, "sv_preference_loss")
+        return logp, margin, loss, g
+
+    return _launch(dev, stream, call)
+
+
+def _is_dense(t):
+    """Whether a tensor's elements fill one stretch of memory, in any order."""
+    if t.is_contiguous():
+        return True
+    at = 1
+    for stride, size in sorted((st, sz) for st, sz in zip(t.stride(), t.shape) if sz != 1):
+        if stride != at:
+            return False
+        at *= size
+    return True
+
+
+def clip_gradients(grads, max_norm=None, kind="l2", out=None, stream=None):
+    """The norm of many gradients together, and their scaling to ``max_norm``
+    (``sv_clip_gradients`` in include/specverify.h).  grads: float32 and
+    bfloat16 tensors on one GPU, each without gaps (None entries are passed
+    over, so ``[p.grad for p in ...]`` will do); kind "l2" or "max".  Without
+    ``max_norm`` nothing is scaled; with it the gradients are scaled in place,
+    or into ``out``, a list like ``grads`` whose tensors are laid out alike and
+    may be float32 for bfloat16 gradients.  Returns the norm before scaling, a
+    float32 tensor without dimensions on the GPU; nothing is synchronised."""
+    lib = load_library()
+    if isinstance(grads, torch.Tensor):
+        raise TypeError("grads must be a list of tensors")
+    if kind not in ("l2", "max"):
+        raise ValueError(f"kind is {kind!r}, expected 'l2' or 'max'")
+    if max_norm is not None and not max_norm > 0:
+        raise ValueError(f"max_norm is {max_norm}, expected a positive number")
+    grads = list(grads)
+    if out is not None:
+        out = list(out)
+        if max_norm is None:
+            raise ValueError("out takes the scaled gradients, which need max_norm")
+        if len(out) != len(grads) or any((o is None) != (t is None) for t, o in zip(grads, out)):
+            raise ValueError("out must have a tensor for each of grads")
+        out = [o for o in out if o is not None]
+    grads = [t for t in grads if t is not None]
+    if not grads:
+        raise ValueError("grads holds no tensor")
+    if not isinstance(grads[0], torch.Tensor):
+        raise TypeError("grads must hold torch.Tensors")
+    dev = grads[0].device
+
+    def table(name, tensors):
+        codes = []
+        for t in tensors:
+            if not isinstance(t, torch.Tensor):
+                raise TypeError(f"{name} must hold torch.Tensors")
+            if not t.is_cuda:
+                raise ValueError(f"{name} must hold CUDA tensors (got {t.device})")
+            if t.device != dev:
+                raise ValueError(f"a tensor of {name} is on {t.device}, expected {dev}")
+            code = _DTYPE_CODES.get(t.dtype)
+            if code is None:
+                raise TypeError(f"{name} must be float32 or bfloat16 (got {t.dtype})")
+            if not _is_dense(t):
+                raise ValueError(f"a tensor of {name} has gaps")
+            codes.append(code)
+        n = len(tensors)
+        return (ctypes.c_void_p * n)(*[t.data_ptr() for t in tensors]), (ctypes.c_int * n)(*codes)
+
+    at, codes = table("grads", grads)
+    n = len(grads)
+    sizes = (ctypes.c_longlong * n)(*[t.numel() for t in grads])
+    out_at = out_codes = None
+    if out is not None:
+        out_at, out_codes = table("out", out)
+        for t, o in zip(grads, out):
+            if o.shape != t.shape or o.stride() != t.stride() or not (o.dtype == t.dtype or o.dtype == torch.float32):
+                raise ValueError(f"out has a {o.dtype} tensor {tuple(o.shape)} for a {t.dtype} gradient {tuple(t.shape)}, "
+                                 "or one laid out otherwise")
+
+    def call(handle):
+        norm = torch.empty((), dtype=torch.float32, device=dev)
+        work = torch.empty((SV_CLIP_WORK,), dtype=torch.float64, device=dev)
+        st = lib.sv_clip_gradients(n, at, sizes, codes, SV_NORM_L2 if kind == "l2" else SV_NORM_MAX,
+                                   math.inf if max_norm is None else max_norm, out_at, out_codes, norm.data_ptr(),
+                                   work.data_ptr(), handle)
+        if st != SV_OK:
+            raise SpecVerifyError(st, "sv_clip_gradients")
+        return norm
 
     return _launch(dev, stream, call)
 

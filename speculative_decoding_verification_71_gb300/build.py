@@ -17,7 +17,8 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libspecverify.so")
 BUILD_DIR = os.path.join(PKG, "_build")
 SOURCES = ["sv_kernels.cu", "sv_pieces.cu", "sv_api.cu", "sv_noalloc.cu", "sv_kd.cu", "sv_ctrl.cu", "sv_tree.cu",
-           "sv_micro.cu", "sv_logits.cu", "sv_top.cu", "sv_toploss.cu"]
+           "sv_micro.cu", "sv_logits.cu", "sv_top.cu", "sv_toploss.cu", "sv_policy.cu", "sv_preference.cu",
+           "sv_clip.cu"]
 NVCC_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a", "-O3", "-lineinfo", "-std=c++17",
               "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall", "-I", INCLUDE]
 
@@ -30,7 +31,8 @@ def _nvcc():
 def _inputs():
     files = [os.path.join(CSRC, s) for s in SOURCES]
     files += [os.path.join(CSRC, "sv_internal.h"), os.path.join(CSRC, "sv_device.cuh"),
-              os.path.join(CSRC, "sv_rowvec.cuh"), os.path.join(CSRC, "sv_kd.h"),
+              os.path.join(CSRC, "sv_rowvec.cuh"), os.path.join(CSRC, "sv_rowsum.cuh"),
+              os.path.join(CSRC, "sv_token.cuh"), os.path.join(CSRC, "sv_kd.h"),
               os.path.join(INCLUDE, "specverify.h"), __file__]
     return files
 

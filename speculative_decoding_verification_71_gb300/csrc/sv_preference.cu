@@ -1,0 +1,129 @@
+// A loss of pairs of sequences, one preferred to the other, and its gradient in
+// the logits, for sm_103a.
+//
+// With s_b the sum (or the mean) of a sequence's log-probabilities, a pair's
+// h = (s_c - s_r) - (ref_c - ref_r) and m = beta h, the loss is
+//   sigmoid  (1 - e) log(1 + e^-m) + e log(1 + e^m),  e the smoothing;
+//   hinge    max(0, 1 - m);
+//   ipo      (h - 1 / (2 beta))^2.
+// Its derivative in a token's log-probability is that in h, with the other sign
+// for the rejected sequence, divided by the tokens for the mean; from there on
+// the gradient is that of sv_token.cuh.
+
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "../../include/specverify.h"
+#include "sv_internal.h"
+#include "sv_token.cuh"
+
+namespace sv {
+namespace {
+
+struct PairParams {
+  const int* tokens;           // [2 n_pair, t_len]
+  const float* logp;           // [2 n_pair, t_len]
+  const float* ref;            // [2 n_pair]
+  const float* weights;        // [n_pair]
+  float *margin, *loss;        // [n_pair]
+  float* d_logp;               // [2 n_pair, t_len] or null
+  int t_len, kind, average;
+  float beta, smoothing;
+};
+
+constexpr int kPairThreads = 256, kPairWarps = kPairThreads / 32;
+
+// log(1 + e^x)
+__device__ __forceinline__ double softplus(double x) { return fmax(x, 0.0) + log1p(exp(-fabs(x))); }
+
+__global__ void __launch_bounds__(kPairThreads) pair_kernel(const __grid_constant__ PairParams P) {
+  __shared__ double sums[2][kPairWarps];
+  __shared__ int counts[2][kPairWarps];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const long long i = blockIdx.x;
+  for (int q = 0; q < 2; ++q) {
+    const long long at = (2 * i + q) * P.t_len;
+    double s = 0.0;
+    int n = 0;
+    for (int t = tid; t < P.t_len; t += kPairThreads) {
+      s += static_cast<double>(P.logp[at + t]);
+      n += P.tokens[at + t] >= 0;
+    }
+    s = warp_sum(s);
+    n = __reduce_add_sync(0xffffffffu, n);
+    if (lane == 0) sums[q][warp] = s, counts[q][warp] = n;
+  }
+  __syncthreads();
+  double s[2] = {0.0, 0.0};
+  int n[2] = {0, 0};
+  for (int w = 0; w < kPairWarps; ++w)
+    for (int q = 0; q < 2; ++q) s[q] += sums[q][w], n[q] += counts[q][w];
+  double per[2] = {1.0, 1.0};
+  if (P.average)
+    for (int q = 0; q < 2; ++q) per[q] = 1.0 / (n[q] > 1 ? n[q] : 1);
+  const double h = (s[0] * per[0] - s[1] * per[1]) -
+                   (static_cast<double>(P.ref[2 * i]) - static_cast<double>(P.ref[2 * i + 1]));
+  const double beta = P.beta, m = beta * h, e = P.smoothing, w = P.weights[i];
+  double loss, slope;
+  if (P.kind == SV_PREF_SIGMOID) {
+    loss = (1.0 - e) * softplus(-m) + (e > 0.0 ? e * softplus(m) : 0.0);
+    slope = beta * (e / (1.0 + exp(-m)) - (1.0 - e) / (1.0 + exp(m)));
+  } else if (P.kind == SV_PREF_HINGE) {
+    loss = m < 1.0 ? 1.0 - m : m == m ? 0.0 : m;
+    slope = m < 1.0 ? -beta : m == m ? 0.0 : m;
+  } else {
+    const double off = h - 0.5 / beta;
+    loss = off * off;
+    slope = 2.0 * off;
+  }
+  if (tid == 0) {
+    P.margin[i] = static_cast<float>(m);
+    P.loss[i] = static_cast<float>(w * loss);
+  }
+  if (P.d_logp)
+    for (int q = 0; q < 2; ++q) {
+      const float g = static_cast<float>((q ? -w : w) * slope * per[q]);
+      for (int t = tid; t < P.t_len; t += kPairThreads) P.d_logp[(2 * i + q) * P.t_len + t] = g;
+    }
+}
+
+}  // namespace
+}  // namespace sv
+
+extern "C" size_t sv_preference_work(int n_pair, int t_len) {
+  // each row's log-sum-exp and derivative
+  return n_pair < 1 || t_len < 1 ? 0 : static_cast<size_t>(n_pair) * static_cast<size_t>(t_len) * 2 * 2;
+}
+
+extern "C" sv_status sv_preference_loss(int n_pair, int t_len, int V, sv_dtype dtype, const void* logits,
+                                        const int32_t* tokens, const float* ref_logp, const float* weights,
+                                        float temperature, float beta, int kind, float smoothing, int average,
+                                        float* logp, float* margin, float* loss, void* grad, float* work,
+                                        sv_stream_t stream) {
+  using namespace sv;
+  if (n_pair < 1 || n_pair > (1 << 27) || !tokens || !ref_logp || !weights || !logp || !margin || !loss || !work)
+    return SV_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(work) % 16) return SV_ERR_INVALID_ARG;
+  if (!(beta > 0.f) || !std::isfinite(beta)) return SV_ERR_INVALID_ARG;
+  if (kind != SV_PREF_SIGMOID && kind != SV_PREF_HINGE && kind != SV_PREF_IPO) return SV_ERR_INVALID_ARG;
+  if (!(smoothing >= 0.f && smoothing < 0.5f) || (smoothing != 0.f && kind != SV_PREF_SIGMOID)) return SV_ERR_INVALID_ARG;
+  if (average != 0 && average != 1) return SV_ERR_INVALID_ARG;
+  const int n_seq = 2 * n_pair;
+  const uintptr_t g = reinterpret_cast<uintptr_t>(grad), a = reinterpret_cast<uintptr_t>(logits);
+  const int elt = dtype == SV_F32 ? 4 : 2;
+  const uintptr_t bytes = static_cast<uintptr_t>(n_seq) * (t_len > 0 ? t_len : 0) * (V > 0 ? V : 0) * elt;
+  if (grad && (g % elt || (a != g && a < g + bytes && g < a + bytes))) return SV_ERR_INVALID_ARG;
+  NvtxRange range("sv_preference_loss");
+  float* lse = work;
+  sv_status st = sv_token_logp(n_seq, t_len, V, dtype, logits, tokens, temperature, logp, nullptr, lse, stream);
+  if (st != SV_OK) return st;
+  float* d_logp = grad ? work + static_cast<size_t>(n_seq) * t_len : nullptr;
+  const PairParams p{tokens, logp, ref_logp, weights, margin, loss, d_logp, t_len, kind, average, beta, smoothing};
+  pair_kernel<<<static_cast<unsigned>(n_pair), kPairThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(p);
+  if (cudaGetLastError() != cudaSuccess) return SV_ERR_CUDA;
+  if (!grad) return SV_OK;
+  return sv_token_logp_grad(n_seq, t_len, V, dtype, logits, tokens, logp, lse, nullptr, d_logp, nullptr, temperature,
+                            grad, stream);
+}

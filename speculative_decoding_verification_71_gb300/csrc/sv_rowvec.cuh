@@ -54,6 +54,33 @@ __device__ __forceinline__ uint4 load_row_vec(const unsigned char* row, int V, i
   return Vec<ELT>::pack(f);   // exact: the values are of the row's type
 }
 
+// A vector with -inf in the places of `bits`.
+template <int ELT>
+__device__ __noinline__ uint4 with_neg_inf(uint4 w, uint32_t bits) {
+  constexpr int N = Vec<ELT>::N;
+  float z[N];
+  Vec<ELT>::unpack(w, z);
+#pragma unroll
+  for (int e = 0; e < N; ++e)
+    if ((bits >> e) & 1u) z[e] = -INFINITY;
+  return Vec<ELT>::pack(z);
+}
+
+// A vector's gradients where it may reach past its row, or the rows lie unlike.
+template <int ELT>
+__device__ __noinline__ void store_edge(unsigned char* grad, int V, int t0, int same_shift, uint4 g) {
+  constexpr int N = Vec<ELT>::N;
+  if (same_shift && t0 >= 0 && t0 <= V - N) {
+    store_vec16(grad + static_cast<long long>(t0) * ELT, g);
+    return;
+  }
+  float z[N];
+  Vec<ELT>::unpack(g, z);
+#pragma unroll
+  for (int e = 0; e < N; ++e)
+    if (t0 + e >= 0 && t0 + e < V) Vec<ELT>::store_rounded(grad, t0 + e, z[e]);   // exact: of the type already
+}
+
 // N bits of a little-endian bit string from bit `at` on (at >= 0).  The word
 // after the first is read only where the N bits reach into it.
 template <int N, typename Word>

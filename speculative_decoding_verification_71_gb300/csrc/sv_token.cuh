@@ -1,0 +1,221 @@
+// What the operators over a row of logits and its token share: the row's sums,
+// the numbers that follow from them, and the gradient in the logits.
+//
+// With x the row's token, p = softmax(z / T) and H the entropy of p, a loss of
+// log p(x) and H with derivatives g and h has
+//   d/dz(v) = (g (1[v = x] - p(v)) - h p(v) (log p(v) + H)) / T.
+// The tokens but x are summed apart from it, about their own maximum m:
+//   s = sum 2^t, a = sum 2^t t, t = (z - m) c, c = log2(e) / T,
+// so that 1 - p(x) is never formed by a subtraction: a policy is sure of most of
+// its tokens, and there log p(x) = -log(1 + s') and the gradient at x is
+// g s' / Z, with s' the others' sum on x's scale.  For the other tokens
+//   d/dz(v) = 2^t (alpha + gamma t) : one exponential, and one multiply-add where
+// the entropy counts.
+#pragma once
+
+#include "sv_rowvec.cuh"
+
+namespace sv {
+namespace {
+
+// t below this is taken as this where it is a factor beside 2^t = 0 (0 times
+// -inf would be NaN).
+constexpr float kTokFloor = -16384.f;
+constexpr float kLn2 = 0.6931471805599453f, kLog2e = 1.4426950408889634f;
+
+struct TokPart {
+  float m, s, a;
+};
+__device__ __forceinline__ TokPart tok_none() { return TokPart{-INFINITY, 0.f, 0.f}; }
+
+// A thread's running maximum and sums over vectors of a row.
+template <int ELT, bool ENT>
+struct TokSum {
+  float m = -INFINITY;
+  f2 s2 = 0ull, s3 = 0ull, a2 = 0ull, a3 = 0ull;
+
+  template <int U>
+  __device__ __forceinline__ void add(const uint4 (&w)[U], float c2) {
+    using VT = Vec<ELT>;
+    const float vm = VT::vmax(w);        // NaN is passed over here and kept by the sum
+    if (vm > m) {
+      const float d = m > -INFINITY ? __fmul_rn(__fsub_rn(m, vm), c2) : kTokFloor;
+      const float f = fast_exp2(d);
+      const f2 ff = pack2(f, f);
+      if (ENT) {
+        const float dk = fmaxf(d, kTokFloor);
+        const f2 dd = pack2(dk, dk);
+        a2 = mul2(ff, fma2(s2, dd, a2));
+        a3 = mul2(ff, fma2(s3, dd, a3));
+      }
+      s2 = mul2(s2, ff);
+      s3 = mul2(s3, ff);
+      m = vm;
+    }
+    const float mb = m > -INFINITY ? m : 0.f;
+    const f2 mm = pack2(mb, mb), cc = pack2(c2, c2);
+#pragma unroll
+    for (const uint4& x : w) {
+      f2 z[VT::N / 2];
+      VT::pairs(x, z);
+#pragma unroll
+      for (int i = 0; i < VT::N / 2; i += 2) {
+        const f2 t0 = mul2(sub2(z[i], mm), cc), t1 = mul2(sub2(z[i + 1], mm), cc);
+        const f2 e0 = exp2_2(t0), e1 = exp2_2(t1);
+        s2 = add2(s2, e0);
+        s3 = add2(s3, e1);
+        if (ENT) {
+          a2 = fma2(e0, floored(t0), a2);
+          a3 = fma2(e1, floored(t1), a3);
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ static f2 floored(f2 t) {
+    float a, b;
+    unpack2(t, a, b);
+    return pack2(fmaxf(a, kTokFloor), fmaxf(b, kTokFloor));
+  }
+  __device__ __forceinline__ TokPart part() const {
+    TokPart p{m, 0.f, 0.f};
+    float hi;
+    unpack2(add2(s2, s3), p.s, hi);
+    p.s += hi;
+    if (ENT) {
+      unpack2(add2(a2, a3), p.a, hi);
+      p.a += hi;
+    }
+    return p;
+  }
+};
+
+// The lanes' parts on their common maximum, the same in every lane and in a
+// fixed order; a NaN among the sums stays (with its maximum at -inf too).
+template <bool ENT>
+__device__ __forceinline__ TokPart tok_join(const TokPart& p, float c2) {
+  TokPart r;
+  r.m = from_ordered_key(__reduce_max_sync(0xffffffffu, ordered_key(p.m)));
+  const float d = __fmul_rn(__fsub_rn(p.m, r.m), c2);
+  const float f = p.m > -INFINITY ? fast_exp2(d) : 1.f;
+  r.s = warp_sum(p.s * f);
+  r.a = ENT ? warp_sum(f > 0.f && p.m > -INFINITY ? f * __fmaf_rn(p.s, d, p.a) : 0.f) : 0.f;
+  return r;
+}
+
+// (z - m) / T, also where z - m passes the range and the quotient does not.
+__device__ __forceinline__ float tok_below(float z, float m, float inv_T) {
+  const float d = __fsub_rn(z, m);
+  if (d > -INFINITY || !(z > -INFINITY)) return __fmul_rn(d, inv_T);
+  return __fsub_rn(__fmul_rn(z, inv_T), __fmul_rn(m, inv_T));
+}
+
+struct TokRow {
+  float M, Z;          // the row's maximum and its sum about it
+  float rest, px;      // 1 - p(x), p(x)
+  float logp, lse;
+  float U, H;          // sum p (z - M) / T, the entropy
+  int valid;
+};
+
+template <bool ENT>
+__device__ __forceinline__ TokRow tok_row(const TokPart& part, float zx, float inv_T) {
+  TokRow R;
+  R.M = fmaxf(part.m, zx);
+  R.valid = part.s == part.s && zx == zx && R.M > -INFINITY && R.M < INFINITY;
+  const float dr = part.m > -INFINITY ? tok_below(part.m, R.M, inv_T) : -INFINITY;
+  const float dx = zx > -INFINITY ? tok_below(zx, R.M, inv_T) : -INFINITY;
+  const float fr = dr == 0.f ? 1.f : expf(dr), ex = dx == 0.f ? 1.f : expf(dx);
+  const float rest = __fmul_rn(part.s, fr);
+  R.Z = __fadd_rn(rest, ex);
+  const float log_Z = dx == 0.f ? log1pf(rest) : logf(R.Z);
+  R.rest = __fdiv_rn(rest, R.Z);
+  R.px = __fdiv_rn(ex, R.Z);
+  R.logp = __fsub_rn(dx, log_Z);
+  R.lse = __fmaf_rn(R.M, inv_T, log_Z);
+  R.U = R.H = 0.f;
+  if (ENT) {
+    float u = fr > 0.f ? __fmul_rn(fr, __fmaf_rn(part.a, kLn2, part.s * dr)) : 0.f;
+    if (ex > 0.f) u = __fmaf_rn(ex, dx, u);
+    R.U = __fdiv_rn(u, R.Z);
+    R.H = __fsub_rn(log_Z, R.U);
+  }
+  if (!R.valid) R.logp = R.lse = R.H = NAN;
+  return R;
+}
+
+// The gradient of a row: 2^t (alpha + gamma t) with t = (z - base) c + k, and
+// at the token itself.
+struct TokGrad {
+  float base, k, alpha, gamma, at_token;
+  __device__ __forceinline__ void none() { base = k = alpha = gamma = at_token = 0.f; }
+  __device__ __forceinline__ bool zero() const { return alpha == 0.f && gamma == 0.f && at_token == 0.f; }
+};
+
+// A derivative past the range has no gradient: NaN for the whole row.
+__device__ __forceinline__ void tok_check(TokGrad& G, bool valid) {
+  if (valid && fabsf(G.alpha) < INFINITY && fabsf(G.gamma) < INFINITY && fabsf(G.at_token) < INFINITY) return;
+  G.alpha = G.at_token = NAN;
+}
+
+__device__ __forceinline__ TokGrad tok_grad(const TokRow& R, float g, float h, float inv_T) {
+  const float q = __fdiv_rn(inv_T, R.Z);
+  TokGrad G;
+  G.base = R.M;
+  G.k = 0.f;
+  G.alpha = __fmul_rn(q, __fmaf_rn(h, R.U, -g));
+  G.gamma = -h * kLn2 * q;
+  const float own = R.px > 0.f ? h * R.px * __fadd_rn(R.logp, R.H) : 0.f;
+  G.at_token = __fmul_rn(inv_T, __fmaf_rn(g, R.rest, -own));
+  tok_check(G, R.valid);
+  return G;
+}
+
+// The same from what token_logp gave for the row.
+__device__ __forceinline__ TokGrad tok_grad_from(float zx, float logp, float lse, float H, float g, float h, float inv_T) {
+  TokGrad G;
+  // about the token's own logit, whose difference from the others keeps its
+  // digits at any level; about lse where the token is far below them
+  const bool near_token = logp > -32.f;
+  G.base = near_token ? zx : 0.f;
+  G.k = __fmul_rn(near_token ? logp : -lse, kLog2e);
+  G.alpha = __fmul_rn(inv_T, __fmaf_rn(-h, H, -g));
+  G.gamma = -h * kLn2 * inv_T;
+  const float px = expf(logp);
+  const float own = px > 0.f ? h * px * __fadd_rn(logp, H) : 0.f;
+  G.at_token = __fmul_rn(inv_T, __fmaf_rn(g, -expm1f(logp), -own));
+  tok_check(G, logp == logp && lse == lse);
+  return G;
+}
+
+// A vector's gradients; x_at is the token's place in it, or outside 0..N-1.
+template <int ELT, bool ENT>
+__device__ __forceinline__ uint4 tok_vec_grad(const uint4& w, const TokGrad& G, float c2, int x_at) {
+  using VT = Vec<ELT>;
+  constexpr int N = VT::N;
+  const f2 bb = pack2(G.base, G.base), cc = pack2(c2, c2), kk = pack2(G.k, G.k);
+  const f2 aa = pack2(G.alpha, G.alpha), gg = pack2(G.gamma, G.gamma);
+  f2 z[N / 2];
+  float d[N];
+  VT::pairs(w, z);
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) {
+    const f2 t = fma2(sub2(z[i], bb), cc, kk);
+    const f2 f = ENT ? fma2(TokSum<ELT, ENT>::floored(t), gg, aa) : aa;
+    unpack2(mul2(exp2_2(t), f), d[2 * i], d[2 * i + 1]);
+  }
+  if (static_cast<unsigned>(x_at) < static_cast<unsigned>(N)) {
+#pragma unroll
+    for (int e = 0; e < N; ++e)
+      if (e == x_at) d[e] = G.at_token;
+  }
+  return VT::pack(d);
+}
+
+// A vector without the token at place x_at (which may lie outside).
+template <int ELT>
+__device__ __forceinline__ void tok_take_out(uint4& w, int x_at) {
+  if (static_cast<unsigned>(x_at) < static_cast<unsigned>(Vec<ELT>::N)) w = with_neg_inf<ELT>(w, 1u << x_at);
+}
+
+}  // namespace
+}  // namespace sv

@@ -50,6 +50,7 @@
 #include "../../include/specverify.h"
 #include "sv_internal.h"
 #include "sv_kd.h"
+#include "sv_rowsum.cuh"
 #include "sv_rowvec.cuh"
 
 namespace sv {
@@ -142,33 +143,6 @@ __device__ __forceinline__ bool tl_any(bool x, int threads) {
   asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.s32 p, %1, 0;\n\tbarrier.red.or.pred q, 1, %2, p;\n\t"
                "selp.s32 %0, 1, 0, q;\n\t}" : "=r"(any) : "r"(static_cast<int>(x)), "r"(threads) : "memory");
   return any != 0;
-}
-
-// A vector with -inf in the places of `bits`.
-template <int ELT>
-__device__ __noinline__ uint4 with_neg_inf(uint4 w, uint32_t bits) {
-  constexpr int N = Vec<ELT>::N;
-  float z[N];
-  Vec<ELT>::unpack(w, z);
-#pragma unroll
-  for (int e = 0; e < N; ++e)
-    if ((bits >> e) & 1u) z[e] = -INFINITY;
-  return Vec<ELT>::pack(z);
-}
-
-// A vector's gradients where it may reach past its row, or the rows lie unlike.
-template <int ELT>
-__device__ __noinline__ void store_edge(unsigned char* grad, int V, int t0, int same_shift, uint4 g) {
-  constexpr int N = Vec<ELT>::N;
-  if (same_shift && t0 >= 0 && t0 <= V - N) {
-    store_vec16(grad + static_cast<long long>(t0) * ELT, g);
-    return;
-  }
-  float z[N];
-  Vec<ELT>::unpack(g, z);
-#pragma unroll
-  for (int e = 0; e < N; ++e)
-    if (t0 + e >= 0 && t0 + e < V) Vec<ELT>::store_rounded(grad, t0 + e, z[e]);   // exact: of the type already
 }
 
 constexpr int kTrWarps = 8;                           // consumer warps
@@ -755,36 +729,6 @@ __global__ void __launch_bounds__(kTsThreads, U > 4 ? 3 : 4) toploss_short_kerne
   }
 }
 
-// loss[b] = w_b * sum_t row_kl[b, t] in 64 bits and a fixed order: by a warp,
-// by all warps of a CTA where positions are many (one rollout of 4096: 3 us,
-// by one thread 300).
-constexpr int kTlSumThreads = 256, kTlSumWarps = kTlSumThreads / 32;
-constexpr int kTlSumMany = 256;
-__global__ void __launch_bounds__(kTlSumThreads) toploss_sum_kernel(int n_seq, int t_len, const float* row_kl,
-                                                                    const float* weights, float* loss) {
-  __shared__ double parts[kTlSumWarps];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const bool many = t_len > kTlSumMany;
-  const int b = many ? blockIdx.x : static_cast<int>(blockIdx.x) * kTlSumWarps + warp;
-  const int step = many ? kTlSumThreads : 32;
-  grid_dependency_wait();
-  double s = 0.0;
-  if (b < n_seq) {
-    const float* kl = row_kl + static_cast<long long>(b) * t_len;
-#pragma unroll 8
-    for (int t = many ? static_cast<int>(threadIdx.x) : lane; t < t_len; t += step) s += static_cast<double>(kl[t]);
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  if (many) {
-    if (lane == 0) parts[warp] = s;
-    __syncthreads();
-    s = 0.0;
-    for (int w = 0; w < kTlSumWarps; ++w) s += parts[w];
-  }
-  if (b < n_seq && (many ? threadIdx.x == 0 : lane == 0)) loss[b] = static_cast<float>(static_cast<double>(weights[b]) * s);
-}
-
 template <int ELT>
 cudaError_t launch_toploss(const TopLossParams& p, int rows, cudaStream_t s) {
   // Few rows: as many CTAs to a row as give the SMs work (a row of 128256 bf16
@@ -869,16 +813,6 @@ extern "C" sv_status spec_kd_top_loss(int n_seq, int t_len, int V, sv_dtype dtyp
   const int rows = n_seq * t_len;
   const cudaError_t e = elt == 2 ? launch_toploss<2>(p, rows, s) : launch_toploss<4>(p, rows, s);
   if (e != cudaSuccess || cudaGetLastError() != cudaSuccess) return SV_ERR_CUDA;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(t_len > kTlSumMany ? n_seq : (n_seq + kTlSumWarps - 1) / kTlSumWarps));
-  cfg.blockDim = dim3(kTlSumThreads);
-  cfg.stream = s;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, toploss_sum_kernel, n_seq, t_len, static_cast<const float*>(row_kl), weights, loss) != cudaSuccess)
-    return SV_ERR_CUDA;
+  if (launch_row_sum(n_seq, t_len, row_kl, weights, loss, s) != cudaSuccess) return SV_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? SV_OK : SV_ERR_CUDA;
 }
