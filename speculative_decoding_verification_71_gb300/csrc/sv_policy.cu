@@ -13,6 +13,8 @@
 
 #include <cuda_runtime.h>
 
+#include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 
@@ -45,13 +47,14 @@ struct RowParams {
   int t_len, V;
   int same_shift;              // logits and grad lie alike: 16-byte stores
   float c2, inv_T;             // log2(e) / T, 1 / T
+  long long wait_limit_ns;     // of a wait for staged logits
   PolicyArgs policy;
 };
 
-// (e^d - d - 1), without cancellation where d is small.
-__device__ __forceinline__ float kl_term(float d) {
+// (e^d - d - 1) from e^d - 1, without cancellation where d is small.
+__device__ __forceinline__ float kl_term(float d, float up) {
   if (d == INFINITY) return d;             // a token that the policy cannot say
-  if (!(fabsf(d) <= 0.125f)) return __fsub_rn(expm1f(d), d);
+  if (!(fabsf(d) <= 0.125f)) return __fsub_rn(up, d);
   // d^2 (1/2 + d/6 + ... + d^4/720): the next term is below 2e-9 of it
   float s = __fmaf_rn(d, 1.f / 720.f, 1.f / 120.f);
   s = __fmaf_rn(d, s, 1.f / 24.f);
@@ -60,10 +63,22 @@ __device__ __forceinline__ float kl_term(float d) {
   return d * d * s;
 }
 
+// What a row's loss needs besides its logits.
+struct PolicyRow {
+  float A, old_logp, ref_logp, weight;
+  __device__ __forceinline__ static PolicyRow of(const PolicyArgs& P, int r, int t_len) {
+    const int b = static_cast<unsigned>(r) / static_cast<unsigned>(t_len);
+    return PolicyRow{P.advantages[P.per_token ? r : b], P.old_logp ? P.old_logp[r] : 0.f,
+                     P.ref_logp ? P.ref_logp[r] : 0.f, P.weights[b]};
+  }
+};
+
 // A row's loss and its derivative in the token's log-probability.
-__device__ __forceinline__ void policy_row(const PolicyArgs& P, float A, float old_logp, float ref_logp, const TokRow& R,
-                                           float& loss, float& slope) {
-  const float r = P.old_logp ? expf(__fsub_rn(R.logp, old_logp)) : 1.f;
+template <bool ENT>
+__device__ __forceinline__ void policy_row(const PolicyArgs& P, const PolicyRow& row, const TokRow& R, float& loss,
+                                           float& slope) {
+  const float A = row.A;
+  const float r = P.old_logp ? expf(__fsub_rn(R.logp, row.old_logp)) : 1.f;
   const float low = 1.f - P.low, high = 1.f + P.high;
   const float gained = r * A, held = (r < low ? low : r > high ? high : r) * A;
   float gain = gained <= held ? gained : held;
@@ -73,13 +88,13 @@ __device__ __forceinline__ void policy_row(const PolicyArgs& P, float A, float o
     gain = P.dual * A;
     slope = 0.f;
   }
-  loss = -gain;
+  loss = R.valid ? -gain : NAN;
   if (P.ref_logp) {
-    const float d = __fsub_rn(ref_logp, R.logp);
-    loss = __fmaf_rn(P.kl, kl_term(d), loss);
-    slope = __fmaf_rn(-P.kl, expm1f(d), slope);
+    const float d = __fsub_rn(row.ref_logp, R.logp), up = expm1f(d);
+    loss = __fmaf_rn(P.kl, kl_term(d, up), loss);
+    slope = __fmaf_rn(-P.kl, up, slope);
   }
-  if (P.entropy != 0.f) loss = __fmaf_rn(-P.entropy, R.H, loss);
+  if (ENT) loss = __fmaf_rn(-P.entropy, R.entropy(), loss);
 }
 
 constexpr int kRowThreads = 512, kRowWarps = kRowThreads / 32;
@@ -96,7 +111,8 @@ __device__ __forceinline__ void write_gradient(const unsigned char* row, unsigne
   constexpr int N = Vec<ELT>::N;
   for (int v = threadIdx.x; v < nvec; v += blockDim.x) {
     const uint4 w = load_row_vec<ELT>(row, V, shift, v);
-    store_edge<ELT>(grad, V, v * N - shift, same_shift, tok_vec_grad<ELT, ENT>(w, G, c2, x + shift - v * N));
+    store_edge<ELT>(grad, V, v * N - shift, same_shift, tok_vec_grad<ELT, ENT>(w, G, c2));
+    if (static_cast<unsigned>(x + shift - v * N) < static_cast<unsigned>(N)) Vec<ELT>::store_rounded(grad, x, G.at_token);
   }
 }
 
@@ -134,22 +150,380 @@ __global__ void __launch_bounds__(kRowThreads) token_row_kernel(const __grid_con
   part = tok_join<ENT>(lane < kRowWarps ? parts[lane] : tok_none(), P.c2);
   const TokRow R = tok_row<ENT>(part, zx, P.inv_T);
   float loss = 0.f, slope = 0.f;
+  float w = 0.f;
   if (P.row_loss) {
-    const PolicyArgs& a = P.policy;
-    policy_row(a, a.advantages[a.per_token ? r : r / P.t_len], a.old_logp ? a.old_logp[r] : 0.f,
-               a.ref_logp ? a.ref_logp[r] : 0.f, R, loss, slope);
+    const PolicyRow mine = PolicyRow::of(P.policy, static_cast<int>(r), P.t_len);
+    policy_row<ENT>(P.policy, mine, R, loss, slope);
+    w = mine.weight;
   }
   if (tid == 0) {
     P.logp[r] = R.logp;
-    if (ENT && P.entropy) P.entropy[r] = R.H;
-    if (P.lse) P.lse[r] = R.lse;
+    if (ENT && P.entropy) P.entropy[r] = R.entropy();
+    if (P.lse) P.lse[r] = R.lse(P.inv_T);
     if (P.row_loss) P.row_loss[r] = loss;
   }
   if (GRAD) {
-    const float w = P.policy.weights[r / P.t_len];
-    const TokGrad G = tok_grad(R, w * slope, ENT ? -P.policy.entropy * w : 0.f, P.inv_T);
+    const TokGrad G = tok_grad<ENT>(R, w * slope, ENT ? -P.policy.entropy * w : 0.f, P.inv_T);
     __syncthreads();             // (in place: every thread has read the row)
     write_gradient<ELT, ENT>(row, grad, P.V, shift, nvec, P.same_shift, x, G, P.c2);
+  }
+}
+
+// ---- long rows: streamed through shared memory, where they stay for the gradient
+//
+// A row goes to a cluster of 1 to 8 CTAs of 8 warps and is split evenly over
+// their warps.  Each warp streams its share through a ring of its own, of 4 KB
+// slots: it asks for the copies itself, so nothing is handed from warp to warp.
+// Few warps with much work each: what a slot and a row cost besides their logits
+// is paid by every warp.  It sums its share as it lands and, once the warps
+// (and through distributed shared memory the CTAs) have joined their sums,
+// reads it a second time from the ring, writes the gradient and asks for the next
+// row's vectors in each slot that it leaves: every logit crosses HBM once and
+// every gradient value once, and the loads run ahead through the row's end.
+// That takes an SM's shared memory, seven slots a warp.  Without a gradient a slot
+// is filled again as soon as it is read, and two CTAs of three slots a warp share
+// an SM, one streaming while the other puts a row's numbers together.
+//
+// Rows with a token are dealt to the clusters in turn, whatever lies between them
+// (a batch of padded rollouts dealt by row number keeps some clusters a third
+// longer at work): every CTA counts the tokens of a window of rows and lists its
+// own.  Rows without one are zero-filled by single CTAs in between.
+//
+// Every wait has a limit.  A warp whose wait for a slot expires touches its ring
+// no more: its sums and gradients are NaN from there on, and so are all later rows
+// of its cluster.  A CTA whose cluster does not answer takes the row and all later
+// ones as NaN.  No copy is in flight when a CTA leaves.
+constexpr int kRgWarps = 8, kRgThreads = kRgWarps * 32;
+constexpr int kRgPerLane = 8;                               // vectors per lane and slot
+constexpr int kRgSlotVecs = kRgPerLane * 32, kRgSlotBytes = kRgSlotVecs * 16;
+constexpr int kRgKept = 7, kRgPassed = 3;                   // slots of a warp with and without a gradient
+constexpr int kRgMaxCtas = 8;
+constexpr int kRgWindow = 8192;                             // rows whose tokens are looked at together
+constexpr int kRgLive = 448, kRgDead = 64;                  // of which a cluster, a CTA gets so many at most
+constexpr int kRgSms = 152;
+constexpr int kRgMinRow = 32 * 1024;                        // bytes of a row that is streamed
+constexpr int kRgPart = 160 * 1024;                         // a CTA's part for the gradient at most
+constexpr int kRgMinPart = 16 * 1024;                       // and where a row is split for want of rows
+static_assert((kTokMaxRow + kRgMaxCtas - 1) / kRgMaxCtas <= kRgPart, "the longest row fits a cluster");
+static_assert(kRgPart / 16 + kRgWarps <= kRgWarps * (kRgKept - 1) * kRgSlotVecs, "a part fits the rings");
+constexpr long long kRgJoinLimitNs = 4 * kDrainLimitNs;     // a CTA's part comes within an expired wait
+
+struct RgShared {
+  uint64_t full[kRgWarps][kRgKept];
+  uint64_t joined[2];            // the cluster's parts of a row are here, by row parity as what follows
+  uint4 part[2][kRgMaxCtas];     // the CTAs' sums
+  TokPart warp[2][kRgWarps];     // the warps' sums
+  int counts[kRgWarps];          // rows with and without a token in a warp's strip of the window
+  int failed;                    // the first row in which the cluster did not answer, or kRgNoRow
+  unsigned short live[kRgLive], dead[kRgDead];
+};
+constexpr int kRgNoRow = 0x7fffffff;
+constexpr int kRgRingAt = (static_cast<int>(sizeof(RgShared)) + 127) / 128 * 128;
+constexpr int rg_smem(bool grad) { return kRgRingAt + kRgWarps * (grad ? kRgKept : kRgPassed) * kRgSlotBytes; }
+static_assert(rg_smem(true) <= 227 * 1024 && 2 * (rg_smem(false) + 1024) <= 228 * 1024, "an SM's shared memory");
+
+// A warp's share of a row's whole vectors: the place of its first one, which of
+// the row's vectors that is, and their number (the row's ends are taken apart).
+struct RgShare {
+  const unsigned char* at;
+  int first, n, shift, nvec;
+  template <int ELT>
+  __device__ __forceinline__ static RgShare of(const unsigned char* row, int V, int per, int index) {
+    constexpr int N = Vec<ELT>::N;
+    RgShare t;
+    t.shift = row_shift<ELT>(row);
+    t.nvec = row_vecs<ELT>(V, t.shift);
+    const int head = t.shift ? 1 : 0;
+    const int all = t.nvec - head - ((V + t.shift) % N && t.nvec > head ? 1 : 0);
+    const int from = min(all, index * per);
+    t.first = head + from;
+    t.n = min(all, index * per + per) - from;
+    t.at = row + (static_cast<long long>(t.first) * N - t.shift) * ELT;
+    return t;
+  }
+};
+
+__device__ __forceinline__ bool rg_wait(uint64_t* bar, uint32_t parity, long long limit_ns) {
+  return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, limit_ns));
+}
+
+// How many of the numbers below `x` are `mine` modulo `of`.
+__device__ __forceinline__ long long rg_own(long long x, int mine, int of) { return x > mine ? (x - mine + of - 1) / of : 0; }
+
+// `window`: rows whose tokens are looked at together; `per`: vectors of a warp's share.
+template <int ELT, bool ENT, bool GRAD>
+__global__ void __launch_bounds__(kRgThreads, GRAD ? 1 : 2) token_ring_kernel(const __grid_constant__ RowParams P, int rows,
+                                                                              int window, int per) {
+  constexpr int kRgSlots = GRAD ? kRgKept : kRgPassed;
+  using VT = Vec<ELT>;
+  constexpr int N = VT::N;
+  extern __shared__ __align__(1024) unsigned char smem[];
+  RgShared& sh = *reinterpret_cast<RgShared*>(smem);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  unsigned char* ring = smem + kRgRingAt + warp * (kRgSlots * kRgSlotBytes);
+  uint64_t* full = sh.full[warp];
+  const int ctas = cluster_ctas(), rank = cluster_rank();
+  const int cluster = blockIdx.x / ctas, clusters = gridDim.x / ctas;
+  if (lane < kRgSlots) mbar_init(&full[lane], 1);
+  if (tid == 0) {
+    for (int b = 0; b < 2; ++b) mbar_init(&sh.joined[b], 1);
+    sh.failed = kRgNoRow;
+  }
+  fence_mbar_init();
+  if (ctas > 1) cluster_sync();   // the others' barriers are set up too
+  if (P.row_loss) grid_dependents_launch();   // the sum of the rows may take its place on an SM
+
+  const uint64_t first_out = evict_first_policy();
+  int slot = 0, ask_slot = 0;     // the next one to take and to ask for
+  uint32_t round = 0;             // the parity of `slot`'s copies
+  unsigned asked = 0;
+  unsigned turn = 0;              // rows with a token
+  int armed = -1;                 // (warp 0) the last turn whose parts are expected
+  bool closed = false;            // (warp 0) no more are
+  bool dead = false;              // a wait of this warp has expired
+  long long seen_live = 0, seen_dead = 0;
+  for (long long w0 = 0; w0 < rows; w0 += window) {
+    // ---- which rows of the window are this cluster's, and this CTA's to fill
+    const int in_window = static_cast<int>(rows - w0 < window ? rows - w0 : window);
+    const int words = (in_window + 32 * kRgWarps - 1) / (32 * kRgWarps);   // 32 rows each, a lane for each
+    uint32_t live_bits = 0, dead_bits = 0;
+    for (int j = 0; j < words; ++j) {
+      const int at = (warp * words + j) * 32 + lane;
+      const bool in = at < in_window, has = in && P.tokens[w0 + at] >= 0;
+      const uint32_t l = __ballot_sync(0xffffffffu, has), d = __ballot_sync(0xffffffffu, in && !has);
+      if (lane == j) live_bits = l, dead_bits = d;
+    }
+    const int mine = __popc(live_bits) | __popc(dead_bits) << 16;
+    int upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int up = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += up;
+    }
+    __syncthreads();              // the last window's lists have been read
+    if (lane == 31) sh.counts[warp] = upto;
+    __syncthreads();
+    const int count = lane < kRgWarps ? sh.counts[lane] : 0;
+    const int total = static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(count)));
+    const int before = static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(lane < warp ? count : 0))) + upto - mine;
+    const long long own_live = rg_own(seen_live, cluster, clusters), own_dead = rg_own(seen_dead, blockIdx.x, gridDim.x);
+    {
+      long long k = seen_live + (before & 0xffff);
+      for (uint32_t b = live_bits; b; b &= b - 1, ++k)
+        if (k % clusters == cluster)
+          sh.live[rg_own(k, cluster, clusters) - own_live] = static_cast<unsigned short>((warp * words + lane) * 32 + __ffs(b) - 1);
+      k = seen_dead + (before >> 16);
+      for (uint32_t b = dead_bits; b; b &= b - 1, ++k)
+        if (k % gridDim.x == blockIdx.x) {
+          const int at = (warp * words + lane) * 32 + __ffs(b) - 1;
+          const long long r = w0 + at;
+          sh.dead[rg_own(k, blockIdx.x, gridDim.x) - own_dead] = static_cast<unsigned short>(at);
+          P.logp[r] = 0.f;
+          if (P.entropy) P.entropy[r] = 0.f;
+          if (P.lse) P.lse[r] = -INFINITY;
+          if (P.row_loss) P.row_loss[r] = 0.f;
+        }
+    }
+    seen_live += total & 0xffff;
+    seen_dead += total >> 16;
+    const int n_live = static_cast<int>(rg_own(seen_live, cluster, clusters) - own_live);
+    const int n_dead = static_cast<int>(rg_own(seen_dead, blockIdx.x, gridDim.x) - own_dead);
+    __syncthreads();
+
+    // ---- the copies: the next slot's vectors of this warp's shares, row after row
+    int ask = 0, ask_left = 0;    // the row after the one whose vectors are asked for, and what is left of that one
+    const unsigned char* ask_at = nullptr;
+    auto ask_one = [&] {
+      while (ask_left == 0) {
+        if (ask >= n_live) return false;
+        const RgShare t = RgShare::of<ELT>(P.logits + (w0 + sh.live[ask++]) * P.V * ELT, P.V, per, rank * kRgWarps + warp);
+        ask_at = t.at;
+        ask_left = t.n;
+      }
+      const int n = min(ask_left, kRgSlotVecs);
+      if (lane == 0) {
+        const uint32_t bytes = static_cast<uint32_t>(n) * 16u;
+        mbar_expect_tx(&full[ask_slot], bytes);
+        bulk_load_hint(ring + ask_slot * kRgSlotBytes, ask_at, bytes, &full[ask_slot], first_out);
+      }
+      ask_at += static_cast<long long>(n) * 16;
+      ask_left -= n;
+      ++asked;
+      if (++ask_slot == kRgSlots) ask_slot = 0;
+      return true;
+    };
+    if (!dead)
+      for (int s = 0; s < kRgSlots; ++s)
+        if (!ask_one()) break;
+
+    int next_x = n_live ? P.tokens[w0 + sh.live[0]] : 0;
+    float next_zx = n_live && next_x < P.V ? load_elem<ELT>(P.logits + (w0 + sh.live[0]) * P.V * ELT, next_x) : NAN;
+    int filled = 0;
+    for (int i = 0; i < n_live; ++i, ++turn) {
+      const long long r = w0 + sh.live[i];
+      const unsigned char* row = P.logits + r * P.V * ELT;
+      unsigned char* grad = GRAD ? P.grad + r * P.V * ELT : nullptr;
+      const RgShare t = RgShare::of<ELT>(row, P.V, per, rank * kRgWarps + warp);
+      const int par = turn & 1;
+      const uint32_t phase = turn >> 1 & 1;
+      const int x = next_x < P.V ? next_x : -(1 << 30);
+      const float zx = next_zx;
+      // what the row's numbers need is loaded while it is summed
+      const long long r_next = i + 1 < n_live ? w0 + sh.live[i + 1] : r;
+      next_x = P.tokens[r_next];
+      PolicyRow mine{};
+      if (P.row_loss) mine = PolicyRow::of(P.policy, static_cast<int>(r), P.t_len);
+
+      // ---- the sums of this warp's share, and by two threads of the row's ends
+      TokSum<ELT, ENT> sum;
+      int end = -1;
+      if (rank == 0 && tid == 0 && t.shift) end = 0;
+      if (rank == 0 && tid == 32 && (P.V + t.shift) % N && t.nvec > (t.shift ? 1 : 0)) end = t.nvec - 1;
+      uint4 end_vec = VT::neg_inf();
+      if (end >= 0) end_vec = load_row_vec<ELT>(row, P.V, t.shift, end);
+      // where x lies from the share's first vector on, and whether this lane reads it
+      const int x_vec = (x + t.shift) / N - t.first, x_in = (x + t.shift) % N;
+      const bool own_x = x_vec >= 0 && x_vec < t.n && x_vec % 32 == lane;
+      const int row_slot = slot;
+      for (int v = 0; v < t.n; v += kRgSlotVecs) {
+        const int n = t.n - v;
+        unsigned char* at = ring + slot * kRgSlotBytes;
+        if (!dead) dead = !rg_wait(&full[slot], round, P.wait_limit_ns);
+        if (++slot == kRgSlots) slot = 0, round ^= 1;
+        if (dead) continue;
+        if (own_x && x_vec >= v && x_vec < v + kRgSlotVecs) {   // out of the sum: this lane reads what it writes here
+          VT::store_scalar(at, (x_vec - v) * N + x_in, -INFINITY);
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // before the slot is filled again
+        }
+        const uint4* src = reinterpret_cast<const uint4*>(at) + lane;
+        if (n > kRgSlotVecs / 2) {
+          uint4 w[kRgPerLane];
+#pragma unroll
+          for (int k = 0; k < kRgPerLane; ++k) w[k] = n >= kRgSlotVecs || lane + k * 32 < n ? src[k * 32] : VT::neg_inf();
+          if (!GRAD) {
+            __syncwarp();
+            ask_one();
+          }
+          sum.add(w, P.c2);
+        } else {
+          uint4 w[kRgPerLane / 2];
+#pragma unroll
+          for (int k = 0; k < kRgPerLane / 2; ++k) w[k] = lane + k * 32 < n ? src[k * 32] : VT::neg_inf();
+          if (!GRAD) {
+            __syncwarp();
+            ask_one();
+          }
+          sum.add(w, P.c2);
+        }
+      }
+      if (end >= 0) {
+        uint4 one[1] = {end_vec};
+        tok_take_out<ELT>(one[0], x + t.shift - end * N);
+        sum.add(one, P.c2);
+      }
+      TokPart part = sum.part();
+      // (the token's logit is part of what the others wait for: in place they may write over it afterwards)
+      if (dead || zx != zx) part.s = NAN;
+      part = tok_join<ENT>(part, P.c2);
+      if (lane == 0) sh.warp[par][warp] = part;
+      __syncthreads();
+      part = tok_join<ENT>(lane < kRgWarps ? sh.warp[par][lane] : tok_none(), P.c2);
+      bool answered = true;
+      if (ctas > 1) {
+        const bool alone = *static_cast<volatile int*>(&sh.failed) != kRgNoRow;
+        if (warp == 0 && !closed) {
+          // (alone: others may still get here once, which is waited for at the end)
+          closed = alone;
+          if (lane == 0) mbar_expect_tx(&sh.joined[par], static_cast<uint32_t>(ctas) * 16u);
+          armed = static_cast<int>(turn);
+          if (!alone && lane < ctas)
+            st_async(peer(&sh.part[par][rank], lane),
+                     make_uint4(__float_as_uint(part.m), __float_as_uint(part.s), __float_as_uint(part.a), 0u),
+                     peer(&sh.joined[par], lane));
+        }
+        answered = !alone && rg_wait(&sh.joined[par], phase, kRgJoinLimitNs);
+        TokPart other = tok_none();
+        if (answered && lane < ctas) {
+          const uint4 y = sh.part[par][lane];
+          other = TokPart{__uint_as_float(y.x), __uint_as_float(y.y), __uint_as_float(y.z)};
+        }
+        if (!answered && lane == 0) atomicMin(&sh.failed, static_cast<int>(r));
+        part = tok_join<ENT>(other, P.c2);
+        if (!answered) part.s = NAN;
+      }
+      const TokRow R = tok_row<ENT>(part, zx, P.inv_T);
+      next_zx = next_x < P.V && next_x >= 0 ? load_elem<ELT>(P.logits + r_next * P.V * ELT, next_x) : NAN;
+      float loss = 0.f, slope = 0.f;
+      if (P.row_loss) policy_row<ENT>(P.policy, mine, R, loss, slope);
+      if (tid == 0 && rank == 0) {
+        P.logp[r] = R.logp;
+        if (ENT && P.entropy) P.entropy[r] = R.entropy();
+        if (P.lse) P.lse[r] = R.lse(P.inv_T);
+        if (P.row_loss) P.row_loss[r] = loss;
+      }
+
+      // ---- the gradient, from the ring
+      if (GRAD) {
+        const TokGrad G = tok_grad<ENT>(R, mine.weight * slope, ENT ? -P.policy.entropy * mine.weight : 0.f, P.inv_T);
+        unsigned char* out = grad + (static_cast<long long>(t.first) * N - t.shift) * ELT;
+        int from = row_slot;
+        for (int v = 0; v < t.n; v += kRgSlotVecs) {
+          const int n = t.n - v;
+          const uint4* src = reinterpret_cast<const uint4*>(ring + from * kRgSlotBytes) + lane;
+          if (++from == kRgSlots) from = 0;
+          uint4 w[kRgPerLane];
+#pragma unroll
+          for (int k = 0; k < kRgPerLane; ++k) w[k] = n >= kRgSlotVecs || lane + k * 32 < n ? src[k * 32] : VT::neg_inf();
+          if (dead) {            // (alpha is NaN)
+#pragma unroll
+            for (int k = 0; k < kRgPerLane; ++k) w[k] = VT::neg_inf();
+          }
+          __syncwarp();
+          if (!dead) ask_one();
+          unsigned char* at = out + static_cast<long long>(v + lane) * 16;
+          if (P.same_shift && n >= kRgSlotVecs) {
+#pragma unroll
+            for (int k = 0; k < kRgPerLane; ++k) store_vec16(at + k * 512, tok_vec_grad<ELT, ENT>(w[k], G, P.c2));
+          } else {
+#pragma unroll
+            for (int k = 0; k < kRgPerLane; ++k)
+              if (lane + k * 32 < n)
+                store_edge<ELT>(grad, P.V, (t.first + v + lane + k * 32) * N - t.shift, P.same_shift, tok_vec_grad<ELT, ENT>(w[k], G, P.c2));
+          }
+        }
+        if (end >= 0) store_edge<ELT>(grad, P.V, end * N - t.shift, P.same_shift, tok_vec_grad<ELT, ENT>(end_vec, G, P.c2));
+        // the token's own after its vector's, by the same thread
+        if (own_x || (end >= 0 && (x + t.shift) / N == end && x >= 0)) VT::store_rounded(grad, x, G.at_token);
+        // rows without a token, as many as there are for each row with one
+        for (; static_cast<long long>(filled) * n_live < static_cast<long long>(i + 1) * n_dead; ++filled) {
+          unsigned char* zero = P.grad + (w0 + sh.dead[filled]) * P.V * ELT;
+          const int shift = row_shift<ELT>(zero);
+          zero_row<ELT>(zero, P.V, shift, row_vecs<ELT>(P.V, shift), 1);
+        }
+      }
+    }
+    if (GRAD)
+      for (; filled < n_dead; ++filled) {
+        unsigned char* zero = P.grad + (w0 + sh.dead[filled]) * P.V * ELT;
+        const int shift = row_shift<ELT>(zero);
+        zero_row<ELT>(zero, P.V, shift, row_vecs<ELT>(P.V, shift), 1);
+      }
+  }
+  // ---- no copy is left in flight, and nothing on its way to a CTA that has left
+  if (dead && lane == 0)
+    for (unsigned k = asked > kRgSlots ? asked - kRgSlots : 0; k < asked; ++k)
+      mbar_wait_bounded(&full[k % kRgSlots], k / kRgSlots & 1, kDrainLimitNs);
+  if (ctas > 1) {
+    cluster_sync();
+    if (sh.failed != kRgNoRow && tid == 0) {
+      for (int k = armed > 0 ? armed - 1 : 0; k <= armed; ++k)
+        mbar_wait_bounded(&sh.joined[k & 1], static_cast<uint32_t>(k >> 1 & 1), kDrainLimitNs);
+      // the row may have been put together by the others before
+      P.logp[sh.failed] = NAN;
+      if (P.entropy) P.entropy[sh.failed] = NAN;
+      if (P.lse) P.lse[sh.failed] = NAN;
+      if (P.row_loss) P.row_loss[sh.failed] = NAN;
+    }
   }
 }
 
@@ -181,17 +555,76 @@ __global__ void __launch_bounds__(kRowThreads) token_grad_kernel(const __grid_co
   else write_gradient<ELT, ENT>(row, grad, P.V, shift, nvec, P.same_shift, x, G, P.c2);
 }
 
+// Clusters of `ctas` of the ring kernel that fit at once, asked for once per
+// instance, size and device.
+template <int ELT, bool ENT, bool GRAD>
+cudaError_t ring_clusters(int ctas, int* fit) {
+  static std::atomic<int> known[64][kRgMaxCtas + 1];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 64 && (*fit = known[dev][ctas].load(std::memory_order_acquire)) > 0) return cudaSuccess;
+  const void* fn = reinterpret_cast<const void*>(&token_ring_kernel<ELT, ENT, GRAD>);
+  e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, rg_smem(GRAD));
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = static_cast<unsigned>(ctas);
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+  cfg.blockDim = dim3(kRgThreads);
+  cfg.dynamicSmemBytes = static_cast<size_t>(rg_smem(GRAD));
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  e = cudaOccupancyMaxActiveClusters(fit, fn, &cfg);
+  if (e != cudaSuccess) return e;
+  if (*fit < 1) return cudaErrorInvalidConfiguration;
+  if (dev < 64) known[dev][ctas].store(*fit, std::memory_order_release);
+  return cudaSuccess;
+}
+
+template <int ELT, bool ENT, bool GRAD>
+cudaError_t launch_ring(const RowParams& p, int rows, cudaStream_t s) {
+  const long long row_bytes = static_cast<long long>(p.V) * ELT;
+  // For the gradient a CTA's part of a row stays in its ring, with room for what
+  // is on its way.  Few rows: as many CTAs to a row as give the SMs work.
+  int ctas = GRAD ? static_cast<int>((row_bytes + kRgPart - 1) / kRgPart) : 1;
+  const int room = GRAD ? kRgSms : 2 * kRgSms;
+  while (ctas < kRgMaxCtas && static_cast<long long>(rows) * 2 * ctas <= room && row_bytes / (2 * ctas) >= kRgMinPart) ctas *= 2;
+  if (ctas > kRgMaxCtas) ctas = kRgMaxCtas;
+  int fit = 0;
+  cudaError_t e = ring_clusters<ELT, ENT, GRAD>(ctas, &fit);
+  if (e != cudaSuccess) return e;
+  const int clusters = rows < fit ? rows : fit;
+  const long long window = std::min<long long>(kRgWindow, std::min<long long>(static_cast<long long>(kRgLive) * clusters,
+                                                                              static_cast<long long>(kRgDead) * clusters * ctas));
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = static_cast<unsigned>(ctas);
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(clusters * ctas));
+  cfg.blockDim = dim3(kRgThreads);
+  cfg.dynamicSmemBytes = static_cast<size_t>(rg_smem(GRAD));
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  const int shares = ctas * kRgWarps, per = (p.V / Vec<ELT>::N + shares - 1) / shares;
+  return cudaLaunchKernelEx(&cfg, token_ring_kernel<ELT, ENT, GRAD>, p, rows, static_cast<int>(window), per);
+}
+
+template <int ELT, bool ENT, bool GRAD>
+cudaError_t launch_rows(const RowParams& p, int rows, cudaStream_t s) {
+  if (static_cast<long long>(p.V) * ELT > kRgMinRow) return launch_ring<ELT, ENT, GRAD>(p, rows, s);
+  token_row_kernel<ELT, ENT, GRAD><<<static_cast<unsigned>(rows), kRowThreads, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
 template <int ELT>
 cudaError_t launch_rows(const RowParams& p, int rows, bool ent, cudaStream_t s) {
-  const unsigned n = static_cast<unsigned>(rows);
-  if (p.grad) {
-    if (ent) token_row_kernel<ELT, true, true><<<n, kRowThreads, 0, s>>>(p);
-    else token_row_kernel<ELT, false, true><<<n, kRowThreads, 0, s>>>(p);
-  } else {
-    if (ent) token_row_kernel<ELT, true, false><<<n, kRowThreads, 0, s>>>(p);
-    else token_row_kernel<ELT, false, false><<<n, kRowThreads, 0, s>>>(p);
-  }
-  return cudaGetLastError();
+  if (p.grad) return ent ? launch_rows<ELT, true, true>(p, rows, s) : launch_rows<ELT, false, true>(p, rows, s);
+  return ent ? launch_rows<ELT, true, false>(p, rows, s) : launch_rows<ELT, false, false>(p, rows, s);
 }
 
 // The sizes, types, temperature and rows that every entry point here checks
@@ -219,6 +652,7 @@ RowParams row_params(int t_len, int V, const void* logits, const int32_t* tokens
   p.same_shift = reinterpret_cast<uintptr_t>(logits) % 16 == reinterpret_cast<uintptr_t>(grad) % 16;
   p.c2 = static_cast<float>(1.4426950408889634 / static_cast<double>(temperature));
   p.inv_T = 1.f / temperature;
+  p.wait_limit_ns = kd_wait_limit_ns();
   return p;
 }
 

@@ -110,36 +110,38 @@ __device__ __forceinline__ float tok_below(float z, float m, float inv_T) {
 }
 
 struct TokRow {
-  float M, Z;          // the row's maximum and its sum about it
+  float M, Z, rZ;      // the row's maximum, its sum about it, and 1 / Z
   float rest, px;      // 1 - p(x), p(x)
-  float logp, lse;
-  float U, H;          // sum p (z - M) / T, the entropy
-  int valid;
+  float logp, log_Z;
+  float U;             // sum p (z - M) / T
+  bool valid;
+  __device__ __forceinline__ float entropy() const { return __fsub_rn(log_Z, U); }
+  __device__ __forceinline__ float lse(float inv_T) const { return valid ? __fmaf_rn(M, inv_T, log_Z) : NAN; }
 };
 
 template <bool ENT>
 __device__ __forceinline__ TokRow tok_row(const TokPart& part, float zx, float inv_T) {
   TokRow R;
-  R.M = fmaxf(part.m, zx);
+  const bool top = zx >= part.m;           // the token is the likeliest
+  R.M = top ? zx : part.m;
   R.valid = part.s == part.s && zx == zx && R.M > -INFINITY && R.M < INFINITY;
-  const float dr = part.m > -INFINITY ? tok_below(part.m, R.M, inv_T) : -INFINITY;
-  const float dx = zx > -INFINITY ? tok_below(zx, R.M, inv_T) : -INFINITY;
-  const float fr = dr == 0.f ? 1.f : expf(dr), ex = dx == 0.f ? 1.f : expf(dx);
-  const float rest = __fmul_rn(part.s, fr);
+  const float low = top ? part.m : zx;
+  const float d = low > -INFINITY ? tok_below(low, R.M, inv_T) : -INFINITY;
+  const float e = expf(d);
+  const float rest = top ? __fmul_rn(part.s, e) : part.s, ex = top ? 1.f : e;
   R.Z = __fadd_rn(rest, ex);
-  const float log_Z = dx == 0.f ? log1pf(rest) : logf(R.Z);
-  R.rest = __fdiv_rn(rest, R.Z);
-  R.px = __fdiv_rn(ex, R.Z);
-  R.logp = __fsub_rn(dx, log_Z);
-  R.lse = __fmaf_rn(R.M, inv_T, log_Z);
-  R.U = R.H = 0.f;
+  R.rZ = __fdiv_rn(1.f, R.Z);
+  R.log_Z = top ? log1pf(rest) : logf(R.Z);
+  R.rest = __fmul_rn(rest, R.rZ);
+  R.px = __fmul_rn(ex, R.rZ);
+  R.logp = R.valid ? __fsub_rn(top ? 0.f : d, R.log_Z) : NAN;
+  R.U = 0.f;
   if (ENT) {
-    float u = fr > 0.f ? __fmul_rn(fr, __fmaf_rn(part.a, kLn2, part.s * dr)) : 0.f;
-    if (ex > 0.f) u = __fmaf_rn(ex, dx, u);
-    R.U = __fdiv_rn(u, R.Z);
-    R.H = __fsub_rn(log_Z, R.U);
+    float u = 0.f;
+    if (e > 0.f) u = top ? __fmul_rn(e, __fmaf_rn(part.a, kLn2, part.s * d)) : __fmul_rn(e, d);
+    if (!top) u = __fmaf_rn(part.a, kLn2, u);
+    R.U = R.valid ? __fmul_rn(u, R.rZ) : NAN;
   }
-  if (!R.valid) R.logp = R.lse = R.H = NAN;
   return R;
 }
 
@@ -157,14 +159,19 @@ __device__ __forceinline__ void tok_check(TokGrad& G, bool valid) {
   G.alpha = G.at_token = NAN;
 }
 
+template <bool ENT>
 __device__ __forceinline__ TokGrad tok_grad(const TokRow& R, float g, float h, float inv_T) {
-  const float q = __fdiv_rn(inv_T, R.Z);
+  const float q = __fmul_rn(inv_T, R.rZ);
   TokGrad G;
   G.base = R.M;
   G.k = 0.f;
-  G.alpha = __fmul_rn(q, __fmaf_rn(h, R.U, -g));
-  G.gamma = -h * kLn2 * q;
-  const float own = R.px > 0.f ? h * R.px * __fadd_rn(R.logp, R.H) : 0.f;
+  G.alpha = __fmul_rn(q, ENT ? __fmaf_rn(h, R.U, -g) : -g);
+  G.gamma = 0.f;
+  float own = 0.f;
+  if (ENT) {
+    G.gamma = -h * kLn2 * q;
+    if (R.px > 0.f) own = h * R.px * __fadd_rn(R.logp, R.entropy());
+  }
   G.at_token = __fmul_rn(inv_T, __fmaf_rn(g, R.rest, -own));
   tok_check(G, R.valid);
   return G;
@@ -187,9 +194,9 @@ __device__ __forceinline__ TokGrad tok_grad_from(float zx, float logp, float lse
   return G;
 }
 
-// A vector's gradients; x_at is the token's place in it, or outside 0..N-1.
+// A vector's gradients, as if none of it were the row's token.
 template <int ELT, bool ENT>
-__device__ __forceinline__ uint4 tok_vec_grad(const uint4& w, const TokGrad& G, float c2, int x_at) {
+__device__ __forceinline__ uint4 tok_vec_grad(const uint4& w, const TokGrad& G, float c2) {
   using VT = Vec<ELT>;
   constexpr int N = VT::N;
   const f2 bb = pack2(G.base, G.base), cc = pack2(c2, c2), kk = pack2(G.k, G.k);
@@ -202,11 +209,6 @@ __device__ __forceinline__ uint4 tok_vec_grad(const uint4& w, const TokGrad& G, 
     const f2 t = fma2(sub2(z[i], bb), cc, kk);
     const f2 f = ENT ? fma2(TokSum<ELT, ENT>::floored(t), gg, aa) : aa;
     unpack2(mul2(exp2_2(t), f), d[2 * i], d[2 * i + 1]);
-  }
-  if (static_cast<unsigned>(x_at) < static_cast<unsigned>(N)) {
-#pragma unroll
-    for (int e = 0; e < N; ++e)
-      if (e == x_at) d[e] = G.at_token;
   }
   return VT::pack(d);
 }
