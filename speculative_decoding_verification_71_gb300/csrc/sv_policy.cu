@@ -100,8 +100,8 @@ __device__ __forceinline__ void policy_row(const PolicyArgs& P, const PolicyRow&
 constexpr int kRowThreads = 512, kRowWarps = kRowThreads / 32;
 
 template <int ELT>
-__device__ __forceinline__ void zero_row(unsigned char* grad, int V, int shift, int nvec, int same_shift) {
-  for (int v = threadIdx.x; v < nvec; v += blockDim.x)
+__device__ __forceinline__ void zero_row(unsigned char* grad, int V, int shift, int nvec, int same_shift, int threads) {
+  for (int v = threadIdx.x; v < nvec; v += threads)
     store_edge<ELT>(grad, V, v * Vec<ELT>::N - shift, same_shift, make_uint4(0, 0, 0, 0));
 }
 
@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(kRowThreads) token_row_kernel(const __grid_con
       if (P.lse) P.lse[r] = -INFINITY;
       if (P.row_loss) P.row_loss[r] = 0.f;
     }
-    if (GRAD) zero_row<ELT>(grad, P.V, shift, nvec, P.same_shift);
+    if (GRAD) zero_row<ELT>(grad, P.V, shift, nvec, P.same_shift, kRowThreads);
     return;
   }
   const float zx = x < P.V ? load_elem<ELT>(row, x) : NAN;
@@ -169,130 +169,151 @@ __global__ void __launch_bounds__(kRowThreads) token_row_kernel(const __grid_con
   }
 }
 
+constexpr int kRgGradWorkers = 16;
 // ---- long rows: streamed through shared memory, where they stay for the gradient
 //
-// A row goes to a cluster of 1 to 8 CTAs of 8 warps and is split evenly over
-// their warps.  Each warp streams its share through a ring of its own, of 4 KB
-// slots: it asks for the copies itself, so nothing is handed from warp to warp.
-// Few warps with much work each: what a slot and a row cost besides their logits
-// is paid by every warp.  It sums its share as it lands and, once the warps
-// (and through distributed shared memory the CTAs) have joined their sums,
-// reads it a second time from the ring, writes the gradient and asks for the next
-// row's vectors in each slot that it leaves: every logit crosses HBM once and
-// every gradient value once, and the loads run ahead through the row's end.
-// That takes an SM's shared memory, seven slots a warp.  Without a gradient a slot
-// is filled again as soon as it is read, and two CTAs of three slots a warp share
-// an SM, one streaming while the other puts a row's numbers together.
+// A row goes to a cluster of 1 to 8 CTAs, a part to each.  A producer warp streams
+// the part through a ring of 16 KB slots, worker warps sum it as it lands, and a
+// warp of its own puts the row's numbers together from their sums (and through
+// distributed shared memory from the other CTAs'), so that the workers need not:
+// with every warp working them out a row cost each 1780 instructions besides its
+// logits.  For the gradient the slots keep the row: the workers read them a second
+// time once the numbers are there, and give them back to the producer one by one.
+// Meanwhile they sum the next row, where two parts fit the ring.  So every logit
+// crosses HBM once and every gradient value once, and neither the loads nor the
+// workers stop at a row's end.  That takes an SM's shared memory.  Without a
+// gradient a slot is given back as soon as it is read, and two CTAs share an SM.
 //
 // Rows with a token are dealt to the clusters in turn, whatever lies between them
 // (a batch of padded rollouts dealt by row number keeps some clusters a third
 // longer at work): every CTA counts the tokens of a window of rows and lists its
 // own.  Rows without one are zero-filled by single CTAs in between.
 //
-// Every wait has a limit.  A warp whose wait for a slot expires touches its ring
-// no more: its sums and gradients are NaN from there on, and so are all later rows
-// of its cluster.  A CTA whose cluster does not answer takes the row and all later
-// ones as NaN.  No copy is in flight when a CTA leaves.
-constexpr int kRgWarps = 8, kRgThreads = kRgWarps * 32;
-constexpr int kRgPerLane = 8;                               // vectors per lane and slot
-constexpr int kRgSlotVecs = kRgPerLane * 32, kRgSlotBytes = kRgSlotVecs * 16;
-constexpr int kRgKept = 7, kRgPassed = 3;                   // slots of a warp with and without a gradient
+// Every wait has a limit.  A worker thread whose wait for a slot expires touches the
+// ring no more: its sums and gradients are NaN from there on, and so are all later
+// rows of its cluster.  A CTA whose cluster does not answer takes the row and all
+// later ones as NaN.  The producer, which then waits in vain for slots, leaves
+// last, when its copies have landed.
+template <bool GRAD>
+struct Rg {
+  static constexpr int kWorkers = GRAD ? kRgGradWorkers : 8;
+  static constexpr int kPerLane = 32 / kWorkers;             // vectors per lane and slot
+  static constexpr int kWork = kWorkers * 32, kThreads = kWork + 64;   // + the producer's and the row's warp
+  static constexpr int kSlotVecs = kWork * kPerLane, kSlotBytes = kSlotVecs * 16;
+  static constexpr int kSlots = GRAD ? 14 : 6;
+  static constexpr int kPerSm = GRAD ? 1 : 2;                // CTAs
+};
+constexpr int kRgSlotVecs = 1024, kRgSlotBytes = kRgSlotVecs * 16;
+constexpr int kRgMaxWorkers = 16, kRgMaxSlots = 14;
 constexpr int kRgMaxCtas = 8;
 constexpr int kRgWindow = 8192;                             // rows whose tokens are looked at together
 constexpr int kRgLive = 448, kRgDead = 64;                  // of which a cluster, a CTA gets so many at most
 constexpr int kRgSms = 152;
 constexpr int kRgMinRow = 32 * 1024;                        // bytes of a row that is streamed
-constexpr int kRgPart = 160 * 1024;                         // a CTA's part for the gradient at most
+constexpr int kRgPart = 96 * 1024;                          // a CTA's part for the gradient, if the row allows
 constexpr int kRgMinPart = 16 * 1024;                       // and where a row is split for want of rows
-static_assert((kTokMaxRow + kRgMaxCtas - 1) / kRgMaxCtas <= kRgPart, "the longest row fits a cluster");
-static_assert(kRgPart / 16 + kRgWarps <= kRgWarps * (kRgKept - 1) * kRgSlotVecs, "a part fits the rings");
 constexpr long long kRgJoinLimitNs = 4 * kDrainLimitNs;     // a CTA's part comes within an expired wait
+constexpr long long kRgRowLimitNs = 2 * kRgJoinLimitNs;     // and a row's numbers within that one
+constexpr int kRgNoRow = 0x7fffffff;
+static_assert(Rg<true>::kSlotBytes == kRgSlotBytes && Rg<false>::kSlotBytes == kRgSlotBytes, "slots");
+static_assert((kTokMaxRow / kRgMaxCtas + kRgSlotBytes - 1) / kRgSlotBytes < Rg<true>::kSlots, "the longest row fits a cluster");
 
 struct RgShared {
-  uint64_t full[kRgWarps][kRgKept];
-  uint64_t joined[2];            // the cluster's parts of a row are here, by row parity as what follows
+  uint64_t full[kRgMaxSlots], empty[kRgMaxSlots];
+  uint64_t summed[2];            // the workers' sums of a row are here, by row parity as what follows
+  uint64_t joined[2];            // the CTAs' are
+  uint64_t ready[2];             // what the gradient takes is (without one: the sums have been read)
   uint4 part[2][kRgMaxCtas];     // the CTAs' sums
-  TokPart warp[2][kRgWarps];     // the warps' sums
-  int counts[kRgWarps];          // rows with and without a token in a warp's strip of the window
+  TokPart warp[2][kRgMaxWorkers];
+  TokGrad grad[2];
+  int counts[kRgMaxWorkers];     // rows with and without a token in a warp's strip of the window
   int failed;                    // the first row in which the cluster did not answer, or kRgNoRow
   unsigned short live[kRgLive], dead[kRgDead];
 };
-constexpr int kRgNoRow = 0x7fffffff;
 constexpr int kRgRingAt = (static_cast<int>(sizeof(RgShared)) + 127) / 128 * 128;
-constexpr int rg_smem(bool grad) { return kRgRingAt + kRgWarps * (grad ? kRgKept : kRgPassed) * kRgSlotBytes; }
-static_assert(rg_smem(true) <= 227 * 1024 && 2 * (rg_smem(false) + 1024) <= 228 * 1024, "an SM's shared memory");
+template <bool GRAD>
+constexpr int rg_smem() { return kRgRingAt + Rg<GRAD>::kSlots * kRgSlotBytes; }
+static_assert(rg_smem<true>() <= 227 * 1024 && 2 * (rg_smem<false>() + 1024) <= 228 * 1024, "an SM's shared memory");
 
-// A warp's share of a row's whole vectors: the place of its first one, which of
+// A CTA's part of a row's whole vectors: the place of its first one, which of
 // the row's vectors that is, and their number (the row's ends are taken apart).
-struct RgShare {
+struct RgPart {
   const unsigned char* at;
   int first, n, shift, nvec;
   template <int ELT>
-  __device__ __forceinline__ static RgShare of(const unsigned char* row, int V, int per, int index) {
+  __device__ __forceinline__ static RgPart of(const unsigned char* row, int V, int per, int rank) {
     constexpr int N = Vec<ELT>::N;
-    RgShare t;
+    RgPart t;
     t.shift = row_shift<ELT>(row);
     t.nvec = row_vecs<ELT>(V, t.shift);
     const int head = t.shift ? 1 : 0;
     const int all = t.nvec - head - ((V + t.shift) % N && t.nvec > head ? 1 : 0);
-    const int from = min(all, index * per);
+    const int from = min(all, rank * per);
     t.first = head + from;
-    t.n = min(all, index * per + per) - from;
+    t.n = min(all, rank * per + per) - from;
     t.at = row + (static_cast<long long>(t.first) * N - t.shift) * ELT;
     return t;
   }
 };
 
-__device__ __forceinline__ bool rg_wait(uint64_t* bar, uint32_t parity, long long limit_ns) {
-  return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, limit_ns));
-}
-
 // How many of the numbers below `x` are `mine` modulo `of`.
 __device__ __forceinline__ long long rg_own(long long x, int mine, int of) { return x > mine ? (x - mine + of - 1) / of : 0; }
 
-// `window`: rows whose tokens are looked at together; `per`: vectors of a warp's share.
+// `window`: rows whose tokens are looked at together; `per`: vectors of a CTA's
+// part at most; `ahead`: two parts fit the ring.
 template <int ELT, bool ENT, bool GRAD>
-__global__ void __launch_bounds__(kRgThreads, GRAD ? 1 : 2) token_ring_kernel(const __grid_constant__ RowParams P, int rows,
-                                                                              int window, int per) {
-  constexpr int kRgSlots = GRAD ? kRgKept : kRgPassed;
+__global__ void __launch_bounds__(Rg<GRAD>::kThreads, Rg<GRAD>::kPerSm)
+    token_ring_kernel(const __grid_constant__ RowParams P, int rows, int window, int per, int ahead) {
   using VT = Vec<ELT>;
-  constexpr int N = VT::N;
+  using R_ = Rg<GRAD>;
+  constexpr int N = VT::N, kSlots = R_::kSlots, kWorkers = R_::kWorkers, kWork = R_::kWork, U = R_::kPerLane;
   extern __shared__ __align__(1024) unsigned char smem[];
   RgShared& sh = *reinterpret_cast<RgShared*>(smem);
+  unsigned char* ring = smem + kRgRingAt;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  unsigned char* ring = smem + kRgRingAt + warp * (kRgSlots * kRgSlotBytes);
-  uint64_t* full = sh.full[warp];
   const int ctas = cluster_ctas(), rank = cluster_rank();
   const int cluster = blockIdx.x / ctas, clusters = gridDim.x / ctas;
-  if (lane < kRgSlots) mbar_init(&full[lane], 1);
   if (tid == 0) {
-    for (int b = 0; b < 2; ++b) mbar_init(&sh.joined[b], 1);
+    for (int s = 0; s < kSlots; ++s) {
+      mbar_init(&sh.full[s], 1);
+      mbar_init(&sh.empty[s], kWorkers);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&sh.summed[b], kWorkers);
+      mbar_init(&sh.joined[b], 1);
+      mbar_init(&sh.ready[b], 1);
+    }
     sh.failed = kRgNoRow;
+    fence_mbar_init();
   }
-  fence_mbar_init();
   if (ctas > 1) cluster_sync();   // the others' barriers are set up too
+  else __syncthreads();
   if (P.row_loss) grid_dependents_launch();   // the sum of the rows may take its place on an SM
 
-  const uint64_t first_out = evict_first_policy();
-  int slot = 0, ask_slot = 0;     // the next one to take and to ask for
-  uint32_t round = 0;             // the parity of `slot`'s copies
-  unsigned asked = 0;
+  // every role's place in the ring, and the parity of that slot's copies
+  int slot = 0;
+  uint32_t round = 0;
+  auto step = [&](int& s, uint32_t& odd) {
+    if (++s == kSlots) s = 0, odd ^= 1;
+  };
+  unsigned copies = 0;            // (producer)
   unsigned turn = 0;              // rows with a token
-  int armed = -1;                 // (warp 0) the last turn whose parts are expected
-  bool closed = false;            // (warp 0) no more are
-  bool dead = false;              // a wait of this warp has expired
+  bool dead = false;              // a wait of this thread has expired; the producer has given up
+  bool alone = false;             // (the row's warp) the cluster did not answer
+  unsigned alone_turn = 0;
   long long seen_live = 0, seen_dead = 0;
   for (long long w0 = 0; w0 < rows; w0 += window) {
     // ---- which rows of the window are this cluster's, and this CTA's to fill
     const int in_window = static_cast<int>(rows - w0 < window ? rows - w0 : window);
-    const int words = (in_window + 32 * kRgWarps - 1) / (32 * kRgWarps);   // 32 rows each, a lane for each
+    const int words = (in_window + kWork - 1) / kWork;      // 32 rows each, a lane for each
     uint32_t live_bits = 0, dead_bits = 0;
-    for (int j = 0; j < words; ++j) {
-      const int at = (warp * words + j) * 32 + lane;
-      const bool in = at < in_window, has = in && P.tokens[w0 + at] >= 0;
-      const uint32_t l = __ballot_sync(0xffffffffu, has), d = __ballot_sync(0xffffffffu, in && !has);
-      if (lane == j) live_bits = l, dead_bits = d;
-    }
+    if (warp < kWorkers)
+      for (int j = 0; j < words; ++j) {
+        const int at = (warp * words + j) * 32 + lane;
+        const bool in = at < in_window, has = in && P.tokens[w0 + at] >= 0;
+        const uint32_t l = __ballot_sync(0xffffffffu, has), d = __ballot_sync(0xffffffffu, in && !has);
+        if (lane == j) live_bits = l, dead_bits = d;
+      }
     const int mine = __popc(live_bits) | __popc(dead_bits) << 16;
     int upto = mine;
 #pragma unroll
@@ -301,9 +322,9 @@ __global__ void __launch_bounds__(kRgThreads, GRAD ? 1 : 2) token_ring_kernel(co
       if (lane >= o) upto += up;
     }
     __syncthreads();              // the last window's lists have been read
-    if (lane == 31) sh.counts[warp] = upto;
+    if (lane == 31 && warp < kWorkers) sh.counts[warp] = upto;
     __syncthreads();
-    const int count = lane < kRgWarps ? sh.counts[lane] : 0;
+    const int count = lane < kWorkers ? sh.counts[lane] : 0;
     const int total = static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(count)));
     const int before = static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(lane < warp ? count : 0))) + upto - mine;
     const long long own_live = rg_own(seen_live, cluster, clusters), own_dead = rg_own(seen_dead, blockIdx.x, gridDim.x);
@@ -330,200 +351,236 @@ __global__ void __launch_bounds__(kRgThreads, GRAD ? 1 : 2) token_ring_kernel(co
     const int n_dead = static_cast<int>(rg_own(seen_dead, blockIdx.x, gridDim.x) - own_dead);
     __syncthreads();
 
-    // ---- the copies: the next slot's vectors of this warp's shares, row after row
-    int ask = 0, ask_left = 0;    // the row after the one whose vectors are asked for, and what is left of that one
-    const unsigned char* ask_at = nullptr;
-    auto ask_one = [&] {
-      while (ask_left == 0) {
-        if (ask >= n_live) return false;
-        const RgShare t = RgShare::of<ELT>(P.logits + (w0 + sh.live[ask++]) * P.V * ELT, P.V, per, rank * kRgWarps + warp);
-        ask_at = t.at;
-        ask_left = t.n;
+    if (warp == kWorkers) {
+      // ---- the producer
+      const uint64_t first_out = evict_first_policy();
+      for (int i = 0; i < n_live && !dead; ++i) {
+        const RgPart t = RgPart::of<ELT>(P.logits + (w0 + sh.live[i]) * P.V * ELT, P.V, per, rank);
+        for (int v = 0; v < t.n && !dead; v += kRgSlotVecs) {
+          int ok = 1;
+          if (lane == 0) ok = mbar_wait_bounded(&sh.empty[slot], round ^ 1, kDrainLimitNs) ? 1 : 0;
+          dead = !__shfl_sync(0xffffffffu, ok, 0);
+          if (dead) break;        // as a worker has
+          if (lane == 0) {
+            const uint32_t bytes = static_cast<uint32_t>(min(kRgSlotVecs, t.n - v)) * 16u;
+            mbar_expect_tx(&sh.full[slot], bytes);
+            bulk_load_hint(ring + slot * kRgSlotBytes, t.at + static_cast<long long>(v) * 16, bytes, &sh.full[slot], first_out);
+          }
+          ++copies;
+          step(slot, round);
+        }
       }
-      const int n = min(ask_left, kRgSlotVecs);
-      if (lane == 0) {
-        const uint32_t bytes = static_cast<uint32_t>(n) * 16u;
-        mbar_expect_tx(&full[ask_slot], bytes);
-        bulk_load_hint(ring + ask_slot * kRgSlotBytes, ask_at, bytes, &full[ask_slot], first_out);
-      }
-      ask_at += static_cast<long long>(n) * 16;
-      ask_left -= n;
-      ++asked;
-      if (++ask_slot == kRgSlots) ask_slot = 0;
-      return true;
-    };
-    if (!dead)
-      for (int s = 0; s < kRgSlots; ++s)
-        if (!ask_one()) break;
+      continue;
+    }
 
-    int next_x = n_live ? P.tokens[w0 + sh.live[0]] : 0;
-    float next_zx = n_live && next_x < P.V ? load_elem<ELT>(P.logits + (w0 + sh.live[0]) * P.V * ELT, next_x) : NAN;
+    if (warp == kWorkers + 1) {
+      // ---- the row's warp: the next row's token and logit are loaded while it waits
+      int x = n_live ? P.tokens[w0 + sh.live[0]] : 0;
+      float zx = n_live && x < P.V ? load_elem<ELT>(P.logits + (w0 + sh.live[0]) * P.V * ELT, x) : NAN;
+      for (int i = 0; i < n_live; ++i, ++turn) {
+        const long long r = w0 + sh.live[i], r_next = i + 1 < n_live ? w0 + sh.live[i + 1] : r;
+        const int par = turn & 1;
+        const uint32_t phase = turn >> 1 & 1;
+        PolicyRow mine_row{};
+        if (P.row_loss) mine_row = PolicyRow::of(P.policy, static_cast<int>(r), P.t_len);
+        const int x_next = P.tokens[r_next];
+        bool here = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.summed[par], phase, kRgRowLimitNs));
+        const float zx_next = x_next < P.V ? load_elem<ELT>(P.logits + r_next * P.V * ELT, x_next) : NAN;
+        TokPart part = tok_join<ENT>(lane < kWorkers ? sh.warp[par][lane] : tok_none(), P.c2);
+        if (!GRAD && lane == 0) mbar_arrive(&sh.ready[par]);   // the row after the next may take the sums' place
+        // (the token's logit is part of what the others wait for: in place they may write over it afterwards)
+        if (!here || zx != zx) part.s = NAN;
+        if (ctas > 1) {
+          TokPart other = tok_none();
+          if (!alone) {
+            if (lane == 0) mbar_expect_tx(&sh.joined[par], static_cast<uint32_t>(ctas) * 16u);
+            if (lane < ctas)
+              st_async(peer(&sh.part[par][rank], lane),
+                       make_uint4(__float_as_uint(part.m), __float_as_uint(part.s), __float_as_uint(part.a), 0u),
+                       peer(&sh.joined[par], lane));
+            alone = !__all_sync(0xffffffffu, mbar_wait_bounded(&sh.joined[par], phase, kRgJoinLimitNs));
+            if (alone) {
+              // another CTA may still get here and on to the next row, where it
+              // waits in vain: what it sends until then is waited for at the end
+              if (lane == 0) mbar_expect_tx(&sh.joined[par ^ 1], static_cast<uint32_t>(ctas) * 16u);
+              alone_turn = turn;
+            } else if (lane < ctas) {
+              const uint4 y = sh.part[par][lane];
+              other = TokPart{__uint_as_float(y.x), __uint_as_float(y.y), __uint_as_float(y.z)};
+            }
+          }
+          part = tok_join<ENT>(other, P.c2);
+          here = !alone;
+        }
+        if (!here) {
+          part.s = NAN;
+          if (lane == 0) atomicMin(&sh.failed, static_cast<int>(r));
+        }
+        const TokRow row = tok_row<ENT>(part, zx, P.inv_T);
+        float loss = 0.f, slope = 0.f;
+        if (P.row_loss) policy_row<ENT>(P.policy, mine_row, row, loss, slope);
+        if (GRAD) {
+          const TokGrad G = tok_grad<ENT>(row, mine_row.weight * slope, ENT ? -P.policy.entropy * mine_row.weight : 0.f, P.inv_T);
+          if (lane == 0) {
+            sh.grad[par] = G;
+            mbar_arrive(&sh.ready[par]);
+          }
+        }
+        if (lane == 0 && rank == 0) {
+          P.logp[r] = row.logp;
+          if (ENT && P.entropy) P.entropy[r] = row.entropy();
+          if (P.lse) P.lse[r] = row.lse(P.inv_T);
+          if (P.row_loss) P.row_loss[r] = loss;
+        }
+        x = x_next;
+        zx = zx_next;
+      }
+      continue;
+    }
+
+    // ---- the workers: row i summed, and the gradient of the row before (of row i
+    // itself where two do not fit)
+    int kept_slot = slot;         // where the row begins whose gradient is next
     int filled = 0;
-    for (int i = 0; i < n_live; ++i, ++turn) {
-      const long long r = w0 + sh.live[i];
-      const unsigned char* row = P.logits + r * P.V * ELT;
-      unsigned char* grad = GRAD ? P.grad + r * P.V * ELT : nullptr;
-      const RgShare t = RgShare::of<ELT>(row, P.V, per, rank * kRgWarps + warp);
-      const int par = turn & 1;
-      const uint32_t phase = turn >> 1 & 1;
-      const int x = next_x < P.V ? next_x : -(1 << 30);
-      const float zx = next_zx;
-      // what the row's numbers need is loaded while it is summed
-      const long long r_next = i + 1 < n_live ? w0 + sh.live[i + 1] : r;
-      next_x = P.tokens[r_next];
-      PolicyRow mine{};
-      if (P.row_loss) mine = PolicyRow::of(P.policy, static_cast<int>(r), P.t_len);
-
-      // ---- the sums of this warp's share, and by two threads of the row's ends
-      TokSum<ELT, ENT> sum;
-      int end = -1;
-      if (rank == 0 && tid == 0 && t.shift) end = 0;
-      if (rank == 0 && tid == 32 && (P.V + t.shift) % N && t.nvec > (t.shift ? 1 : 0)) end = t.nvec - 1;
-      uint4 end_vec = VT::neg_inf();
-      if (end >= 0) end_vec = load_row_vec<ELT>(row, P.V, t.shift, end);
-      // where x lies from the share's first vector on, and whether this lane reads it
-      const int x_vec = (x + t.shift) / N - t.first, x_in = (x + t.shift) % N;
-      const bool own_x = x_vec >= 0 && x_vec < t.n && x_vec % 32 == lane;
-      const int row_slot = slot;
-      for (int v = 0; v < t.n; v += kRgSlotVecs) {
-        const int n = t.n - v;
-        unsigned char* at = ring + slot * kRgSlotBytes;
-        if (!dead) dead = !rg_wait(&full[slot], round, P.wait_limit_ns);
-        if (++slot == kRgSlots) slot = 0, round ^= 1;
-        if (dead) continue;
-        if (own_x && x_vec >= v && x_vec < v + kRgSlotVecs) {   // out of the sum: this lane reads what it writes here
-          VT::store_scalar(at, (x_vec - v) * N + x_in, -INFINITY);
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // before the slot is filled again
-        }
-        const uint4* src = reinterpret_cast<const uint4*>(at) + lane;
-        if (n > kRgSlotVecs / 2) {
-          uint4 w[kRgPerLane];
-#pragma unroll
-          for (int k = 0; k < kRgPerLane; ++k) w[k] = n >= kRgSlotVecs || lane + k * 32 < n ? src[k * 32] : VT::neg_inf();
-          if (!GRAD) {
-            __syncwarp();
-            ask_one();
-          }
-          sum.add(w, P.c2);
-        } else {
-          uint4 w[kRgPerLane / 2];
-#pragma unroll
-          for (int k = 0; k < kRgPerLane / 2; ++k) w[k] = lane + k * 32 < n ? src[k * 32] : VT::neg_inf();
-          if (!GRAD) {
-            __syncwarp();
-            ask_one();
-          }
-          sum.add(w, P.c2);
-        }
-      }
-      if (end >= 0) {
-        uint4 one[1] = {end_vec};
-        tok_take_out<ELT>(one[0], x + t.shift - end * N);
-        sum.add(one, P.c2);
-      }
-      TokPart part = sum.part();
-      // (the token's logit is part of what the others wait for: in place they may write over it afterwards)
-      if (dead || zx != zx) part.s = NAN;
-      part = tok_join<ENT>(part, P.c2);
-      if (lane == 0) sh.warp[par][warp] = part;
-      __syncthreads();
-      part = tok_join<ENT>(lane < kRgWarps ? sh.warp[par][lane] : tok_none(), P.c2);
-      bool answered = true;
-      if (ctas > 1) {
-        const bool alone = *static_cast<volatile int*>(&sh.failed) != kRgNoRow;
-        if (warp == 0 && !closed) {
-          // (alone: others may still get here once, which is waited for at the end)
-          closed = alone;
-          if (lane == 0) mbar_expect_tx(&sh.joined[par], static_cast<uint32_t>(ctas) * 16u);
-          armed = static_cast<int>(turn);
-          if (!alone && lane < ctas)
-            st_async(peer(&sh.part[par][rank], lane),
-                     make_uint4(__float_as_uint(part.m), __float_as_uint(part.s), __float_as_uint(part.a), 0u),
-                     peer(&sh.joined[par], lane));
-        }
-        answered = !alone && rg_wait(&sh.joined[par], phase, kRgJoinLimitNs);
-        TokPart other = tok_none();
-        if (answered && lane < ctas) {
-          const uint4 y = sh.part[par][lane];
-          other = TokPart{__uint_as_float(y.x), __uint_as_float(y.y), __uint_as_float(y.z)};
-        }
-        if (!answered && lane == 0) atomicMin(&sh.failed, static_cast<int>(r));
-        part = tok_join<ENT>(other, P.c2);
-        if (!answered) part.s = NAN;
-      }
-      const TokRow R = tok_row<ENT>(part, zx, P.inv_T);
-      next_zx = next_x < P.V && next_x >= 0 ? load_elem<ELT>(P.logits + r_next * P.V * ELT, next_x) : NAN;
-      float loss = 0.f, slope = 0.f;
-      if (P.row_loss) policy_row<ENT>(P.policy, mine, R, loss, slope);
-      if (tid == 0 && rank == 0) {
-        P.logp[r] = R.logp;
-        if (ENT && P.entropy) P.entropy[r] = R.entropy();
-        if (P.lse) P.lse[r] = R.lse(P.inv_T);
-        if (P.row_loss) P.row_loss[r] = loss;
-      }
-
-      // ---- the gradient, from the ring
-      if (GRAD) {
-        const TokGrad G = tok_grad<ENT>(R, mine.weight * slope, ENT ? -P.policy.entropy * mine.weight : 0.f, P.inv_T);
-        unsigned char* out = grad + (static_cast<long long>(t.first) * N - t.shift) * ELT;
-        int from = row_slot;
+    int x_next = n_live ? P.tokens[w0 + sh.live[0]] : 0, x_before = 0;
+    const unsigned first_turn = turn;
+    for (int i = 0; i < n_live + (GRAD ? ahead : 0); ++i) {
+      int x_now = x_next;
+      if (i < n_live) {
+        const long long r = w0 + sh.live[i];
+        const unsigned char* row = P.logits + r * P.V * ELT;
+        const RgPart t = RgPart::of<ELT>(row, P.V, per, rank);
+        const int x = x_now < P.V ? x_now : -(1 << 30);
+        if (i + 1 < n_live) x_next = P.tokens[w0 + sh.live[i + 1]];
+        // where x lies from the part's first vector on, and whether this thread reads it
+        const int x_vec = (x + t.shift) / N - t.first;
+        const bool own_x = x_vec >= 0 && x_vec < t.n && x_vec % kWork == tid;
+        // the row's ends by two threads
+        const int end = rank ? -1 : tid == 0 && t.shift ? 0 : tid == 32 && (P.V + t.shift) % N && t.nvec > (t.shift ? 1 : 0) ? t.nvec - 1 : -1;
+        uint4 end_vec = VT::neg_inf();
+        if (end >= 0) end_vec = load_row_vec<ELT>(row, P.V, t.shift, end);
+        TokSum<ELT, ENT> sum;
         for (int v = 0; v < t.n; v += kRgSlotVecs) {
           const int n = t.n - v;
-          const uint4* src = reinterpret_cast<const uint4*>(ring + from * kRgSlotBytes) + lane;
-          if (++from == kRgSlots) from = 0;
-          uint4 w[kRgPerLane];
-#pragma unroll
-          for (int k = 0; k < kRgPerLane; ++k) w[k] = n >= kRgSlotVecs || lane + k * 32 < n ? src[k * 32] : VT::neg_inf();
-          if (dead) {            // (alpha is NaN)
-#pragma unroll
-            for (int k = 0; k < kRgPerLane; ++k) w[k] = VT::neg_inf();
+          unsigned char* at = ring + slot * kRgSlotBytes;
+          if (!dead) dead = !mbar_wait_bounded(&sh.full[slot], round, P.wait_limit_ns);
+          if (own_x && x_vec >= v && x_vec < v + kRgSlotVecs && !dead) {   // out of the sum: this thread reads what it writes here
+            VT::store_scalar(at, (x_vec - v) * N + (x + t.shift) % N, -INFINITY);
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // before the slot is filled again
           }
-          __syncwarp();
-          if (!dead) ask_one();
-          unsigned char* at = out + static_cast<long long>(v + lane) * 16;
-          if (P.same_shift && n >= kRgSlotVecs) {
+          const uint4* src = reinterpret_cast<const uint4*>(at) + tid;
+          uint4 w[U];
+          if (n >= kRgSlotVecs && !dead) {
 #pragma unroll
-            for (int k = 0; k < kRgPerLane; ++k) store_vec16(at + k * 512, tok_vec_grad<ELT, ENT>(w[k], G, P.c2));
+            for (int k = 0; k < U; ++k) w[k] = src[k * kWork];
           } else {
 #pragma unroll
-            for (int k = 0; k < kRgPerLane; ++k)
-              if (lane + k * 32 < n)
-                store_edge<ELT>(grad, P.V, (t.first + v + lane + k * 32) * N - t.shift, P.same_shift, tok_vec_grad<ELT, ENT>(w[k], G, P.c2));
+            for (int k = 0; k < U; ++k) w[k] = !dead && tid + k * kWork < n ? src[k * kWork] : VT::neg_inf();
+          }
+          if (!GRAD) {
+            __syncwarp();
+            if (lane == 0 && !dead) mbar_arrive(&sh.empty[slot]);
+          }
+          step(slot, round);
+          sum.add(w, P.c2);
+        }
+        if (end >= 0) {
+          uint4 one[1] = {end_vec};
+          tok_take_out<ELT>(one[0], x + t.shift - end * N);
+          sum.add(one, P.c2);
+        }
+        TokPart part = sum.part();
+        if (dead) part.s = NAN;
+        part = tok_join<ENT>(part, P.c2);
+        const unsigned at_turn = first_turn + static_cast<unsigned>(i);
+        const int par = at_turn & 1;
+        // (for the gradient the workers have waited for that row's numbers)
+        if (!GRAD && at_turn >= 2 && !mbar_wait_bounded(&sh.ready[par], (at_turn >> 1 & 1) ^ 1, kRgRowLimitNs)) dead = true;
+        if (lane == 0) {
+          sh.warp[par][warp] = part;
+          mbar_arrive(&sh.summed[par]);
+        }
+      }
+      if (GRAD && i >= ahead) {
+        const long long r = w0 + sh.live[i - ahead];
+        const unsigned at_turn = first_turn + static_cast<unsigned>(i - ahead);
+        const RgPart t = RgPart::of<ELT>(P.logits + r * P.V * ELT, P.V, per, rank);
+        unsigned char* grad = P.grad + r * P.V * ELT;
+        const int x_row = ahead ? x_before : x_now;
+        const int x = x_row < P.V ? x_row : -(1 << 30), x_vec = (x + t.shift) / N - t.first;
+        const int end = rank ? -1 : tid == 0 && t.shift ? 0 : tid == 32 && (P.V + t.shift) % N && t.nvec > (t.shift ? 1 : 0) ? t.nvec - 1 : -1;
+        uint4 end_vec = VT::neg_inf();
+        if (end >= 0) end_vec = load_row_vec<ELT>(P.logits + r * P.V * ELT, P.V, t.shift, end);
+        const bool here = mbar_wait_bounded(&sh.ready[at_turn & 1], at_turn >> 1 & 1, kRgRowLimitNs);
+        TokGrad G = sh.grad[at_turn & 1];
+        if (!here) {
+          atomicMin(&sh.failed, static_cast<int>(r));
+          dead = true;
+        }
+        if (dead) G.alpha = G.at_token = NAN;
+        unsigned char* out = grad + (static_cast<long long>(t.first) * N - t.shift) * ELT + tid * 16;
+        for (int v = 0; v < t.n; v += kRgSlotVecs, out += kRgSlotBytes) {
+          const int n = t.n - v;
+          const uint4* src = reinterpret_cast<const uint4*>(ring + kept_slot * kRgSlotBytes) + tid;
+          uint4 w[U];
+          if (n >= kRgSlotVecs && !dead) {
+#pragma unroll
+            for (int k = 0; k < U; ++k) w[k] = src[k * kWork];
+          } else {
+#pragma unroll
+            for (int k = 0; k < U; ++k) w[k] = !dead && tid + k * kWork < n ? src[k * kWork] : VT::neg_inf();
+          }
+          __syncwarp();
+          if (lane == 0 && !dead) mbar_arrive(&sh.empty[kept_slot]);
+          if (++kept_slot == kSlots) kept_slot = 0;
+          if (P.same_shift && n >= kRgSlotVecs) {
+#pragma unroll
+            for (int k = 0; k < U; ++k) store_vec16(out + k * kWork * 16, tok_vec_grad<ELT, ENT>(w[k], G, P.c2));
+          } else {
+#pragma unroll
+            for (int k = 0; k < U; ++k)
+              if (tid + k * kWork < n)
+                store_edge<ELT>(grad, P.V, (t.first + v + tid + k * kWork) * N - t.shift, P.same_shift, tok_vec_grad<ELT, ENT>(w[k], G, P.c2));
           }
         }
         if (end >= 0) store_edge<ELT>(grad, P.V, end * N - t.shift, P.same_shift, tok_vec_grad<ELT, ENT>(end_vec, G, P.c2));
         // the token's own after its vector's, by the same thread
-        if (own_x || (end >= 0 && (x + t.shift) / N == end && x >= 0)) VT::store_rounded(grad, x, G.at_token);
+        if ((x_vec >= 0 && x_vec < t.n && x_vec % kWork == tid) || (end >= 0 && x >= 0 && (x + t.shift) / N == end))
+          VT::store_rounded(grad, x, G.at_token);
         // rows without a token, as many as there are for each row with one
-        for (; static_cast<long long>(filled) * n_live < static_cast<long long>(i + 1) * n_dead; ++filled) {
+        for (; static_cast<long long>(filled) * n_live < static_cast<long long>(i + 1 - ahead) * n_dead; ++filled) {
           unsigned char* zero = P.grad + (w0 + sh.dead[filled]) * P.V * ELT;
           const int shift = row_shift<ELT>(zero);
-          zero_row<ELT>(zero, P.V, shift, row_vecs<ELT>(P.V, shift), 1);
+          zero_row<ELT>(zero, P.V, shift, row_vecs<ELT>(P.V, shift), 1, kWork);
         }
       }
+      x_before = x_now;
     }
+    turn += static_cast<unsigned>(n_live);
     if (GRAD)
       for (; filled < n_dead; ++filled) {
         unsigned char* zero = P.grad + (w0 + sh.dead[filled]) * P.V * ELT;
         const int shift = row_shift<ELT>(zero);
-        zero_row<ELT>(zero, P.V, shift, row_vecs<ELT>(P.V, shift), 1);
+        zero_row<ELT>(zero, P.V, shift, row_vecs<ELT>(P.V, shift), 1, kWork);
       }
   }
   // ---- no copy is left in flight, and nothing on its way to a CTA that has left
-  if (dead && lane == 0)
-    for (unsigned k = asked > kRgSlots ? asked - kRgSlots : 0; k < asked; ++k)
-      mbar_wait_bounded(&full[k % kRgSlots], k / kRgSlots & 1, kDrainLimitNs);
+  if (warp == kWorkers && lane == 0)
+    for (unsigned k = copies > kSlots ? copies - kSlots : 0; k < copies; ++k)
+      mbar_wait_bounded(&sh.full[k % kSlots], k / kSlots & 1, kDrainLimitNs);
   if (ctas > 1) {
     cluster_sync();
-    if (sh.failed != kRgNoRow && tid == 0) {
-      for (int k = armed > 0 ? armed - 1 : 0; k <= armed; ++k)
-        mbar_wait_bounded(&sh.joined[k & 1], static_cast<uint32_t>(k >> 1 & 1), kDrainLimitNs);
-      // the row may have been put together by the others before
-      P.logp[sh.failed] = NAN;
-      if (P.entropy) P.entropy[sh.failed] = NAN;
-      if (P.lse) P.lse[sh.failed] = NAN;
-      if (P.row_loss) P.row_loss[sh.failed] = NAN;
-    }
+    if (alone)
+      for (unsigned k = alone_turn; k < alone_turn + 2; ++k) mbar_wait_bounded(&sh.joined[k & 1], k >> 1 & 1, kDrainLimitNs);
+  } else {
+    __syncthreads();
+  }
+  // a row that the others may have put together before
+  if (tid == 0 && sh.failed != kRgNoRow) {
+    P.logp[sh.failed] = NAN;
+    if (P.entropy) P.entropy[sh.failed] = NAN;
+    if (P.lse) P.lse[sh.failed] = NAN;
+    if (P.row_loss) P.row_loss[sh.failed] = NAN;
   }
 }
 
@@ -551,7 +608,7 @@ __global__ void __launch_bounds__(kRowThreads) token_grad_kernel(const __grid_co
                       ENT ? P.d_entropy[r] : 0.f, P.inv_T);
   }
   __syncthreads();               // (in place: every thread has the token's logit)
-  if (G.zero()) zero_row<ELT>(grad, P.V, shift, nvec, P.same_shift);
+  if (G.zero()) zero_row<ELT>(grad, P.V, shift, nvec, P.same_shift, kRowThreads);
   else write_gradient<ELT, ENT>(row, grad, P.V, shift, nvec, P.same_shift, x, G, P.c2);
 }
 
@@ -565,7 +622,7 @@ cudaError_t ring_clusters(int ctas, int* fit) {
   if (e != cudaSuccess) return e;
   if (dev < 64 && (*fit = known[dev][ctas].load(std::memory_order_acquire)) > 0) return cudaSuccess;
   const void* fn = reinterpret_cast<const void*>(&token_ring_kernel<ELT, ENT, GRAD>);
-  e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, rg_smem(GRAD));
+  e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, rg_smem<GRAD>());
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeClusterDimension;
@@ -573,8 +630,8 @@ cudaError_t ring_clusters(int ctas, int* fit) {
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(ctas));
-  cfg.blockDim = dim3(kRgThreads);
-  cfg.dynamicSmemBytes = static_cast<size_t>(rg_smem(GRAD));
+  cfg.blockDim = dim3(Rg<GRAD>::kThreads);
+  cfg.dynamicSmemBytes = static_cast<size_t>(rg_smem<GRAD>());
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   e = cudaOccupancyMaxActiveClusters(fit, fn, &cfg);
@@ -587,10 +644,11 @@ cudaError_t ring_clusters(int ctas, int* fit) {
 template <int ELT, bool ENT, bool GRAD>
 cudaError_t launch_ring(const RowParams& p, int rows, cudaStream_t s) {
   const long long row_bytes = static_cast<long long>(p.V) * ELT;
-  // For the gradient a CTA's part of a row stays in its ring, with room for what
-  // is on its way.  Few rows: as many CTAs to a row as give the SMs work.
+  // For the gradient a CTA's part of a row stays in its ring, with the next row's
+  // where the cluster is not too large for it.  Few rows: as many CTAs to a row as
+  // give the SMs work.
   int ctas = GRAD ? static_cast<int>((row_bytes + kRgPart - 1) / kRgPart) : 1;
-  const int room = GRAD ? kRgSms : 2 * kRgSms;
+  const int room = kRgSms * Rg<GRAD>::kPerSm;
   while (ctas < kRgMaxCtas && static_cast<long long>(rows) * 2 * ctas <= room && row_bytes / (2 * ctas) >= kRgMinPart) ctas *= 2;
   if (ctas > kRgMaxCtas) ctas = kRgMaxCtas;
   int fit = 0;
@@ -605,13 +663,14 @@ cudaError_t launch_ring(const RowParams& p, int rows, cudaStream_t s) {
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(clusters * ctas));
-  cfg.blockDim = dim3(kRgThreads);
-  cfg.dynamicSmemBytes = static_cast<size_t>(rg_smem(GRAD));
+  cfg.blockDim = dim3(Rg<GRAD>::kThreads);
+  cfg.dynamicSmemBytes = static_cast<size_t>(rg_smem<GRAD>());
   cfg.stream = s;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  const int shares = ctas * kRgWarps, per = (p.V / Vec<ELT>::N + shares - 1) / shares;
-  return cudaLaunchKernelEx(&cfg, token_ring_kernel<ELT, ENT, GRAD>, p, rows, static_cast<int>(window), per);
+  const int per = (p.V / Vec<ELT>::N + ctas - 1) / ctas;
+  const int ahead = 2 * ((per + kRgSlotVecs - 1) / kRgSlotVecs) <= Rg<GRAD>::kSlots;
+  return cudaLaunchKernelEx(&cfg, token_ring_kernel<ELT, ENT, GRAD>, p, rows, static_cast<int>(window), per, ahead);
 }
 
 template <int ELT, bool ENT, bool GRAD>
