@@ -17,10 +17,12 @@
 #include <atomic>
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "../../include/specverify.h"
 #include "sv_internal.h"
 #include "sv_kd.h"
+#include "sv_policy.h"
 #include "sv_rowsum.cuh"
 #include "sv_token.cuh"
 
@@ -46,6 +48,7 @@ struct RowParams {
   unsigned char* grad;         // [rows, V] or null
   int t_len, V;
   int same_shift;              // logits and grad lie alike: 16-byte stores
+  int followed;                // by a kernel that waits for this one: it may take its place on an SM early
   float c2, inv_T;             // log2(e) / T, 1 / T
   long long wait_limit_ns;     // of a wait for staged logits
   PolicyArgs policy;
@@ -125,7 +128,7 @@ __global__ void __launch_bounds__(kRowThreads) token_row_kernel(const __grid_con
   const unsigned char* row = P.logits + r * P.V * ELT;
   unsigned char* grad = GRAD ? P.grad + r * P.V * ELT : nullptr;
   const int shift = row_shift<ELT>(row), nvec = row_vecs<ELT>(P.V, shift);
-  if (P.row_loss) grid_dependents_launch();   // the sum of the rows may take its place on an SM
+  if (P.followed) grid_dependents_launch();
   const int x = P.tokens[r];
   if (x < 0) {
     if (tid == 0) {
@@ -138,7 +141,7 @@ __global__ void __launch_bounds__(kRowThreads) token_row_kernel(const __grid_con
     return;
   }
   const float zx = x < P.V ? load_elem<ELT>(row, x) : NAN;
-  TokSum<ELT, ENT> sum;
+  TokSum<ELT, ENT> sum(zx);
   for (int v = tid; v < nvec; v += kRowThreads) {
     uint4 w[1] = {load_row_vec<ELT>(row, P.V, shift, v)};
     tok_take_out<ELT>(w[0], x + shift - v * N);
@@ -210,13 +213,12 @@ constexpr int kRgWindow = 8192;                             // rows whose tokens
 constexpr int kRgLive = 448, kRgDead = 64;                  // of which a cluster, a CTA gets so many at most
 constexpr int kRgSms = 152;
 constexpr int kRgMinRow = 32 * 1024;                        // bytes of a row that is streamed
-constexpr int kRgPart = 96 * 1024;                          // a CTA's part for the gradient, if the row allows
 constexpr int kRgMinPart = 16 * 1024;                       // and where a row is split for want of rows
 constexpr long long kRgJoinLimitNs = 4 * kDrainLimitNs;     // a CTA's part comes within an expired wait
 constexpr long long kRgRowLimitNs = 2 * kRgJoinLimitNs;     // and a row's numbers within that one
 constexpr int kRgNoRow = 0x7fffffff;
 static_assert(Rg<true>::kSlotBytes == kRgSlotBytes && Rg<false>::kSlotBytes == kRgSlotBytes, "slots");
-static_assert((kTokMaxRow / kRgMaxCtas + kRgSlotBytes - 1) / kRgSlotBytes < Rg<true>::kSlots, "the longest row fits a cluster");
+static_assert((kTokMaxRow / kRgSlotBytes + 5) / 6 < Rg<true>::kSlots, "the longest row fits a cluster of 6");
 
 struct RgShared {
   uint64_t full[kRgMaxSlots], empty[kRgMaxSlots];
@@ -235,10 +237,9 @@ template <bool GRAD>
 constexpr int rg_smem() { return kRgRingAt + Rg<GRAD>::kSlots * kRgSlotBytes; }
 static_assert(rg_smem<true>() <= 227 * 1024 && 2 * (rg_smem<false>() + 1024) <= 228 * 1024, "an SM's shared memory");
 
-// A CTA's part of a row's whole vectors: the place of its first one, which of
-// the row's vectors that is, and their number (the row's ends are taken apart).
+// A CTA's part of a row's whole vectors: which of the row's vectors is its first,
+// and their number (the row's ends are taken apart).
 struct RgPart {
-  const unsigned char* at;
   int first, n, shift, nvec;
   template <int ELT>
   __device__ __forceinline__ static RgPart of(const unsigned char* row, int V, int per, int rank) {
@@ -251,13 +252,45 @@ struct RgPart {
     const int from = min(all, rank * per);
     t.first = head + from;
     t.n = min(all, rank * per + per) - from;
-    t.at = row + (static_cast<long long>(t.first) * N - t.shift) * ELT;
     return t;
+  }
+  // of the first vector, in bytes from the row's start on
+  __device__ __forceinline__ int offset(int elt) const { return first * 16 - shift * elt; }
+  // the token that this thread takes of the row's ends, of whole vectors no part, or -1
+  template <int ELT>
+  __device__ __forceinline__ int end(int V, int rank, int tid) const {
+    constexpr int N = Vec<ELT>::N;
+    const int e = tid & 31;
+    if (rank || tid >= 64 || e >= N) return -1;
+    if (tid < 32) return shift && e < N - shift ? e : -1;
+    const int over = (V + shift) % N;    // of the last vector's places
+    return e < over ? V - over + e : -1;
   }
 };
 
-// How many of the numbers below `x` are `mine` modulo `of`.
-__device__ __forceinline__ long long rg_own(long long x, int mine, int of) { return x > mine ? (x - mine + of - 1) / of : 0; }
+// A vector of one value, the others -inf.
+template <int ELT>
+__device__ __forceinline__ uint4 rg_one(uint32_t bits) {
+  uint4 w = Vec<ELT>::neg_inf();
+  w.x = ELT == 4 ? bits : (w.x & 0xffff0000u) | bits;
+  return w;
+}
+
+// A wait of at most `limit_ns`, the warp parked meanwhile.
+__device__ __noinline__ bool rg_wait_longer(uint64_t* bar, uint32_t parity, long long limit_ns) {
+  const unsigned long long t0 = global_ns();
+  while (!mbar_park(bar, parity, 20000))
+    if (static_cast<long long>(global_ns() - t0) >= limit_ns) return false;
+  return true;
+}
+__device__ __forceinline__ bool rg_wait(uint64_t* bar, uint32_t parity, long long limit_ns) {
+  return mbar_try_wait(bar, parity) || rg_wait_longer(bar, parity, limit_ns);
+}
+
+// How many of the numbers from `from`, which is below `of`, to `to` are `own` modulo `of`.
+__device__ __forceinline__ int rg_own(unsigned from, unsigned to, unsigned own, unsigned of) {
+  return static_cast<int>((to > own ? (to - own + of - 1) / of : 0u) - (from > own ? 1u : 0u));
+}
 
 // `window`: rows whose tokens are looked at together; `per`: vectors of a CTA's
 // part at most; `ahead`: two parts fit the ring.
@@ -288,7 +321,15 @@ __global__ void __launch_bounds__(Rg<GRAD>::kThreads, Rg<GRAD>::kPerSm)
   }
   if (ctas > 1) cluster_sync();   // the others' barriers are set up too
   else __syncthreads();
-  if (P.row_loss) grid_dependents_launch();   // the sum of the rows may take its place on an SM
+  if (P.followed) grid_dependents_launch();
+
+  // rows of whole vectors lie alike, so one part stands for all
+  const unsigned row_bytes = static_cast<unsigned>(P.V) * ELT;
+  const bool alike = row_bytes % 16 == 0;
+  RgPart t = RgPart::of<ELT>(P.logits, P.V, per, rank);
+  auto row_at = [&](long long w, int i) {      // byte offset of row i of this cluster's
+    return static_cast<unsigned long long>(static_cast<unsigned>(w) + sh.live[i]) * row_bytes;
+  };
 
   // every role's place in the ring, and the parity of that slot's copies
   int slot = 0;
@@ -298,10 +339,12 @@ __global__ void __launch_bounds__(Rg<GRAD>::kThreads, Rg<GRAD>::kPerSm)
   };
   unsigned copies = 0;            // (producer)
   unsigned turn = 0;              // rows with a token
-  bool dead = false;              // a wait of this thread has expired; the producer has given up
+  // a wait of this thread has expired (at a limit of 0, looked at here once, every
+  // one has); the producer has given up
+  bool dead = P.wait_limit_ns <= 0 && warp < kWorkers;
   bool alone = false;             // (the row's warp) the cluster did not answer
   unsigned alone_turn = 0;
-  long long seen_live = 0, seen_dead = 0;
+  unsigned turn_live = 0, turn_dead = 0;   // whose the next rows are
   for (long long w0 = 0; w0 < rows; w0 += window) {
     // ---- which rows of the window are this cluster's, and this CTA's to fill
     const int in_window = static_cast<int>(rows - w0 < window ? rows - w0 : window);
@@ -327,44 +370,50 @@ __global__ void __launch_bounds__(Rg<GRAD>::kThreads, Rg<GRAD>::kPerSm)
     const int count = lane < kWorkers ? sh.counts[lane] : 0;
     const int total = static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(count)));
     const int before = static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(lane < warp ? count : 0))) + upto - mine;
-    const long long own_live = rg_own(seen_live, cluster, clusters), own_dead = rg_own(seen_dead, blockIdx.x, gridDim.x);
-    {
-      long long k = seen_live + (before & 0xffff);
-      for (uint32_t b = live_bits; b; b &= b - 1, ++k)
-        if (k % clusters == cluster)
-          sh.live[rg_own(k, cluster, clusters) - own_live] = static_cast<unsigned short>((warp * words + lane) * 32 + __ffs(b) - 1);
-      k = seen_dead + (before >> 16);
-      for (uint32_t b = dead_bits; b; b &= b - 1, ++k)
-        if (k % gridDim.x == blockIdx.x) {
-          const int at = (warp * words + lane) * 32 + __ffs(b) - 1;
-          const long long r = w0 + at;
-          sh.dead[rg_own(k, blockIdx.x, gridDim.x) - own_dead] = static_cast<unsigned short>(at);
-          P.logp[r] = 0.f;
-          if (P.entropy) P.entropy[r] = 0.f;
-          if (P.lse) P.lse[r] = -INFINITY;
-          if (P.row_loss) P.row_loss[r] = 0.f;
+    // row k of those with a token (from `turn_live` on, modulo the clusters) is
+    // cluster k % clusters's, and likewise for the CTAs and the others
+    for (int j = 0; j < words; ++j) {
+      const uint32_t l = __shfl_sync(0xffffffffu, live_bits, j), d = __shfl_sync(0xffffffffu, dead_bits, j);
+      const int from = __shfl_sync(0xffffffffu, before, j), at = (warp * words + j) * 32 + lane;
+      const uint32_t lower = (1u << lane) - 1u;
+      const bool has = l >> lane & 1u;
+      if (has || (d >> lane & 1u)) {
+        const unsigned k = (has ? turn_live + (from & 0xffff) : turn_dead + (from >> 16)) + __popc((has ? l : d) & lower);
+        const unsigned of = has ? clusters : gridDim.x, own = has ? cluster : blockIdx.x;
+        if (k % of == own) {
+          const unsigned place = k / of - (own < (has ? turn_live : turn_dead) ? 1u : 0u);
+          (has ? sh.live : sh.dead)[place] = static_cast<unsigned short>(at);
+          if (!has) {
+            const long long r = w0 + at;
+            P.logp[r] = 0.f;
+            if (P.entropy) P.entropy[r] = 0.f;
+            if (P.lse) P.lse[r] = -INFINITY;
+            if (P.row_loss) P.row_loss[r] = 0.f;
+          }
         }
+      }
     }
-    seen_live += total & 0xffff;
-    seen_dead += total >> 16;
-    const int n_live = static_cast<int>(rg_own(seen_live, cluster, clusters) - own_live);
-    const int n_dead = static_cast<int>(rg_own(seen_dead, blockIdx.x, gridDim.x) - own_dead);
+    const int n_live = rg_own(turn_live, turn_live + (total & 0xffff), cluster, clusters);
+    const int n_dead = rg_own(turn_dead, turn_dead + (total >> 16), blockIdx.x, gridDim.x);
+    turn_live = (turn_live + (total & 0xffff)) % clusters;
+    turn_dead = (turn_dead + (total >> 16)) % gridDim.x;
     __syncthreads();
 
     if (warp == kWorkers) {
       // ---- the producer
-      const uint64_t first_out = evict_first_policy();
       for (int i = 0; i < n_live && !dead; ++i) {
-        const RgPart t = RgPart::of<ELT>(P.logits + (w0 + sh.live[i]) * P.V * ELT, P.V, per, rank);
+        const unsigned char* row = P.logits + row_at(w0, i);
+        if (!alike) t = RgPart::of<ELT>(row, P.V, per, rank);
+        const unsigned char* from = row + t.offset(ELT);
         for (int v = 0; v < t.n && !dead; v += kRgSlotVecs) {
           int ok = 1;
-          if (lane == 0) ok = mbar_wait_bounded(&sh.empty[slot], round ^ 1, kDrainLimitNs) ? 1 : 0;
+          if (lane == 0) ok = rg_wait(&sh.empty[slot], round ^ 1, kDrainLimitNs) ? 1 : 0;
           dead = !__shfl_sync(0xffffffffu, ok, 0);
           if (dead) break;        // as a worker has
           if (lane == 0) {
             const uint32_t bytes = static_cast<uint32_t>(min(kRgSlotVecs, t.n - v)) * 16u;
             mbar_expect_tx(&sh.full[slot], bytes);
-            bulk_load_hint(ring + slot * kRgSlotBytes, t.at + static_cast<long long>(v) * 16, bytes, &sh.full[slot], first_out);
+            bulk_load(ring + slot * kRgSlotBytes, from + v * 16, bytes, &sh.full[slot]);
           }
           ++copies;
           step(slot, round);
@@ -384,7 +433,7 @@ __global__ void __launch_bounds__(Rg<GRAD>::kThreads, Rg<GRAD>::kPerSm)
         PolicyRow mine_row{};
         if (P.row_loss) mine_row = PolicyRow::of(P.policy, static_cast<int>(r), P.t_len);
         const int x_next = P.tokens[r_next];
-        bool here = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.summed[par], phase, kRgRowLimitNs));
+        bool here = __all_sync(0xffffffffu, rg_wait(&sh.summed[par], phase, kRgRowLimitNs));
         const float zx_next = x_next < P.V ? load_elem<ELT>(P.logits + r_next * P.V * ELT, x_next) : NAN;
         TokPart part = tok_join<ENT>(lane < kWorkers ? sh.warp[par][lane] : tok_none(), P.c2);
         if (!GRAD && lane == 0) mbar_arrive(&sh.ready[par]);   // the row after the next may take the sums' place
@@ -398,7 +447,7 @@ __global__ void __launch_bounds__(Rg<GRAD>::kThreads, Rg<GRAD>::kPerSm)
               st_async(peer(&sh.part[par][rank], lane),
                        make_uint4(__float_as_uint(part.m), __float_as_uint(part.s), __float_as_uint(part.a), 0u),
                        peer(&sh.joined[par], lane));
-            alone = !__all_sync(0xffffffffu, mbar_wait_bounded(&sh.joined[par], phase, kRgJoinLimitNs));
+            alone = !__all_sync(0xffffffffu, rg_wait(&sh.joined[par], phase, kRgJoinLimitNs));
             if (alone) {
               // another CTA may still get here and on to the next row, where it
               // waits in vain: what it sends until then is waited for at the end
@@ -442,111 +491,122 @@ __global__ void __launch_bounds__(Rg<GRAD>::kThreads, Rg<GRAD>::kPerSm)
     // itself where two do not fit)
     int kept_slot = slot;         // where the row begins whose gradient is next
     int filled = 0;
+    uint32_t end_next = 0u, end_kept = 0u;   // this thread's logit at the ends of the row summed last and of the one before
     int x_next = n_live ? P.tokens[w0 + sh.live[0]] : 0, x_before = 0;
+    uint32_t zx_next = n_live ? load_bits<ELT>(P.logits + row_at(w0, 0), min(x_next, P.V - 1)) : 0u;
     const unsigned first_turn = turn;
     for (int i = 0; i < n_live + (GRAD ? ahead : 0); ++i) {
       int x_now = x_next;
       if (i < n_live) {
-        const long long r = w0 + sh.live[i];
-        const unsigned char* row = P.logits + r * P.V * ELT;
-        const RgPart t = RgPart::of<ELT>(row, P.V, per, rank);
+        const unsigned char* row = P.logits + row_at(w0, i);
+        if (!alike) t = RgPart::of<ELT>(row, P.V, per, rank);
         const int x = x_now < P.V ? x_now : -(1 << 30);
         if (i + 1 < n_live) x_next = P.tokens[w0 + sh.live[i + 1]];
-        // where x lies from the part's first vector on, and whether this thread reads it
+        // where x lies from the part's first vector on; the slot in which this thread reads it
         const int x_vec = (x + t.shift) / N - t.first;
-        const bool own_x = x_vec >= 0 && x_vec < t.n && x_vec % kWork == tid;
-        // the row's ends by two threads
-        const int end = rank ? -1 : tid == 0 && t.shift ? 0 : tid == 32 && (P.V + t.shift) % N && t.nvec > (t.shift ? 1 : 0) ? t.nvec - 1 : -1;
-        uint4 end_vec = VT::neg_inf();
-        if (end >= 0) end_vec = load_row_vec<ELT>(row, P.V, t.shift, end);
-        TokSum<ELT, ENT> sum;
-        for (int v = 0; v < t.n; v += kRgSlotVecs) {
-          const int n = t.n - v;
+        const int x_at = x_vec >= 0 && x_vec < t.n && x_vec % kWork == tid ? x_vec / kRgSlotVecs : -1;
+        const int end = t.end<ELT>(P.V, rank, tid);
+        const uint32_t end_now = end >= 0 ? load_bits<ELT>(row, end) : 0u;
+        TokSum<ELT, ENT> sum(value_of<ELT>(zx_next));
+        // (after an expired wait the vectors are whatever lies there, which is made
+        // NaN once a row)
+        const int slots = (t.n + kRgSlotVecs - 1) / kRgSlotVecs;
+        auto take = [&](uint4 (&w)[U], int v) {
+          const int n = t.n - v * kRgSlotVecs;
           unsigned char* at = ring + slot * kRgSlotBytes;
-          if (!dead) dead = !mbar_wait_bounded(&sh.full[slot], round, P.wait_limit_ns);
-          if (own_x && x_vec >= v && x_vec < v + kRgSlotVecs && !dead) {   // out of the sum: this thread reads what it writes here
-            VT::store_scalar(at, (x_vec - v) * N + (x + t.shift) % N, -INFINITY);
+          if (!dead) dead = !rg_wait(&sh.full[slot], round, P.wait_limit_ns);
+          if (v == x_at) {        // out of the sum: this thread reads what it writes here
+            VT::store_scalar(at, (x_vec - v * kRgSlotVecs) * N + (x + t.shift) % N, -INFINITY);
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // before the slot is filled again
           }
           const uint4* src = reinterpret_cast<const uint4*>(at) + tid;
-          uint4 w[U];
-          if (n >= kRgSlotVecs && !dead) {
+          if (n >= kRgSlotVecs) {
 #pragma unroll
             for (int k = 0; k < U; ++k) w[k] = src[k * kWork];
           } else {
 #pragma unroll
-            for (int k = 0; k < U; ++k) w[k] = !dead && tid + k * kWork < n ? src[k * kWork] : VT::neg_inf();
+            for (int k = 0; k < U; ++k) w[k] = tid + k * kWork < n ? src[k * kWork] : VT::neg_inf();
           }
           if (!GRAD) {
             __syncwarp();
             if (lane == 0 && !dead) mbar_arrive(&sh.empty[slot]);
           }
           step(slot, round);
-          sum.add(w, P.c2);
+        };
+        // a slot's vectors are on their way from shared memory while the one before is summed
+        uint4 wa[U], wb[U];
+        if (slots) take(wa, 0);
+        for (int v = 0; v < slots; v += 2) {
+          if (v + 1 < slots) take(wb, v + 1);
+          sum.add(wa, P.c2);
+          if (v + 2 < slots) take(wa, v + 2);
+          if (v + 1 < slots) sum.add(wb, P.c2);
         }
-        if (end >= 0) {
-          uint4 one[1] = {end_vec};
-          tok_take_out<ELT>(one[0], x + t.shift - end * N);
+        if (end >= 0 && end != x) {
+          const uint4 one[1] = {rg_one<ELT>(end_now)};
           sum.add(one, P.c2);
         }
+        end_kept = end_next;
+        end_next = end_now;
         TokPart part = sum.part();
         if (dead) part.s = NAN;
         part = tok_join<ENT>(part, P.c2);
         const unsigned at_turn = first_turn + static_cast<unsigned>(i);
         const int par = at_turn & 1;
         // (for the gradient the workers have waited for that row's numbers)
-        if (!GRAD && at_turn >= 2 && !mbar_wait_bounded(&sh.ready[par], (at_turn >> 1 & 1) ^ 1, kRgRowLimitNs)) dead = true;
+        if (!GRAD && at_turn >= 2 && !rg_wait(&sh.ready[par], (at_turn >> 1 & 1) ^ 1, kRgRowLimitNs)) dead = true;
         if (lane == 0) {
           sh.warp[par][warp] = part;
           mbar_arrive(&sh.summed[par]);
         }
+        if (i + 1 < n_live) zx_next = load_bits<ELT>(P.logits + row_at(w0, i + 1), min(x_next, P.V - 1));
       }
       if (GRAD && i >= ahead) {
         const long long r = w0 + sh.live[i - ahead];
         const unsigned at_turn = first_turn + static_cast<unsigned>(i - ahead);
-        const RgPart t = RgPart::of<ELT>(P.logits + r * P.V * ELT, P.V, per, rank);
-        unsigned char* grad = P.grad + r * P.V * ELT;
+        const unsigned long long at_row = row_at(w0, i - ahead);
+        if (!alike) t = RgPart::of<ELT>(P.logits + at_row, P.V, per, rank);
+        unsigned char* grad = P.grad + at_row;
         const int x_row = ahead ? x_before : x_now;
         const int x = x_row < P.V ? x_row : -(1 << 30), x_vec = (x + t.shift) / N - t.first;
-        const int end = rank ? -1 : tid == 0 && t.shift ? 0 : tid == 32 && (P.V + t.shift) % N && t.nvec > (t.shift ? 1 : 0) ? t.nvec - 1 : -1;
-        uint4 end_vec = VT::neg_inf();
-        if (end >= 0) end_vec = load_row_vec<ELT>(P.logits + r * P.V * ELT, P.V, t.shift, end);
-        const bool here = mbar_wait_bounded(&sh.ready[at_turn & 1], at_turn >> 1 & 1, kRgRowLimitNs);
+        const int end = t.end<ELT>(P.V, rank, tid);
+        const uint32_t end_bits = ahead && i < n_live ? end_kept : end_next;   // (nothing was summed after the last row)
+        const bool here = rg_wait(&sh.ready[at_turn & 1], at_turn >> 1 & 1, kRgRowLimitNs);
         TokGrad G = sh.grad[at_turn & 1];
         if (!here) {
           atomicMin(&sh.failed, static_cast<int>(r));
           dead = true;
         }
         if (dead) G.alpha = G.at_token = NAN;
-        unsigned char* out = grad + (static_cast<long long>(t.first) * N - t.shift) * ELT + tid * 16;
-        for (int v = 0; v < t.n; v += kRgSlotVecs, out += kRgSlotBytes) {
-          const int n = t.n - v;
+        unsigned char* out = grad + t.offset(ELT) + tid * 16;
+        auto give = [&](int v, auto full) {
+          const int n = t.n - v * kRgSlotVecs;
           const uint4* src = reinterpret_cast<const uint4*>(ring + kept_slot * kRgSlotBytes) + tid;
           uint4 w[U];
-          if (n >= kRgSlotVecs && !dead) {
 #pragma unroll
-            for (int k = 0; k < U; ++k) w[k] = src[k * kWork];
-          } else {
-#pragma unroll
-            for (int k = 0; k < U; ++k) w[k] = !dead && tid + k * kWork < n ? src[k * kWork] : VT::neg_inf();
-          }
+          for (int k = 0; k < U; ++k) w[k] = decltype(full)::value || tid + k * kWork < n ? src[k * kWork] : VT::neg_inf();
           __syncwarp();
           if (lane == 0 && !dead) mbar_arrive(&sh.empty[kept_slot]);
           if (++kept_slot == kSlots) kept_slot = 0;
-          if (P.same_shift && n >= kRgSlotVecs) {
 #pragma unroll
-            for (int k = 0; k < U; ++k) store_vec16(out + k * kWork * 16, tok_vec_grad<ELT, ENT>(w[k], G, P.c2));
-          } else {
-#pragma unroll
-            for (int k = 0; k < U; ++k)
-              if (tid + k * kWork < n)
-                store_edge<ELT>(grad, P.V, (t.first + v + tid + k * kWork) * N - t.shift, P.same_shift, tok_vec_grad<ELT, ENT>(w[k], G, P.c2));
+          for (int k = 0; k < U; ++k) {
+            const uint4 d = tok_vec_grad<ELT, ENT>(w[k], G, P.c2);
+            if (decltype(full)::value) store_vec16(out + k * kWork * 16, d);
+            else if (tid + k * kWork < n)
+              store_edge<ELT>(grad, P.V, (t.first + v * kRgSlotVecs + tid + k * kWork) * N - t.shift, P.same_shift, d);
           }
+          out += kRgSlotBytes;
+        };
+        const int whole = P.same_shift ? t.n / kRgSlotVecs : 0;
+        for (int v = 0; v < whole; ++v) give(v, std::true_type());
+        for (int v = whole; v * kRgSlotVecs < t.n; ++v) give(v, std::false_type());
+        if (end >= 0) {
+          float d[N];
+          VT::unpack(tok_vec_grad<ELT, ENT>(rg_one<ELT>(end_bits), G, P.c2), d);
+          VT::store_rounded(grad, end, end == x ? G.at_token : d[0]);
         }
-        if (end >= 0) store_edge<ELT>(grad, P.V, end * N - t.shift, P.same_shift, tok_vec_grad<ELT, ENT>(end_vec, G, P.c2));
         // the token's own after its vector's, by the same thread
-        if ((x_vec >= 0 && x_vec < t.n && x_vec % kWork == tid) || (end >= 0 && x >= 0 && (x + t.shift) / N == end))
-          VT::store_rounded(grad, x, G.at_token);
+        if (x_vec >= 0 && x_vec < t.n && x_vec % kWork == tid) VT::store_rounded(grad, x, G.at_token);
         // rows without a token, as many as there are for each row with one
         for (; static_cast<long long>(filled) * n_live < static_cast<long long>(i + 1 - ahead) * n_dead; ++filled) {
           unsigned char* zero = P.grad + (w0 + sh.dead[filled]) * P.V * ELT;
@@ -567,11 +627,11 @@ __global__ void __launch_bounds__(Rg<GRAD>::kThreads, Rg<GRAD>::kPerSm)
   // ---- no copy is left in flight, and nothing on its way to a CTA that has left
   if (warp == kWorkers && lane == 0)
     for (unsigned k = copies > kSlots ? copies - kSlots : 0; k < copies; ++k)
-      mbar_wait_bounded(&sh.full[k % kSlots], k / kSlots & 1, kDrainLimitNs);
+      rg_wait(&sh.full[k % kSlots], k / kSlots & 1, kDrainLimitNs);
   if (ctas > 1) {
     cluster_sync();
     if (alone)
-      for (unsigned k = alone_turn; k < alone_turn + 2; ++k) mbar_wait_bounded(&sh.joined[k & 1], k >> 1 & 1, kDrainLimitNs);
+      for (unsigned k = alone_turn; k < alone_turn + 2; ++k) rg_wait(&sh.joined[k & 1], k >> 1 & 1, kDrainLimitNs);
   } else {
     __syncthreads();
   }
@@ -584,32 +644,106 @@ __global__ void __launch_bounds__(Rg<GRAD>::kThreads, Rg<GRAD>::kPerSm)
   }
 }
 
+// ---- the gradient from what token_logp gave: a stream of 32 KB pieces
+//
+// A row's pieces go to as many CTAs, up to eight, each with all its loads in flight
+// at once; four CTAs an SM hide each other's chain of two trips to memory (the
+// row's numbers, then its token's logit).  In place the token's logit may be
+// overwritten by another piece's CTA, so there the row's CTAs are a cluster, which
+// goes on when all of them have it.
 struct GradParams {
   const unsigned char* logits;
   const int* tokens;
   const float *logp, *lse, *entropy, *d_logp, *d_entropy;   // [rows]; the entropies or null
   unsigned char* grad;
   int V, same_shift;
+  int d_rows;                  // rows that share a d_logp
+  int in_place;
   float c2, inv_T;
 };
+constexpr int kGrThreads = 256, kGrPerThread = 8, kGrVecs = kGrThreads * kGrPerThread;
+constexpr int kGrMaxParts = 8;
 
 template <int ELT, bool ENT>
-__global__ void __launch_bounds__(kRowThreads) token_grad_kernel(const __grid_constant__ GradParams P) {
-  const long long r = blockIdx.x;
-  const unsigned char* row = P.logits + r * P.V * ELT;
-  unsigned char* grad = P.grad + r * P.V * ELT;
+__global__ void __launch_bounds__(kGrThreads, 4) token_grad_kernel(const __grid_constant__ GradParams P, int parts, int per) {
+  using VT = Vec<ELT>;
+  constexpr int N = VT::N;
+  const int tid = threadIdx.x;
+  const int r = static_cast<int>(blockIdx.x) / parts, part = static_cast<int>(blockIdx.x) % parts;
+  const unsigned long long at_row = static_cast<unsigned long long>(r) * (static_cast<unsigned>(P.V) * ELT);
+  const unsigned char* row = P.logits + at_row;
+  unsigned char* grad = P.grad + at_row;
   const int shift = row_shift<ELT>(row), nvec = row_vecs<ELT>(P.V, shift);
   const int x = P.tokens[r];
+  grid_dependency_wait();      // (the rows' numbers may be a kernel's before this one; the logits and tokens are not)
   TokGrad G;
   G.none();
   if (x >= 0) {
-    const float zx = x < P.V ? load_elem<ELT>(row, x) : NAN;
-    G = tok_grad_from(zx, x < P.V ? P.logp[r] : NAN, P.lse[r], ENT ? P.entropy[r] : 0.f, P.d_logp[r],
+    const uint32_t zx = load_bits<ELT>(row, min(x, P.V - 1));
+    G = tok_grad_from(value_of<ELT>(zx), x < P.V ? P.logp[r] : NAN, P.lse[r], ENT ? P.entropy[r] : 0.f,
+                      P.d_logp[P.d_rows > 1 ? static_cast<unsigned>(r) / static_cast<unsigned>(P.d_rows) : r],
                       ENT ? P.d_entropy[r] : 0.f, P.inv_T);
   }
-  __syncthreads();               // (in place: every thread has the token's logit)
-  if (G.zero()) zero_row<ELT>(grad, P.V, shift, nvec, P.same_shift, kRowThreads);
-  else write_gradient<ELT, ENT>(row, grad, P.V, shift, nvec, P.same_shift, x, G, P.c2);
+  if (P.in_place) {
+    if (parts > 1) cluster_sync();
+    else __syncthreads();
+  }
+  const int to = min(nvec, (part + 1) * per);
+  const bool zero = G.zero();
+  for (int v0 = part * per; v0 < to; v0 += kGrVecs) {
+    const int v = v0 + tid, n = to - v0;
+    // pieces of whole vectors go without a look at each
+    const bool whole = n >= kGrVecs && P.same_shift && v0 * N - shift >= 0 && (v0 + kGrVecs) * N - shift <= P.V;
+    if (whole) {
+      const long long at = (static_cast<long long>(v) * N - shift) * ELT;
+      if (zero) {
+#pragma unroll
+        for (int k = 0; k < kGrPerThread; ++k) store_vec16(grad + at + k * kGrThreads * 16, make_uint4(0, 0, 0, 0));
+      } else {
+        uint4 w[kGrPerThread];
+#pragma unroll
+        for (int k = 0; k < kGrPerThread; ++k) w[k] = load_vec16(row + at + k * kGrThreads * 16);
+#pragma unroll
+        for (int k = 0; k < kGrPerThread; ++k) store_vec16(grad + at + k * kGrThreads * 16, tok_vec_grad<ELT, ENT>(w[k], G, P.c2));
+      }
+    } else {
+      uint4 w[kGrPerThread];
+#pragma unroll
+      for (int k = 0; k < kGrPerThread; ++k)
+        w[k] = !zero && tid + k * kGrThreads < n ? load_row_vec<ELT>(row, P.V, shift, v + k * kGrThreads) : VT::neg_inf();
+#pragma unroll
+      for (int k = 0; k < kGrPerThread; ++k)
+        if (tid + k * kGrThreads < n)
+          store_edge<ELT>(grad, P.V, (v + k * kGrThreads) * N - shift, P.same_shift,
+                          zero ? make_uint4(0, 0, 0, 0) : tok_vec_grad<ELT, ENT>(w[k], G, P.c2));
+    }
+    // the token's own after its vector's, by the same thread
+    const int x_vec = x >= 0 && x < P.V ? (x + shift) / N - v0 : -1;
+    if (!zero && x_vec >= 0 && x_vec < min(n, kGrVecs) && x_vec % kGrThreads == tid) VT::store_rounded(grad, x, G.at_token);
+  }
+}
+
+template <int ELT, bool ENT>
+cudaError_t launch_grad(const GradParams& p, int rows, bool dependent, cudaStream_t s) {
+  const int nvec = (p.V + 2 * Vec<ELT>::N - 2) / Vec<ELT>::N;      // of a row off the 16-byte boundary
+  const int parts = std::min(kGrMaxParts, (nvec + kGrVecs - 1) / kGrVecs), per = (nvec + parts - 1) / parts;
+  cudaLaunchAttribute attr[2];
+  cudaLaunchConfig_t cfg{};
+  if (dependent) {
+    attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
+  }
+  if (p.in_place && parts > 1) {
+    attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+    attr[cfg.numAttrs].val.clusterDim.x = static_cast<unsigned>(parts);
+    attr[cfg.numAttrs].val.clusterDim.y = attr[cfg.numAttrs].val.clusterDim.z = 1;
+    ++cfg.numAttrs;
+  }
+  cfg.gridDim = dim3(static_cast<unsigned>(rows) * static_cast<unsigned>(parts));
+  cfg.blockDim = dim3(kGrThreads);
+  cfg.stream = s;
+  cfg.attrs = attr;
+  return cudaLaunchKernelEx(&cfg, token_grad_kernel<ELT, ENT>, p, parts, per);
 }
 
 // Clusters of `ctas` of the ring kernel that fit at once, asked for once per
@@ -644,10 +778,20 @@ cudaError_t ring_clusters(int ctas, int* fit) {
 template <int ELT, bool ENT, bool GRAD>
 cudaError_t launch_ring(const RowParams& p, int rows, cudaStream_t s) {
   const long long row_bytes = static_cast<long long>(p.V) * ELT;
-  // For the gradient a CTA's part of a row stays in its ring, with the next row's
-  // where the cluster is not too large for it.  Few rows: as many CTAs to a row as
-  // give the SMs work.
-  int ctas = GRAD ? static_cast<int>((row_bytes + kRgPart - 1) / kRgPart) : 1;
+  // For the gradient a CTA's part of a row stays in its ring.  Clusters of 1, 2, 4
+  // and 6 leave 0, 0, 8 and 14 of the SMs idle.  In bf16, where the workers are as
+  // busy as the memory, the smallest of them that fits two parts, so that one row is
+  // summed while the other's gradient is written (1024 rows of 151936: 120 us, of
+  // 128256 104 us; with one part 127 and 111); in float32 the smallest that fits one
+  // (1024 rows of 50001: 85 us, with two parts 91).
+  const int slots = static_cast<int>((row_bytes + kRgSlotBytes - 1) / kRgSlotBytes), kept = Rg<GRAD>::kSlots - 1;
+  auto fits = [&](int ctas, int most) { return (slots + ctas - 1) / ctas <= most; };
+  int ctas = 1;
+  if (GRAD) {
+    const int most = ELT == 2 ? Rg<GRAD>::kSlots / 2 : kept;
+    ctas = fits(1, most) ? 1 : fits(2, most) ? 2 : fits(4, kept) ? 4 : 6;
+  }
+  // few rows: as many CTAs to a row as give the SMs work
   const int room = kRgSms * Rg<GRAD>::kPerSm;
   while (ctas < kRgMaxCtas && static_cast<long long>(rows) * 2 * ctas <= room && row_bytes / (2 * ctas) >= kRgMinPart) ctas *= 2;
   if (ctas > kRgMaxCtas) ctas = kRgMaxCtas;
@@ -686,21 +830,6 @@ cudaError_t launch_rows(const RowParams& p, int rows, bool ent, cudaStream_t s) 
   return ent ? launch_rows<ELT, true, false>(p, rows, s) : launch_rows<ELT, false, false>(p, rows, s);
 }
 
-// The sizes, types, temperature and rows that every entry point here checks
-// alike; `grad` may be the logits themselves.
-bool rows_ok(int n_seq, int t_len, int V, sv_dtype dtype, const void* logits, const void* grad, float temperature) {
-  if (n_seq < 1 || t_len < 1 || V < 1 || static_cast<long long>(n_seq) * t_len > (1LL << 28)) return false;
-  if (dtype != SV_F32 && dtype != SV_BF16) return false;
-  if (!(temperature > 0.f) || !std::isfinite(temperature)) return false;
-  if (!(1.4426950408889634 / static_cast<double>(temperature) < 1e30) || !(1.f / temperature > 0.f)) return false;
-  const int elt = dtype == SV_F32 ? 4 : 2;
-  if (!logits || static_cast<long long>(V) * elt > kTokMaxRow) return false;
-  const uintptr_t a = reinterpret_cast<uintptr_t>(logits), g = reinterpret_cast<uintptr_t>(grad);
-  if (a % elt || g % elt) return false;
-  const uintptr_t bytes = static_cast<uintptr_t>(n_seq) * t_len * V * elt;
-  return !(grad && a != g && a < g + bytes && g < a + bytes);
-}
-
 RowParams row_params(int t_len, int V, const void* logits, const int32_t* tokens, float temperature, void* grad) {
   RowParams p{};
   p.logits = static_cast<const unsigned char*>(logits);
@@ -716,6 +845,40 @@ RowParams row_params(int t_len, int V, const void* logits, const int32_t* tokens
 }
 
 }  // namespace
+
+bool rows_ok(int n_seq, int t_len, int V, sv_dtype dtype, const void* logits, const void* grad, float temperature) {
+  if (n_seq < 1 || t_len < 1 || V < 1 || static_cast<long long>(n_seq) * t_len > (1LL << 28)) return false;
+  if (dtype != SV_F32 && dtype != SV_BF16) return false;
+  if (!(temperature > 0.f) || !std::isfinite(temperature)) return false;
+  if (!(1.4426950408889634 / static_cast<double>(temperature) < 1e30) || !(1.f / temperature > 0.f)) return false;
+  const int elt = dtype == SV_F32 ? 4 : 2;
+  if (!logits || static_cast<long long>(V) * elt > kTokMaxRow) return false;
+  const uintptr_t a = reinterpret_cast<uintptr_t>(logits), g = reinterpret_cast<uintptr_t>(grad);
+  if (a % elt || g % elt) return false;
+  const uintptr_t bytes = static_cast<uintptr_t>(n_seq) * t_len * V * elt;
+  return !(grad && a != g && a < g + bytes && g < a + bytes);
+}
+
+cudaError_t launch_token_logp(int rows, int V, sv_dtype dtype, const void* logits, const int32_t* tokens,
+                              float temperature, float* logp, float* entropy, float* lse, bool followed, cudaStream_t s) {
+  RowParams p = row_params(1, V, logits, tokens, temperature, nullptr);
+  p.logp = logp;
+  p.entropy = entropy;
+  p.lse = lse;
+  p.followed = followed;
+  return dtype == SV_BF16 ? launch_rows<2>(p, rows, entropy != nullptr, s) : launch_rows<4>(p, rows, entropy != nullptr, s);
+}
+
+cudaError_t launch_token_grad(int rows, int V, sv_dtype dtype, const void* logits, const int32_t* tokens,
+                              const float* logp, const float* lse, const float* entropy, const float* d_logp, int d_rows,
+                              const float* d_entropy, float temperature, void* grad, bool dependent, cudaStream_t s) {
+  const RowParams q = row_params(1, V, logits, tokens, temperature, grad);
+  const GradParams p{q.logits, tokens, logp, lse, entropy, d_logp, d_entropy, q.grad, V, q.same_shift, d_rows,
+                     grad == logits, q.c2, q.inv_T};
+  if (dtype == SV_BF16) return entropy ? launch_grad<2, true>(p, rows, dependent, s) : launch_grad<2, false>(p, rows, dependent, s);
+  return entropy ? launch_grad<4, true>(p, rows, dependent, s) : launch_grad<4, false>(p, rows, dependent, s);
+}
+
 }  // namespace sv
 
 extern "C" sv_status sv_token_logp(int n_seq, int t_len, int V, sv_dtype dtype, const void* logits,
@@ -724,15 +887,9 @@ extern "C" sv_status sv_token_logp(int n_seq, int t_len, int V, sv_dtype dtype, 
   using namespace sv;
   if (!rows_ok(n_seq, t_len, V, dtype, logits, nullptr, temperature) || !tokens || !logp || !lse)
     return SV_ERR_INVALID_ARG;
-  RowParams p = row_params(t_len, V, logits, tokens, temperature, nullptr);
-  p.logp = logp;
-  p.entropy = entropy;
-  p.lse = lse;
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   NvtxRange range("sv_token_logp");
-  const cudaError_t e = dtype == SV_BF16 ? launch_rows<2>(p, n_seq * t_len, entropy != nullptr, s)
-                                         : launch_rows<4>(p, n_seq * t_len, entropy != nullptr, s);
-  return e == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+  return launch_token_logp(n_seq * t_len, V, dtype, logits, tokens, temperature, logp, entropy, lse, false,
+                           reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? SV_OK : SV_ERR_CUDA;
 }
 
 extern "C" sv_status sv_token_logp_grad(int n_seq, int t_len, int V, sv_dtype dtype, const void* logits,
@@ -743,19 +900,9 @@ extern "C" sv_status sv_token_logp_grad(int n_seq, int t_len, int V, sv_dtype dt
   if (!rows_ok(n_seq, t_len, V, dtype, logits, grad, temperature) || !tokens || !logp || !lse || !d_logp || !grad)
     return SV_ERR_INVALID_ARG;
   if (!entropy != !d_entropy) return SV_ERR_INVALID_ARG;
-  const RowParams q = row_params(t_len, V, logits, tokens, temperature, grad);
-  const GradParams p{q.logits, tokens, logp, lse, entropy, d_logp, d_entropy, q.grad, V, q.same_shift, q.c2, q.inv_T};
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   NvtxRange range("sv_token_logp_grad");
-  const unsigned n = static_cast<unsigned>(n_seq) * static_cast<unsigned>(t_len);
-  if (dtype == SV_BF16) {
-    if (entropy) token_grad_kernel<2, true><<<n, kRowThreads, 0, s>>>(p);
-    else token_grad_kernel<2, false><<<n, kRowThreads, 0, s>>>(p);
-  } else {
-    if (entropy) token_grad_kernel<4, true><<<n, kRowThreads, 0, s>>>(p);
-    else token_grad_kernel<4, false><<<n, kRowThreads, 0, s>>>(p);
-  }
-  return cudaGetLastError() == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+  return launch_token_grad(n_seq * t_len, V, dtype, logits, tokens, logp, lse, entropy, d_logp, 1, d_entropy, temperature,
+                           grad, false, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? SV_OK : SV_ERR_CUDA;
 }
 
 extern "C" sv_status sv_policy_loss(int n_seq, int t_len, int V, sv_dtype dtype, const void* logits,
@@ -775,6 +922,7 @@ extern "C" sv_status sv_policy_loss(int n_seq, int t_len, int V, sv_dtype dtype,
   p.logp = logp;
   p.entropy = entropy;
   p.row_loss = row_loss;
+  p.followed = 1;
   p.policy = PolicyArgs{advantages, weights, old_logp, kl_coef != 0.f ? ref_logp : nullptr, per_token,
                         clip_low, clip_high, dual_clip, kl_coef, entropy_coef};
   const bool ent = entropy || entropy_coef != 0.f;

@@ -17,7 +17,8 @@
 
 #include "../../include/specverify.h"
 #include "sv_internal.h"
-#include "sv_token.cuh"
+#include "sv_device.cuh"
+#include "sv_policy.h"
 
 namespace sv {
 namespace {
@@ -28,7 +29,7 @@ struct PairParams {
   const float* ref;            // [2 n_pair]
   const float* weights;        // [n_pair]
   float *margin, *loss;        // [n_pair]
-  float* d_logp;               // [2 n_pair, t_len] or null
+  float* d_logp;               // [2 n_pair], of each token of a sequence, or null
   int t_len, kind, average;
   float beta, smoothing;
 };
@@ -43,6 +44,8 @@ __global__ void __launch_bounds__(kPairThreads) pair_kernel(const __grid_constan
   __shared__ int counts[2][kPairWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const long long i = blockIdx.x;
+  grid_dependents_launch();      // (the gradient's rows wait for the end of this grid)
+  grid_dependency_wait();
   for (int q = 0; q < 2; ++q) {
     const long long at = (2 * i + q) * P.t_len;
     double s = 0.0;
@@ -81,20 +84,17 @@ __global__ void __launch_bounds__(kPairThreads) pair_kernel(const __grid_constan
   if (tid == 0) {
     P.margin[i] = static_cast<float>(m);
     P.loss[i] = static_cast<float>(w * loss);
+    if (P.d_logp)
+      for (int q = 0; q < 2; ++q) P.d_logp[2 * i + q] = static_cast<float>((q ? -w : w) * slope * per[q]);
   }
-  if (P.d_logp)
-    for (int q = 0; q < 2; ++q) {
-      const float g = static_cast<float>((q ? -w : w) * slope * per[q]);
-      for (int t = tid; t < P.t_len; t += kPairThreads) P.d_logp[(2 * i + q) * P.t_len + t] = g;
-    }
 }
 
 }  // namespace
 }  // namespace sv
 
 extern "C" size_t sv_preference_work(int n_pair, int t_len) {
-  // each row's log-sum-exp and derivative
-  return n_pair < 1 || t_len < 1 ? 0 : static_cast<size_t>(n_pair) * static_cast<size_t>(t_len) * 2 * 2;
+  // each row's log-sum-exp and each sequence's derivative
+  return n_pair < 1 || t_len < 1 ? 0 : static_cast<size_t>(n_pair) * 2 * (static_cast<size_t>(t_len) + 1);
 }
 
 extern "C" sv_status sv_preference_loss(int n_pair, int t_len, int V, sv_dtype dtype, const void* logits,
@@ -111,19 +111,26 @@ extern "C" sv_status sv_preference_loss(int n_pair, int t_len, int V, sv_dtype d
   if (!(smoothing >= 0.f && smoothing < 0.5f) || (smoothing != 0.f && kind != SV_PREF_SIGMOID)) return SV_ERR_INVALID_ARG;
   if (average != 0 && average != 1) return SV_ERR_INVALID_ARG;
   const int n_seq = 2 * n_pair;
-  const uintptr_t g = reinterpret_cast<uintptr_t>(grad), a = reinterpret_cast<uintptr_t>(logits);
-  const int elt = dtype == SV_F32 ? 4 : 2;
-  const uintptr_t bytes = static_cast<uintptr_t>(n_seq) * (t_len > 0 ? t_len : 0) * (V > 0 ? V : 0) * elt;
-  if (grad && (g % elt || (a != g && a < g + bytes && g < a + bytes))) return SV_ERR_INVALID_ARG;
+  if (!rows_ok(n_seq, t_len, V, dtype, logits, grad, temperature)) return SV_ERR_INVALID_ARG;
   NvtxRange range("sv_preference_loss");
-  float* lse = work;
-  sv_status st = sv_token_logp(n_seq, t_len, V, dtype, logits, tokens, temperature, logp, nullptr, lse, stream);
-  if (st != SV_OK) return st;
-  float* d_logp = grad ? work + static_cast<size_t>(n_seq) * t_len : nullptr;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const int rows = n_seq * t_len;
+  float *lse = work, *d_logp = grad ? work + rows : nullptr;
+  if (launch_token_logp(rows, V, dtype, logits, tokens, temperature, logp, nullptr, lse, true, s) != cudaSuccess)
+    return SV_ERR_CUDA;
   const PairParams p{tokens, logp, ref_logp, weights, margin, loss, d_logp, t_len, kind, average, beta, smoothing};
-  pair_kernel<<<static_cast<unsigned>(n_pair), kPairThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(p);
-  if (cudaGetLastError() != cudaSuccess) return SV_ERR_CUDA;
-  if (!grad) return SV_OK;
-  return sv_token_logp_grad(n_seq, t_len, V, dtype, logits, tokens, logp, lse, nullptr, d_logp, nullptr, temperature,
-                            grad, stream);
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(n_pair));
+  cfg.blockDim = dim3(kPairThreads);
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, pair_kernel, p) != cudaSuccess) return SV_ERR_CUDA;
+  if (grad && launch_token_grad(rows, V, dtype, logits, tokens, logp, lse, nullptr, d_logp, t_len, nullptr, temperature,
+                                grad, true, s) != cudaSuccess)
+    return SV_ERR_CUDA;
+  return SV_OK;
 }

@@ -34,12 +34,19 @@ __device__ __forceinline__ void store_vec16(void* p, uint4 v) {
 }
 
 // Element t of a row, not through the read-only path (the row may be an
-// output too).
+// output too): its bits, which are waited for only where their value is taken.
+template <int ELT>
+__device__ __forceinline__ uint32_t load_bits(const unsigned char* row, long long t) {
+  if (ELT == 4) return *reinterpret_cast<const volatile uint32_t*>(row + t * 4);
+  return *reinterpret_cast<const volatile unsigned short*>(row + t * 2);
+}
+template <int ELT>
+__device__ __forceinline__ float value_of(uint32_t bits) {
+  return __uint_as_float(ELT == 4 ? bits : bits << 16);
+}
 template <int ELT>
 __device__ __forceinline__ float load_elem(const unsigned char* row, long long t) {
-  if (ELT == 4) return *reinterpret_cast<const volatile float*>(row + t * 4);
-  const unsigned short h = *reinterpret_cast<const volatile unsigned short*>(row + t * 2);
-  return __uint_as_float(static_cast<uint32_t>(h) << 16);
+  return value_of<ELT>(load_bits<ELT>(row, t));
 }
 
 // Vector v of the row, -inf where it reaches past the row.

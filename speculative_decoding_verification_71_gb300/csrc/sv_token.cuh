@@ -4,7 +4,7 @@
 // With x the row's token, p = softmax(z / T) and H the entropy of p, a loss of
 // log p(x) and H with derivatives g and h has
 //   d/dz(v) = (g (1[v = x] - p(v)) - h p(v) (log p(v) + H)) / T.
-// The tokens but x are summed apart from it, about their own maximum m:
+// The tokens but x are summed apart from it, about a base m:
 //   s = sum 2^t, a = sum 2^t t, t = (z - m) c, c = log2(e) / T,
 // so that 1 - p(x) is never formed by a subtraction: a policy is sure of most of
 // its tokens, and there log p(x) = -log(1 + s') and the gradient at x is
@@ -23,21 +23,65 @@ namespace {
 constexpr float kTokFloor = -16384.f;
 constexpr float kLn2 = 0.6931471805599453f, kLog2e = 1.4426950408889634f;
 
+// A vector's values less `m`, as pairs.  bf16 values are subtracted from as they
+// are (mixed-precision sub of sm_100 and later: exact widening, one rounding), a
+// value an instruction where widening first takes one and a half.
+template <int ELT>
+__device__ __forceinline__ void tok_minus(const uint4& w, float m, f2 (&d)[Vec<ELT>::N / 2]) {
+  if constexpr (ELT == 2) {
+    const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float a, b;
+      asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tsub.rn.f32.bf16 %0, l, %3;\n\tsub.rn.f32.bf16 %1, h, %3;\n\t}"
+          : "=f"(a), "=f"(b) : "r"(ws[i]), "f"(m));
+      d[i] = pack2(a, b);
+    }
+  } else {
+    Vec<ELT>::pairs(w, d);
+    const f2 mm = pack2(m, m);
+#pragma unroll
+    for (f2& x : d) x = sub2(x, mm);
+  }
+}
+
 struct TokPart {
   float m, s, a;
 };
 __device__ __forceinline__ TokPart tok_none() { return TokPart{-INFINITY, 0.f, 0.f}; }
 
-// A thread's running maximum and sums over vectors of a row.
+// A thread's sums over vectors of a row, about a base m that need not be the
+// maximum: the token's own logit, from which everything that counts lies less than
+// 2^60 away unless the token is all but impossible.  A running maximum would cost
+// half an instruction a value and a branch in the way of the exponentials; vectors
+// whose sum comes to 2^60 (NaN and infinities among them) raise the base to the
+// maximum so far.
+constexpr float kTokHuge = 0x1p60f;
+
 template <int ELT, bool ENT>
 struct TokSum {
-  float m = -INFINITY;
+  float m;                       // -inf: none yet
   f2 s2 = 0ull, s3 = 0ull, a2 = 0ull, a3 = 0ull;
+  __device__ __forceinline__ explicit TokSum(float base) : m(base > -INFINITY && base < INFINITY ? base : -INFINITY) {}
 
   template <int U>
   __device__ __forceinline__ void add(const uint4 (&w)[U], float c2) {
-    using VT = Vec<ELT>;
-    const float vm = VT::vmax(w);        // NaN is passed over here and kept by the sum
+    if (m > -INFINITY) {
+      f2 l2 = 0ull, l3 = 0ull, b2 = 0ull, b3 = 0ull;
+      about(w, m, c2, l2, l3, b2, b3);
+      float lo, hi;
+      unpack2(add2(l2, l3), lo, hi);
+      if (lo + hi < kTokHuge) {
+        s2 = add2(s2, l2);
+        s3 = add2(s3, l3);
+        if (ENT) {
+          a2 = add2(a2, b2);
+          a3 = add2(a3, b3);
+        }
+        return;
+      }
+    }
+    const float vm = Vec<ELT>::vmax(w);  // NaN is passed over here and kept by the sum
     if (vm > m) {
       const float d = m > -INFINITY ? __fmul_rn(__fsub_rn(m, vm), c2) : kTokFloor;
       const float f = fast_exp2(d);
@@ -52,21 +96,24 @@ struct TokSum {
       s3 = mul2(s3, ff);
       m = vm;
     }
-    const float mb = m > -INFINITY ? m : 0.f;
-    const f2 mm = pack2(mb, mb), cc = pack2(c2, c2);
+    about(w, m > -INFINITY ? m : 0.f, c2, s2, s3, a2, a3);
+  }
+  template <int U>
+  __device__ __forceinline__ static void about(const uint4 (&w)[U], float base, float c2, f2& l2, f2& l3, f2& b2, f2& b3) {
+    const f2 cc = pack2(c2, c2);
 #pragma unroll
     for (const uint4& x : w) {
-      f2 z[VT::N / 2];
-      VT::pairs(x, z);
+      f2 z[Vec<ELT>::N / 2];
+      tok_minus<ELT>(x, base, z);
 #pragma unroll
-      for (int i = 0; i < VT::N / 2; i += 2) {
-        const f2 t0 = mul2(sub2(z[i], mm), cc), t1 = mul2(sub2(z[i + 1], mm), cc);
+      for (int i = 0; i < Vec<ELT>::N / 2; i += 2) {
+        const f2 t0 = mul2(z[i], cc), t1 = mul2(z[i + 1], cc);
         const f2 e0 = exp2_2(t0), e1 = exp2_2(t1);
-        s2 = add2(s2, e0);
-        s3 = add2(s3, e1);
+        l2 = add2(l2, e0);
+        l3 = add2(l3, e1);
         if (ENT) {
-          a2 = fma2(e0, floored(t0), a2);
-          a3 = fma2(e1, floored(t1), a3);
+          b2 = fma2(e0, floored(t0), b2);
+          b3 = fma2(e1, floored(t1), b3);
         }
       }
     }
@@ -89,7 +136,7 @@ struct TokSum {
   }
 };
 
-// The lanes' parts on their common maximum, the same in every lane and in a
+// The lanes' parts on their largest base, the same in every lane and in a
 // fixed order; a NaN among the sums stays (with its maximum at -inf too).
 template <bool ENT>
 __device__ __forceinline__ TokPart tok_join(const TokPart& p, float c2) {
@@ -110,7 +157,7 @@ __device__ __forceinline__ float tok_below(float z, float m, float inv_T) {
 }
 
 struct TokRow {
-  float M, Z, rZ;      // the row's maximum, its sum about it, and 1 / Z
+  float M, Z, rZ;      // a base that is no less than the token's logit, the sum about it, and 1 / Z
   float rest, px;      // 1 - p(x), p(x)
   float logp, log_Z;
   float U;             // sum p (z - M) / T
@@ -122,7 +169,7 @@ struct TokRow {
 template <bool ENT>
 __device__ __forceinline__ TokRow tok_row(const TokPart& part, float zx, float inv_T) {
   TokRow R;
-  const bool top = zx >= part.m;           // the token is the likeliest
+  const bool top = zx >= part.m;           // the token's logit is the base
   R.M = top ? zx : part.m;
   R.valid = part.s == part.s && zx == zx && R.M > -INFINITY && R.M < INFINITY;
   const float low = top ? part.m : zx;
@@ -199,14 +246,14 @@ template <int ELT, bool ENT>
 __device__ __forceinline__ uint4 tok_vec_grad(const uint4& w, const TokGrad& G, float c2) {
   using VT = Vec<ELT>;
   constexpr int N = VT::N;
-  const f2 bb = pack2(G.base, G.base), cc = pack2(c2, c2), kk = pack2(G.k, G.k);
+  const f2 cc = pack2(c2, c2), kk = pack2(G.k, G.k);
   const f2 aa = pack2(G.alpha, G.alpha), gg = pack2(G.gamma, G.gamma);
   f2 z[N / 2];
   float d[N];
-  VT::pairs(w, z);
+  tok_minus<ELT>(w, G.base, z);
 #pragma unroll
   for (int i = 0; i < N / 2; ++i) {
-    const f2 t = fma2(sub2(z[i], bb), cc, kk);
+    const f2 t = fma2(z[i], cc, kk);
     const f2 f = ENT ? fma2(TokSum<ELT, ENT>::floored(t), gg, aa) : aa;
     unpack2(mul2(exp2_2(t), f), d[2 * i], d[2 * i + 1]);
   }
