@@ -461,6 +461,10 @@ sv_status spec_kd_top_loss(int n_seq, int t_len, int V, sv_dtype dtype, int K, c
  * 1 MiB, temperature as for spec_kd_loss.  Asynchronous on `stream`; no context,
  * no allocation; every sum is taken in a fixed order.  Host-checkable errors
  * return SV_ERR_INVALID_ARG and launch nothing.
+ * Rows longer than 32 KB are staged; a wait for staged logits that lasts longer
+ * than 1 s is given up.  There is no status for it: the row and every later row
+ * (with a token) of the CTAs concerned come out as NaN, and so do the losses that
+ * they enter; no copy is left in flight and the next call is not affected.
  * ------------------------------------------------------------------------ */
 
 /* Log-probabilities of the tokens, the rows' entropies and log-sum-exps:
@@ -567,9 +571,10 @@ sv_status sv_clip_gradients(int n, const void *const *grads, const long long *si
                             float *norm, double *work, sv_stream_t stream);
 
 /* Test hook: the limit, in nanoseconds, of spec_kd_loss's and
- * spec_kd_top_loss's waits for staged logits, in the calls of the whole process
- * from here on (default 1 s).  0 makes every such wait report expiry;
- * spec_kd_top_loss's rows that stay in registers (32 KB) have none.  Negative
+ * spec_kd_top_loss's waits for staged logits, and of sv_token_logp's,
+ * sv_policy_loss's and sv_preference_loss's, in the calls of the whole process
+ * from here on (default 1 s).  0 makes every such wait report expiry; rows that
+ * stay in registers (32 KB; spec_kd_loss has none) wait for nothing.  Negative
  * restores the default. */
 sv_status spec_kd_set_wait_limit_ns(long long ns);
 

@@ -9,7 +9,8 @@
 // and its derivative in log p(x) is -r A where the unclipped term is the smaller
 // one (0 otherwise) plus kl (1 - e^d), that in H is -entropy.
 //
-// A CTA takes a row and reads it once for the sums and, for the gradient, again.
+// Short rows stay in the registers of a few warps, long ones in the shared memory
+// of a cluster, so that each is read once.
 
 #include <cuda_runtime.h>
 
@@ -100,79 +101,121 @@ __device__ __forceinline__ void policy_row(const PolicyArgs& P, const PolicyRow&
   if (ENT) loss = __fmaf_rn(-P.entropy, R.entropy(), loss);
 }
 
-constexpr int kRowThreads = 512, kRowWarps = kRowThreads / 32;
-
+// Zeros in a row's place, by `threads` threads of which this is `tid`.
 template <int ELT>
-__device__ __forceinline__ void zero_row(unsigned char* grad, int V, int shift, int nvec, int same_shift, int threads) {
-  for (int v = threadIdx.x; v < nvec; v += threads)
-    store_edge<ELT>(grad, V, v * Vec<ELT>::N - shift, same_shift, make_uint4(0, 0, 0, 0));
+__device__ __forceinline__ void zero_row(unsigned char* grad, int V, int tid, int threads) {
+  const int shift = row_shift<ELT>(grad), nvec = row_vecs<ELT>(V, shift);
+  for (int v = tid; v < nvec; v += threads) store_edge<ELT>(grad, V, v * Vec<ELT>::N - shift, 1, make_uint4(0, 0, 0, 0));
 }
 
-template <int ELT, bool ENT>
-__device__ __forceinline__ void write_gradient(const unsigned char* row, unsigned char* grad, int V, int shift, int nvec,
-                                               int same_shift, int x, const TokGrad& G, float c2) {
-  constexpr int N = Vec<ELT>::N;
-  for (int v = threadIdx.x; v < nvec; v += blockDim.x) {
-    const uint4 w = load_row_vec<ELT>(row, V, shift, v);
-    store_edge<ELT>(grad, V, v * N - shift, same_shift, tok_vec_grad<ELT, ENT>(w, G, c2));
-    if (static_cast<unsigned>(x + shift - v * N) < static_cast<unsigned>(N)) Vec<ELT>::store_rounded(grad, x, G.at_token);
-  }
-}
+// ---- short rows: in the registers of one, two or four warps
+//
+// A warp holds 8 KB of a row, 16 vectors a lane, and asks for them all at once;
+// sixteen warps an SM keep 128 KB on their way.  A row is read once, its warps meet
+// at one barrier, and no CTA waits for another.  Bound by instructions: what a row's
+// numbers take beside its logits, by every warp of its own.
+constexpr int kShThreads = 128, kShWarps = kShThreads / 32, kShPerLane = 16, kShChunk = 4;
+constexpr int kShPerSm = 4;                                 // CTAs
+constexpr int kShMaxVecs = kShWarps * 32 * kShPerLane;      // of a row
 
-template <int ELT, bool ENT, bool GRAD>
-__global__ void __launch_bounds__(kRowThreads) token_row_kernel(const __grid_constant__ RowParams P) {
-  constexpr int N = Vec<ELT>::N;
-  __shared__ TokPart parts[kRowWarps];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const long long r = blockIdx.x;
-  const unsigned char* row = P.logits + r * P.V * ELT;
-  unsigned char* grad = GRAD ? P.grad + r * P.V * ELT : nullptr;
-  const int shift = row_shift<ELT>(row), nvec = row_vecs<ELT>(P.V, shift);
+template <int ELT, bool ENT, bool GRAD, int G>
+__global__ void __launch_bounds__(kShThreads, kShPerSm) token_short_kernel(const __grid_constant__ RowParams P, int rows) {
+  using VT = Vec<ELT>;
+  constexpr int N = VT::N, kGroups = kShWarps / G;
+  __shared__ TokPart parts[2][kShWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, group = warp / G, sub = warp % G, tid = sub * 32 + lane;
   if (P.followed) grid_dependents_launch();
-  const int x = P.tokens[r];
-  if (x < 0) {
-    if (tid == 0) {
-      P.logp[r] = 0.f;
-      if (P.entropy) P.entropy[r] = 0.f;
-      if (P.lse) P.lse[r] = -INFINITY;
-      if (P.row_loss) P.row_loss[r] = 0.f;
+  const int stride = static_cast<int>(gridDim.x) * kGroups;
+  int par = 0, r = static_cast<int>(blockIdx.x) * kGroups + group;
+  int x_next = r < rows ? P.tokens[r] : -1;
+  for (; r < rows; r += stride, par ^= 1) {
+    const int x_row = x_next;
+    x_next = r + stride < rows ? P.tokens[r + stride] : -1;
+    const unsigned long long at_row = static_cast<unsigned long long>(r) * (static_cast<unsigned>(P.V) * ELT);
+    const unsigned char* row = P.logits + at_row;
+    unsigned char* grad = GRAD ? P.grad + at_row : nullptr;
+    if (x_row < 0) {
+      if (tid == 0) {
+        P.logp[r] = 0.f;
+        if (P.entropy) P.entropy[r] = 0.f;
+        if (P.lse) P.lse[r] = -INFINITY;
+        if (P.row_loss) P.row_loss[r] = 0.f;
+      }
+      if (GRAD) zero_row<ELT>(grad, P.V, tid, G * 32);
+      continue;
     }
-    if (GRAD) zero_row<ELT>(grad, P.V, shift, nvec, P.same_shift, kRowThreads);
-    return;
-  }
-  const float zx = x < P.V ? load_elem<ELT>(row, x) : NAN;
-  TokSum<ELT, ENT> sum(zx);
-  for (int v = tid; v < nvec; v += kRowThreads) {
-    uint4 w[1] = {load_row_vec<ELT>(row, P.V, shift, v)};
-    tok_take_out<ELT>(w[0], x + shift - v * N);
-    sum.add(w, P.c2);
-  }
-  TokPart part = tok_join<ENT>(sum.part(), P.c2);
-  if (lane == 0) parts[warp] = part;
-  __syncthreads();
-  part = tok_join<ENT>(lane < kRowWarps ? parts[lane] : tok_none(), P.c2);
-  const TokRow R = tok_row<ENT>(part, zx, P.inv_T);
-  float loss = 0.f, slope = 0.f;
-  float w = 0.f;
-  if (P.row_loss) {
-    const PolicyRow mine = PolicyRow::of(P.policy, static_cast<int>(r), P.t_len);
-    policy_row<ENT>(P.policy, mine, R, loss, slope);
-    w = mine.weight;
-  }
-  if (tid == 0) {
-    P.logp[r] = R.logp;
-    if (ENT && P.entropy) P.entropy[r] = R.entropy();
-    if (P.lse) P.lse[r] = R.lse(P.inv_T);
-    if (P.row_loss) P.row_loss[r] = loss;
-  }
-  if (GRAD) {
-    const TokGrad G = tok_grad<ENT>(R, w * slope, ENT ? -P.policy.entropy * w : 0.f, P.inv_T);
-    __syncthreads();             // (in place: every thread has read the row)
-    write_gradient<ELT, ENT>(row, grad, P.V, shift, nvec, P.same_shift, x, G, P.c2);
+    const int shift = row_shift<ELT>(row), nvec = row_vecs<ELT>(P.V, shift);
+    const uint32_t zx_bits = load_bits<ELT>(row, min(x_row, P.V - 1));
+    uint4 w[kShPerLane];
+#pragma unroll
+    for (int c = 0; c < kShPerLane; c += kShChunk) {
+      const int v0 = c * G * 32, v1 = (c + kShChunk) * G * 32;       // the chunk's vectors, of all the row's warps
+      if (v0 * N - shift >= 0 && v1 * N - shift <= P.V) {
+        const unsigned char* at = row + (static_cast<long long>(v0 + tid) * N - shift) * ELT;
+#pragma unroll
+        for (int k = 0; k < kShChunk; ++k) w[c + k] = load_vec16(at + k * G * 512);
+      } else if (v0 < nvec) {
+#pragma unroll
+        for (int k = 0; k < kShChunk; ++k)
+          w[c + k] = v0 + k * G * 32 + tid < nvec ? load_row_vec<ELT>(row, P.V, shift, v0 + k * G * 32 + tid) : VT::neg_inf();
+      }
+    }
+    PolicyRow mine{};
+    if (P.row_loss) mine = PolicyRow::of(P.policy, r, P.t_len);
+    const int x = x_row < P.V ? x_row : -(1 << 30), x_vec = (x + shift) / N;
+    const float zx = x_row < P.V ? value_of<ELT>(zx_bits) : NAN;
+    TokSum<ELT, ENT> sum(zx);
+#pragma unroll
+    for (int c = 0; c < kShPerLane; c += kShChunk) {
+      if (c * G * 32 < nvec) {
+        uint4 some[kShChunk];
+#pragma unroll
+        for (int k = 0; k < kShChunk; ++k) {
+          some[k] = w[c + k];
+          if ((c + k) * G * 32 + tid == x_vec) tok_take_out<ELT>(some[k], x + shift - x_vec * N);
+        }
+        sum.add(some, P.c2);
+      }
+    }
+    TokPart part = sum.part();
+    if (zx != zx) part.s = NAN;
+    part = tok_join<ENT>(part, P.c2);
+    if (G > 1) {
+      if (lane == 0) parts[par][warp] = part;
+      named_barrier_sync(1 + group, G * 32);
+      part = tok_join<ENT>(lane < G ? parts[par][group * G + lane] : tok_none(), P.c2);
+    }
+    const TokRow R = tok_row<ENT>(part, zx, P.inv_T);
+    float loss = 0.f, slope = 0.f;
+    if (P.row_loss) policy_row<ENT>(P.policy, mine, R, loss, slope);
+    if (tid == 0) {
+      P.logp[r] = R.logp;
+      if (ENT && P.entropy) P.entropy[r] = R.entropy();
+      if (P.lse) P.lse[r] = R.lse(P.inv_T);
+      if (P.row_loss) P.row_loss[r] = loss;
+    }
+    if (GRAD) {
+      const TokGrad D = tok_grad<ENT>(R, mine.weight * slope, ENT ? -P.policy.entropy * mine.weight : 0.f, P.inv_T);
+#pragma unroll
+      for (int c = 0; c < kShPerLane; c += kShChunk) {
+        const int v0 = c * G * 32, v1 = (c + kShChunk) * G * 32;
+        if (P.same_shift && v0 * N - shift >= 0 && v1 * N - shift <= P.V) {
+          unsigned char* at = grad + (static_cast<long long>(v0 + tid) * N - shift) * ELT;
+#pragma unroll
+          for (int k = 0; k < kShChunk; ++k) store_vec16(at + k * G * 512, tok_vec_grad<ELT, ENT>(w[c + k], D, P.c2));
+        } else if (v0 < nvec) {
+#pragma unroll
+          for (int k = 0; k < kShChunk; ++k)
+            if (v0 + k * G * 32 + tid < nvec)
+              store_edge<ELT>(grad, P.V, (v0 + k * G * 32 + tid) * N - shift, P.same_shift, tok_vec_grad<ELT, ENT>(w[c + k], D, P.c2));
+        }
+      }
+      // the token's own after its vector's, by the same thread
+      if (x_vec >= 0 && x >= 0 && x_vec % (G * 32) == tid) VT::store_rounded(grad, x, D.at_token);
+    }
   }
 }
 
-constexpr int kRgGradWorkers = 16;
 // ---- long rows: streamed through shared memory, where they stay for the gradient
 //
 // A row goes to a cluster of 1 to 8 CTAs, a part to each.  A producer warp streams
@@ -199,7 +242,7 @@ constexpr int kRgGradWorkers = 16;
 // last, when its copies have landed.
 template <bool GRAD>
 struct Rg {
-  static constexpr int kWorkers = GRAD ? kRgGradWorkers : 8;
+  static constexpr int kWorkers = GRAD ? 16 : 8;
   static constexpr int kPerLane = 32 / kWorkers;             // vectors per lane and slot
   static constexpr int kWork = kWorkers * 32, kThreads = kWork + 64;   // + the producer's and the row's warp
   static constexpr int kSlotVecs = kWork * kPerLane, kSlotBytes = kSlotVecs * 16;
@@ -212,7 +255,6 @@ constexpr int kRgMaxCtas = 8;
 constexpr int kRgWindow = 8192;                             // rows whose tokens are looked at together
 constexpr int kRgLive = 448, kRgDead = 64;                  // of which a cluster, a CTA gets so many at most
 constexpr int kRgSms = 152;
-constexpr int kRgMinRow = 32 * 1024;                        // bytes of a row that is streamed
 constexpr int kRgMinPart = 16 * 1024;                       // and where a row is split for want of rows
 constexpr long long kRgJoinLimitNs = 4 * kDrainLimitNs;     // a CTA's part comes within an expired wait
 constexpr long long kRgRowLimitNs = 2 * kRgJoinLimitNs;     // and a row's numbers within that one
@@ -609,9 +651,7 @@ __global__ void __launch_bounds__(Rg<GRAD>::kThreads, Rg<GRAD>::kPerSm)
         if (x_vec >= 0 && x_vec < t.n && x_vec % kWork == tid) VT::store_rounded(grad, x, G.at_token);
         // rows without a token, as many as there are for each row with one
         for (; static_cast<long long>(filled) * n_live < static_cast<long long>(i + 1 - ahead) * n_dead; ++filled) {
-          unsigned char* zero = P.grad + (w0 + sh.dead[filled]) * P.V * ELT;
-          const int shift = row_shift<ELT>(zero);
-          zero_row<ELT>(zero, P.V, shift, row_vecs<ELT>(P.V, shift), 1, kWork);
+          zero_row<ELT>(P.grad + static_cast<unsigned long long>(w0 + sh.dead[filled]) * row_bytes, P.V, tid, kWork);
         }
       }
       x_before = x_now;
@@ -619,9 +659,7 @@ __global__ void __launch_bounds__(Rg<GRAD>::kThreads, Rg<GRAD>::kPerSm)
     turn += static_cast<unsigned>(n_live);
     if (GRAD)
       for (; filled < n_dead; ++filled) {
-        unsigned char* zero = P.grad + (w0 + sh.dead[filled]) * P.V * ELT;
-        const int shift = row_shift<ELT>(zero);
-        zero_row<ELT>(zero, P.V, shift, row_vecs<ELT>(P.V, shift), 1, kWork);
+        zero_row<ELT>(P.grad + static_cast<unsigned long long>(w0 + sh.dead[filled]) * row_bytes, P.V, tid, kWork);
       }
   }
   // ---- no copy is left in flight, and nothing on its way to a CTA that has left
@@ -669,7 +707,8 @@ __global__ void __launch_bounds__(kGrThreads, 4) token_grad_kernel(const __grid_
   using VT = Vec<ELT>;
   constexpr int N = VT::N;
   const int tid = threadIdx.x;
-  const int r = static_cast<int>(blockIdx.x) / parts, part = static_cast<int>(blockIdx.x) % parts;
+  // the last rows first: token_logp, just before, has left them in L2
+  const int r = static_cast<int>(gridDim.x / parts - 1 - blockIdx.x / parts), part = static_cast<int>(blockIdx.x) % parts;
   const unsigned long long at_row = static_cast<unsigned long long>(r) * (static_cast<unsigned>(P.V) * ELT);
   const unsigned char* row = P.logits + at_row;
   unsigned char* grad = P.grad + at_row;
@@ -819,8 +858,15 @@ cudaError_t launch_ring(const RowParams& p, int rows, cudaStream_t s) {
 
 template <int ELT, bool ENT, bool GRAD>
 cudaError_t launch_rows(const RowParams& p, int rows, cudaStream_t s) {
-  if (static_cast<long long>(p.V) * ELT > kRgMinRow) return launch_ring<ELT, ENT, GRAD>(p, rows, s);
-  token_row_kernel<ELT, ENT, GRAD><<<static_cast<unsigned>(rows), kRowThreads, 0, s>>>(p);
+  const int nvec = (p.V + 2 * Vec<ELT>::N - 2) / Vec<ELT>::N;      // of a row off the 16-byte boundary
+  if (nvec > kShMaxVecs) return launch_ring<ELT, ENT, GRAD>(p, rows, s);
+  // as few warps to a row as hold it; four where rows are few
+  const int grid = kRgSms * kShPerSm;
+  const int warps = nvec > 2 * 32 * kShPerLane || rows <= grid ? 4 : nvec > 32 * kShPerLane ? 2 : 1;
+  const unsigned ctas = static_cast<unsigned>(std::min<long long>(grid, (static_cast<long long>(rows) * warps + kShWarps - 1) / kShWarps));
+  if (warps == 4) token_short_kernel<ELT, ENT, GRAD, 4><<<ctas, kShThreads, 0, s>>>(p, rows);
+  else if (warps == 2) token_short_kernel<ELT, ENT, GRAD, 2><<<ctas, kShThreads, 0, s>>>(p, rows);
+  else token_short_kernel<ELT, ENT, GRAD, 1><<<ctas, kShThreads, 0, s>>>(p, rows);
   return cudaGetLastError();
 }
 

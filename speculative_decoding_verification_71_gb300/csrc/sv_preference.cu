@@ -36,8 +36,10 @@ struct PairParams {
 
 constexpr int kPairThreads = 256, kPairWarps = kPairThreads / 32;
 
-// log(1 + e^x)
-__device__ __forceinline__ double softplus(double x) { return fmax(x, 0.0) + log1p(exp(-fabs(x))); }
+// log(1 + e^x) and 1 / (1 + e^-x).  The sums and h are taken in 64 bits, what
+// follows in 32: with 64-bit exponentials in every thread a pair took 14 us.
+__device__ __forceinline__ float softplus(float x) { return fmaxf(x, 0.f) + log1pf(expf(-fabsf(x))); }
+__device__ __forceinline__ float sigmoid(float x) { return __fdiv_rn(1.f, 1.f + expf(-x)); }
 
 __global__ void __launch_bounds__(kPairThreads) pair_kernel(const __grid_constant__ PairParams P) {
   __shared__ double sums[2][kPairWarps];
@@ -59,34 +61,42 @@ __global__ void __launch_bounds__(kPairThreads) pair_kernel(const __grid_constan
     if (lane == 0) sums[q][warp] = s, counts[q][warp] = n;
   }
   __syncthreads();
+  if (tid) return;
   double s[2] = {0.0, 0.0};
   int n[2] = {0, 0};
   for (int w = 0; w < kPairWarps; ++w)
     for (int q = 0; q < 2; ++q) s[q] += sums[q][w], n[q] += counts[q][w];
-  double per[2] = {1.0, 1.0};
+  float per[2] = {1.f, 1.f};
   if (P.average)
-    for (int q = 0; q < 2; ++q) per[q] = 1.0 / (n[q] > 1 ? n[q] : 1);
-  const double h = (s[0] * per[0] - s[1] * per[1]) -
-                   (static_cast<double>(P.ref[2 * i]) - static_cast<double>(P.ref[2 * i + 1]));
-  const double beta = P.beta, m = beta * h, e = P.smoothing, w = P.weights[i];
-  double loss, slope;
+    for (int q = 0; q < 2; ++q)
+      if (n[q] > 1) {
+        s[q] /= n[q];
+        per[q] = __fdiv_rn(1.f, static_cast<float>(n[q]));
+      }
+  const double h = (s[0] - s[1]) - (static_cast<double>(P.ref[2 * i]) - static_cast<double>(P.ref[2 * i + 1]));
+  const float m = static_cast<float>(P.beta * h), e = P.smoothing, w = P.weights[i];
+  float loss, slope;
   if (P.kind == SV_PREF_SIGMOID) {
-    loss = (1.0 - e) * softplus(-m) + (e > 0.0 ? e * softplus(m) : 0.0);
-    slope = beta * (e / (1.0 + exp(-m)) - (1.0 - e) / (1.0 + exp(m)));
+    loss = (1.f - e) * softplus(-m);
+    slope = -(1.f - e) * sigmoid(-m);
+    if (e > 0.f) {
+      loss = __fmaf_rn(e, softplus(m), loss);
+      slope = __fmaf_rn(e, sigmoid(m), slope);
+    }
+    slope *= P.beta;
   } else if (P.kind == SV_PREF_HINGE) {
-    loss = m < 1.0 ? 1.0 - m : m == m ? 0.0 : m;
-    slope = m < 1.0 ? -beta : m == m ? 0.0 : m;
+    const double room = 1.0 - P.beta * h;
+    loss = room > 0.0 ? static_cast<float>(room) : m == m ? 0.f : m;
+    slope = room > 0.0 ? -P.beta : m == m ? 0.f : m;
   } else {
-    const double off = h - 0.5 / beta;
-    loss = off * off;
-    slope = 2.0 * off;
+    const double off = h - 0.5 / P.beta;
+    loss = static_cast<float>(off * off);
+    slope = static_cast<float>(2.0 * off);
   }
-  if (tid == 0) {
-    P.margin[i] = static_cast<float>(m);
-    P.loss[i] = static_cast<float>(w * loss);
-    if (P.d_logp)
-      for (int q = 0; q < 2; ++q) P.d_logp[2 * i + q] = static_cast<float>((q ? -w : w) * slope * per[q]);
-  }
+  P.margin[i] = m;
+  P.loss[i] = w * loss;
+  if (P.d_logp)
+    for (int q = 0; q < 2; ++q) P.d_logp[2 * i + q] = (q ? -w : w) * slope * per[q];
 }
 
 }  // namespace

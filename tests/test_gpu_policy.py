@@ -176,9 +176,14 @@ def run_preference(z, x, T=1.0, beta=0.1, kind="sigmoid", smoothing=0.0, average
               for d in (0.0, tol_s[a] + tol_s[b], -tol_s[a] - tol_s[b])]
         (m, l, k), spread = at[0], [max(abs(at[j][q] - at[0][q]) for j in (1, 2)) for q in range(3)]
         assert_close(margin[i], np.array(m), np.array(spread[0]), what="margin")
-        assert_close(loss[i], np.array(l), np.array(spread[1]) + 1e-30, what="loss")
+        # from m, rounded to float32 (2^-24 |m|, of which softplus passes on at most
+        # w |slope| / beta and the sigmoid's logarithm all), the loss and its slope
+        # come by up to eight float32 steps: expf and log1pf or a division (one ulp
+        # each, 2^-23), a sum, 1 - e, the products with it, w, beta and 1 / n (2^-24)
+        near = 2.0 ** -24 * (10 + abs(m)) if math.isfinite(m) else 0.0
+        assert_close(loss[i], np.array(l), np.array(spread[1]) + near * (abs(l) + abs(k) / beta) + 1e-30, what="loss")
         slopes[a], slopes[b] = k * per[a], -k * per[b]
-        tol_g[a], tol_g[b] = (spread[2] + 2.0 ** -23 * abs(k)) * per[a], (spread[2] + 2.0 ** -23 * abs(k)) * per[b]
+        tol_g[a], tol_g[b] = (spread[2] + near * abs(k)) * per[a], (spread[2] + near * abs(k)) * per[b]
     if grad:
         each = lambda v: np.repeat(v, t_len)
         dref, tol = R.gradient(each(slopes), np.zeros(R.n), each(tol_g))
@@ -501,3 +506,98 @@ def test_offsets_past_32_bits():
         assert_close(grad[1:, -1:], ref, tol + 2.0 ** -7 * np.abs(ref), BF16)
         assert (grad[0, 0] == 0).all() and (grad[1, -2] == 0).all()
         del grad
+
+
+@pytest.mark.parametrize("entropy", [False, True])
+@pytest.mark.parametrize("V,dtype", [(17000, BF16), (9001, F32)])
+def test_more_rows_than_are_looked_at_together(V, dtype, entropy):
+    """Padded rollouts of more rows than a window of tokens holds, on rows that
+    are streamed: every row's numbers, and every gradient, in 64 bits."""
+    n_seq, t_len = 3, 6700
+    g = torch.Generator(device=DEV).manual_seed(1)
+    z = (torch.randn(n_seq, t_len, V, device=DEV, generator=g, dtype=F32) * 2).to(dtype)
+    x = torch.randint(0, V, (n_seq, t_len), device=DEV, generator=g).to(torch.int32)
+    x[0, 1500:] = -1
+    x[1, :4000] = -1
+    x[2][torch.rand(t_len, device=DEV, generator=g) < 0.5] = -1
+    A = torch.randn(n_seq, t_len, device=DEV, generator=g)
+    w = torch.ones(n_seq, device=DEV)
+    logp, H, row_loss, loss, grad = svp.policy_loss(z, x, A, w, entropy_coef=0.1 if entropy else 0.0)
+    again = svp.token_logp(z, x, entropy=entropy)
+    have = x >= 0
+    for b in range(n_seq):
+        for a in range(0, t_len, 500):
+            at = slice(a, a + 500)
+            zz, live = z[b, at].double(), have[b, at]
+            lp = torch.log_softmax(zz, 1)
+            p = lp.exp()
+            tok = x[b, at].long().clamp(min=0)[:, None]
+            lpx = torch.where(live, lp.gather(1, tok)[:, 0], 0.0)
+            ent = torch.where(live, -(p * lp).sum(1), 0.0)
+            assert (logp[b, at] - lpx).abs().max() < 2 * REL and (again[0][b, at] - lpx).abs().max() < 2 * REL
+            lse = torch.where(live, torch.logsumexp(zz, 1), -INF)
+            assert (again[2][b, at].double() - lse).nan_to_num(0.0).abs().max() < 2 * REL
+            gg = -A[b, at].double()
+            d = -p * gg[:, None]
+            d.scatter_add_(1, tok, gg[:, None])
+            if entropy:
+                assert (H[b, at] - ent).abs().max() < 10 * REL * (1 + ent.abs().max())
+                d = d + 0.1 * p * (lp + ent[:, None])
+            d = torch.where(live[:, None], d, 0.0)
+            got = grad[b, at].double()
+            # float32: 4 REL of the two parts' sizes; bf16 half a step more
+            size = p * gg.abs()[:, None] + (0.1 * p * (lp.abs() + ent[:, None] + 1) if entropy else 0.0)
+            size.scatter_add_(1, tok, gg.abs()[:, None] * (1 - p.gather(1, tok)))
+            assert ((got - d).abs() <= 4 * REL * size + (2.0 ** -8 if dtype == BF16 else 2.0 ** -24) * d.abs() * 1.001 + 1e-37).all()
+    assert torch.equal(loss, row_loss.double().sum(1).float()) or (loss - row_loss.double().sum(1)).abs().max() < 1e-3
+
+
+# ---------------------------------------------------------------------------
+# Waits that expire
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("V,dtype", [(20000, BF16), (128256, BF16), (151936, F32)])
+def test_an_expired_wait_gives_nan_and_leaves_the_next_call_alone(V, dtype):
+    z, x = make_rows(6, 30, V, dtype, seed=1)
+    zd, xd, w = z.to(DEV), x.to(DEV), torch.ones(6, device=DEV)
+    want = svp.policy_loss(zd, xd, w, w)
+    lib = svp.load_library()
+    live = (x >= 0).to(DEV)
+    try:
+        assert lib.spec_kd_set_wait_limit_ns(0) == svp.SV_OK
+        logp, _, row_loss, loss, grad = svp.policy_loss(zd, xd, w, w)
+        alone = svp.token_logp(zd, xd, entropy=True)
+        torch.cuda.synchronize()
+    finally:
+        lib.spec_kd_set_wait_limit_ns(-1)
+    for t in (logp, row_loss, *alone):
+        assert t[live].isnan().all()
+    assert (logp[~live] == 0).all() and (row_loss[~live] == 0).all() and (alone[2][~live] == -INF).all()
+    assert loss[live.any(1)].isnan().all()
+    assert grad[live].isnan().all() and (grad[~live] == 0).all()
+    for a, b in zip(want, svp.policy_loss(zd, xd, w, w)):
+        assert (a is None and b is None) or torch.equal(a, b)
+
+
+def test_a_first_call_can_be_captured():
+    """In a process of its own: nothing has been launched before the capture."""
+    import subprocess
+    import sys
+    code = """
+import torch, speculative_decoding_verification_71_gb300 as svp
+z = torch.randn(3, 4, 70001, device="cuda"); x = torch.randint(0, 70001, (3, 4), device="cuda").to(torch.int32)
+w = torch.ones(3, device="cuda"); y = z[:2, :, :3001].contiguous(); g = torch.cuda.CUDAGraph()
+torch.cuda.synchronize()
+with torch.cuda.graph(g):
+    a = svp.policy_loss(z, x, w, w, entropy_coef=0.1)
+    b = svp.preference_loss(y, x[:2] % 3001, w[:2], w[:1])
+    c = svp.clip_gradients([z], 1e9)
+g.replay(); torch.cuda.synchronize()
+d = svp.policy_loss(z, x, w, w, entropy_coef=0.1)
+assert all(torch.equal(p, q) for p, q in zip(a, d)) and a[4].abs().max() > 0 and b[3].abs().max() > 0 and c.item() > 0
+print("captured")
+"""
+    import os
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    out = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300, cwd=root)
+    assert "captured" in out.stdout, out.stderr[-2000:]
