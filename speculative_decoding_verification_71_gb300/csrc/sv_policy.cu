@@ -45,6 +45,7 @@ struct RowParams {
   const unsigned char* logits; // [rows, V]
   const int* tokens;           // [rows]
   float *logp, *entropy, *lse; // [rows]; entropy and lse or null
+  float* logp_rest;            // [rows]: what the rounding of logp left, or null
   float* row_loss;             // [rows]: a policy's loss; null for the log-probabilities alone
   unsigned char* grad;         // [rows, V] or null
   int t_len, V;
@@ -82,7 +83,7 @@ template <bool ENT>
 __device__ __forceinline__ void policy_row(const PolicyArgs& P, const PolicyRow& row, const TokRow& R, float& loss,
                                            float& slope) {
   const float A = row.A;
-  const float r = P.old_logp ? expf(__fsub_rn(R.logp, row.old_logp)) : 1.f;
+  const float r = P.old_logp ? expf(__fadd_rn(__fsub_rn(R.logp, row.old_logp), R.logp_rest)) : 1.f;
   const float low = 1.f - P.low, high = 1.f + P.high;
   const float gained = r * A, held = (r < low ? low : r > high ? high : r) * A;
   float gain = gained <= held ? gained : held;
@@ -94,7 +95,7 @@ __device__ __forceinline__ void policy_row(const PolicyArgs& P, const PolicyRow&
   }
   loss = R.valid ? -gain : NAN;
   if (P.ref_logp) {
-    const float d = __fsub_rn(row.ref_logp, R.logp), up = expm1f(d);
+    const float d = __fsub_rn(__fsub_rn(row.ref_logp, R.logp), R.logp_rest), up = expm1f(d);
     loss = __fmaf_rn(P.kl, kl_term(d, up), loss);
     slope = __fmaf_rn(-P.kl, up, slope);
   }
@@ -139,6 +140,7 @@ __global__ void __launch_bounds__(kShThreads, kShPerSm) token_short_kernel(const
         P.logp[r] = 0.f;
         if (P.entropy) P.entropy[r] = 0.f;
         if (P.lse) P.lse[r] = -INFINITY;
+        if (P.logp_rest) P.logp_rest[r] = 0.f;
         if (P.row_loss) P.row_loss[r] = 0.f;
       }
       if (GRAD) zero_row<ELT>(grad, P.V, tid, G * 32);
@@ -192,6 +194,7 @@ __global__ void __launch_bounds__(kShThreads, kShPerSm) token_short_kernel(const
       P.logp[r] = R.logp;
       if (ENT && P.entropy) P.entropy[r] = R.entropy();
       if (P.lse) P.lse[r] = R.lse(P.inv_T);
+      if (P.logp_rest) P.logp_rest[r] = R.logp_rest;
       if (P.row_loss) P.row_loss[r] = loss;
     }
     if (GRAD) {
@@ -430,6 +433,7 @@ __global__ void __launch_bounds__(Rg<GRAD>::kThreads, Rg<GRAD>::kPerSm)
             P.logp[r] = 0.f;
             if (P.entropy) P.entropy[r] = 0.f;
             if (P.lse) P.lse[r] = -INFINITY;
+            if (P.logp_rest) P.logp_rest[r] = 0.f;
             if (P.row_loss) P.row_loss[r] = 0.f;
           }
         }
@@ -521,6 +525,7 @@ __global__ void __launch_bounds__(Rg<GRAD>::kThreads, Rg<GRAD>::kPerSm)
           P.logp[r] = row.logp;
           if (ENT && P.entropy) P.entropy[r] = row.entropy();
           if (P.lse) P.lse[r] = row.lse(P.inv_T);
+          if (P.logp_rest) P.logp_rest[r] = row.logp_rest;
           if (P.row_loss) P.row_loss[r] = loss;
         }
         x = x_next;
@@ -906,11 +911,12 @@ bool rows_ok(int n_seq, int t_len, int V, sv_dtype dtype, const void* logits, co
 }
 
 cudaError_t launch_token_logp(int rows, int V, sv_dtype dtype, const void* logits, const int32_t* tokens,
-                              float temperature, float* logp, float* entropy, float* lse, bool followed, cudaStream_t s) {
+                              float temperature, float* logp, float* entropy, float* lse, float* logp_rest, bool followed, cudaStream_t s) {
   RowParams p = row_params(1, V, logits, tokens, temperature, nullptr);
   p.logp = logp;
   p.entropy = entropy;
   p.lse = lse;
+  p.logp_rest = logp_rest;
   p.followed = followed;
   return dtype == SV_BF16 ? launch_rows<2>(p, rows, entropy != nullptr, s) : launch_rows<4>(p, rows, entropy != nullptr, s);
 }
@@ -934,7 +940,7 @@ extern "C" sv_status sv_token_logp(int n_seq, int t_len, int V, sv_dtype dtype, 
   if (!rows_ok(n_seq, t_len, V, dtype, logits, nullptr, temperature) || !tokens || !logp || !lse)
     return SV_ERR_INVALID_ARG;
   NvtxRange range("sv_token_logp");
-  return launch_token_logp(n_seq * t_len, V, dtype, logits, tokens, temperature, logp, entropy, lse, false,
+  return launch_token_logp(n_seq * t_len, V, dtype, logits, tokens, temperature, logp, entropy, lse, nullptr, false,
                            reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? SV_OK : SV_ERR_CUDA;
 }
 

@@ -15,9 +15,10 @@ bool rows_ok(int n_seq, int t_len, int V, sv_dtype dtype, const void* logits, co
 
 // sv_token_logp and sv_token_logp_grad without their checks.  `followed`: the next
 // kernel on the stream waits for this one itself; `dependent`: the kernel before
-// is so followed.  `d_rows` rows share a d_logp.
+// is so followed.  `d_rows` rows share a d_logp.  logp_rest, or null, takes what
+// the rounding of logp left, for sums of many.
 cudaError_t launch_token_logp(int rows, int V, sv_dtype dtype, const void* logits, const int32_t* tokens,
-                              float temperature, float* logp, float* entropy, float* lse, bool followed, cudaStream_t s);
+                              float temperature, float* logp, float* entropy, float* lse, float* logp_rest, bool followed, cudaStream_t s);
 cudaError_t launch_token_grad(int rows, int V, sv_dtype dtype, const void* logits, const int32_t* tokens,
                               const float* logp, const float* lse, const float* entropy, const float* d_logp, int d_rows,
                               const float* d_entropy, float temperature, void* grad, bool dependent, cudaStream_t s);
