@@ -88,7 +88,8 @@ def parse():
     ap.add_argument("--profile-kernels", default="",
                     help="run each named kernel's representative case twice (for ncu, one kernel per "
                          "capture): comma list of verify (the default schedule), verify_cluster, verify_dense, early_exit, "
-                         "compact, debug, kd, tree, ctrl, process, kd_top, kd_top_loss")
+                         "compact, debug, kd, tree, ctrl, process, kd_top, kd_top_loss, "
+                         "token_logp, policy_loss, token_grad, clip")
     return ap.parse_args()
 
 
@@ -844,7 +845,12 @@ def profile_kernels(args):
                       penalties: logits_kernel
       kd_top          kd_top of the ragged batch's emitted rows, 64 tokens a row: top_kernel
       kd_top_loss     kd_top_loss with the gradient, 16 rollouts x 64 positions, V=151936 bf16, lists of 64 tokens:
-                      toploss_kernel + toploss_sum_kernel
+                      toploss_kernel + row_sum_kernel
+      token_logp      token_logp with entropies, 16 rollouts x 64 positions, V=151936 bf16: token_ring_kernel
+      policy_loss     policy_loss with a divergence and the gradient on them: token_ring_kernel + row_sum_kernel
+      token_grad      token_logp_grad on them: token_grad_kernel
+      clip            clip_gradients of four matrices of 8192 x 8192 bf16 into float32: clip_norm_kernel +
+                      clip_scale_kernel
     """
     import torch
 
@@ -942,6 +948,25 @@ def profile_kernels(args):
                 ids, logp, _ = svp.kd_top(t.to(torch.bfloat16), 64)
                 svp.kd_top_loss(ids, logp, d, torch.rand(16, generator=g, device=device))
                 del t, d
+            elif name in ("token_logp", "policy_loss", "token_grad"):
+                g = torch.Generator(device=device).manual_seed(14)
+                z = (torch.randn(16, 64, 151936, generator=g, device=device) * 3.0).to(torch.bfloat16)
+                x = torch.randint(0, 151936, (16, 64), generator=g, device=device).to(torch.int32)
+                if name == "token_logp":
+                    svp.token_logp(z, x, entropy=True)
+                elif name == "policy_loss":
+                    a = torch.randn(16, generator=g, device=device)
+                    old = torch.full((16, 64), -15.0, device=device)
+                    svp.policy_loss(z, x, a, torch.ones_like(a), old_logp=old, ref_logp=old, kl_coef=0.02)
+                else:
+                    logp, _, lse = svp.token_logp(z, x)
+                    svp.token_logp_grad(z, x, logp, lse, torch.randn(16, 64, generator=g, device=device))
+                del z
+            elif name == "clip":
+                g = torch.Generator(device=device).manual_seed(15)
+                ms = [(torch.randn(8192, 8192, generator=g, device=device) * 1e-3).to(torch.bfloat16) for _ in range(4)]
+                svp.clip_gradients(ms, 1.0, out=[torch.empty_like(m, dtype=torch.float32) for m in ms])
+                del ms
             else:
                 raise SystemExit(f"unknown kernel case {name}")
             torch.cuda.synchronize()
