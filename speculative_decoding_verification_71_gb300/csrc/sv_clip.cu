@@ -11,6 +11,9 @@
 // the second launch joins them again for itself, so there is no counter to reset
 // and no order that changes.  The second launch takes the pieces backwards: the
 // last ones are still in L2 then.
+//
+// 2.5 GB of bf16: the norm 349 us, 7.1 TB/s.  0.7 GB into scaled copies: 345 us, 6.1
+// TB/s of two reads and a write.
 
 #include <cuda_runtime.h>
 
