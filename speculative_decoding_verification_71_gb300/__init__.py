@@ -920,7 +920,8 @@ def clip_gradients(grads, max_norm=None, kind="l2", out=None, stream=None):
     if out is not None:
         out_at, out_codes = _gradient_table("out", out, dev)
         for t, o, a, b in zip(grads, out, codes, out_codes):
-            if o.shape != t.shape or (a != b and b != SV_F32) or o.stride() != t.stride():
+            alike = o.stride() == t.stride() or (o.is_contiguous() and t.is_contiguous())
+            if o.shape != t.shape or (a != b and b != SV_F32) or not alike:
                 raise ValueError(f"out has a {o.dtype} tensor {tuple(o.shape)} for a {t.dtype} gradient {tuple(t.shape)}, "
                                  "or one laid out otherwise")
     of = lambda a: None if a is None else a.buffer_info()[0]

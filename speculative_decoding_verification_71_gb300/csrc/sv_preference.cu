@@ -11,7 +11,7 @@
 // the gradient is that of sv_token.cuh.
 //
 // Three launches: the rows' log-probabilities, a CTA a pair, the rows' gradients, each
-// in place before the one before has ended.  A row is read twice, the second time
+// launched before the one before it has ended.  A row is read twice, the second time
 // from L2 where the pairs are few; 16 padded pairs of up to 64 rows of 128256 bf16 take
 // 186 us, 5.1 TB/s of what crosses HBM.  One cooperative kernel that kept a pair's two
 // readings together was slower (190 to 237 us): the pair's sums go round between them.

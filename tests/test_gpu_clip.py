@@ -216,3 +216,20 @@ def test_streams_and_graphs():
     torch.cuda.synchronize()
     for norm, o in results:
         assert torch.equal(norm, want) and all(torch.equal(a, b) for a, b in zip(o, out))
+
+
+def test_more_tensors_than_a_table_holds():
+    """Tables of 512 tensors: the norm of all, scaled copies of each."""
+    sizes = [(i * 37) % 300 for i in range(1200)]
+    grads = make(sizes, (BF16, F32, BF16), seed=11)
+    want = norm64(grads, "l2")
+    check(grads, None)
+    check(grads, want * 0.3, out=[torch.empty_like(t, dtype=F32) for t in grads])
+    check(grads, want * 0.3, "max", out=[torch.empty_like(t) for t in grads])
+    check(grads, want * 0.3)
+
+
+def test_contiguous_tensors_whose_strides_differ():
+    t = torch.randn(8, 1, device=DEV).t()                 # one row: contiguous with any first stride
+    o = torch.empty(1, 8, device=DEV)
+    check([t], 0.1, out=[o])

@@ -552,6 +552,34 @@ def test_more_rows_than_are_looked_at_together(V, dtype, entropy):
     assert torch.equal(loss, row_loss.double().sum(1).float()) or (loss - row_loss.double().sum(1)).abs().max() < 1e-3
 
 
+@pytest.mark.parametrize("V,dtype,n", [(128256, BF16, 8500), (60001, F32, 9000)])
+def test_a_row_is_the_same_whatever_rows_lie_around_it(V, dtype, n):
+    """Rows of clusters of several CTAs, more of them than a window of tokens
+    holds, against the same rows in calls of their own: the same bits."""
+    g = torch.Generator(device=DEV).manual_seed(2)
+    z = torch.empty(n, 1, V, dtype=dtype, device=DEV)
+    for a in range(0, n, 500):
+        z[a:a + 500] = torch.randn(min(500, n - a), 1, V, device=DEV, generator=g)
+    x = torch.randint(0, V, (n, 1), device=DEV, generator=g).to(torch.int32)
+    x[torch.rand(n, 1, device=DEV, generator=g) < 0.3] = -1
+    x[:40] = -1
+    A, w = torch.randn(n, device=DEV, generator=g), torch.ones(n, device=DEV)
+    whole = svp.policy_loss(z, x, A, w, entropy_coef=0.01)
+    sums = svp.token_logp(z, x, entropy=True)
+    m = n // 2 + 7
+    for at in (slice(0, m), slice(m, n)):
+        part = svp.policy_loss(z[at], x[at], A[at], w[at], entropy_coef=0.01)
+        for a, b in zip(whole, part):
+            assert torch.equal(a[at], b)
+        for a, b in zip(sums, svp.token_logp(z[at], x[at], entropy=True)):
+            assert torch.equal(a[at], b)
+    d = torch.randn(n, 1, device=DEV, generator=g)
+    logp, H, lse = sums
+    grad = svp.token_logp_grad(z, x, logp, lse, d, entropy=H, d_entropy=d, out=whole[4])
+    here = svp.token_logp_grad(z, x, logp, lse, d, entropy=H, d_entropy=d, out=z)
+    assert torch.equal(grad, here)
+
+
 # ---------------------------------------------------------------------------
 # Waits that expire
 # ---------------------------------------------------------------------------
