@@ -45,7 +45,7 @@ struct RowParams {
   const unsigned char* logits; // [rows, V]
   const int* tokens;           // [rows]
   float *logp, *entropy, *lse; // [rows]; entropy and lse or null
-  float* logp_rest;            // [rows]: what the rounding of logp left, or null
+  float4* kept;                // [rows]: base, 1 / Z, 1 - p(x), what logp's rounding left (tok_kept), or null
   float* row_loss;             // [rows]: a policy's loss; null for the log-probabilities alone
   unsigned char* grad;         // [rows, V] or null
   int t_len, V;
@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(kShThreads, kShPerSm) token_short_kernel(const
         P.logp[r] = 0.f;
         if (P.entropy) P.entropy[r] = 0.f;
         if (P.lse) P.lse[r] = -INFINITY;
-        if (P.logp_rest) P.logp_rest[r] = 0.f;
+        if (P.kept) P.kept[r] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (P.row_loss) P.row_loss[r] = 0.f;
       }
       if (GRAD) zero_row<ELT>(grad, P.V, tid, G * 32);
@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(kShThreads, kShPerSm) token_short_kernel(const
       P.logp[r] = R.logp;
       if (ENT && P.entropy) P.entropy[r] = R.entropy();
       if (P.lse) P.lse[r] = R.lse(P.inv_T);
-      if (P.logp_rest) P.logp_rest[r] = R.logp_rest;
+      if (P.kept) P.kept[r] = tok_kept(R);
       if (P.row_loss) P.row_loss[r] = loss;
     }
     if (GRAD) {
@@ -440,7 +440,7 @@ __global__ void __launch_bounds__(Rg<GRAD>::kThreads, Rg<GRAD>::kPerSm)
             P.logp[r] = 0.f;
             if (P.entropy) P.entropy[r] = 0.f;
             if (P.lse) P.lse[r] = -INFINITY;
-            if (P.logp_rest) P.logp_rest[r] = 0.f;
+            if (P.kept) P.kept[r] = make_float4(0.f, 0.f, 0.f, 0.f);
             if (P.row_loss) P.row_loss[r] = 0.f;
           }
         }
@@ -532,7 +532,7 @@ __global__ void __launch_bounds__(Rg<GRAD>::kThreads, Rg<GRAD>::kPerSm)
           P.logp[r] = row.logp;
           if (ENT && P.entropy) P.entropy[r] = row.entropy();
           if (P.lse) P.lse[r] = row.lse(P.inv_T);
-          if (P.logp_rest) P.logp_rest[r] = row.logp_rest;
+          if (P.kept) P.kept[r] = tok_kept(row);
           if (P.row_loss) P.row_loss[r] = loss;
         }
         x = x_next;
@@ -705,15 +705,17 @@ __global__ void __launch_bounds__(Rg<GRAD>::kThreads, Rg<GRAD>::kPerSm)
 // at once; four CTAs an SM hide each other's chain of two trips to memory (the
 // row's numbers, then its token's logit).  In place the token's logit may be
 // overwritten by another piece's CTA, so there the row's CTAs are a cluster, which
-// goes on when all of them have it.  4096 rows of 151936 bf16: 387 us, 6.4 TB/s.
+// goes on when all of them have it (what the preference loss keeps of a row has no
+// need of that logit).  4096 rows of 151936 bf16: 387 us, 6.4 TB/s.
 struct GradParams {
   const unsigned char* logits;
   const int* tokens;
   const float *logp, *lse, *entropy, *d_logp, *d_entropy;   // [rows]; the entropies or null
+  const float4* kept;          // [rows]: in place of logp and lse, or null
   unsigned char* grad;
   int V, same_shift;
   int d_rows;                  // rows that share a d_logp
-  int in_place;
+  int in_place;                // and the token's logit is read
   float c2, inv_T;
 };
 constexpr int kGrThreads = 256, kGrPerThread = 8, kGrVecs = kGrThreads * kGrPerThread;
@@ -734,11 +736,12 @@ __global__ void __launch_bounds__(kGrThreads, 4) token_grad_kernel(const __grid_
   grid_dependency_wait();      // (the rows' numbers may be a kernel's before this one; the logits and tokens are not)
   TokGrad G;
   G.none();
-  if (x >= 0) {
+  if (x >= 0 && P.kept) {
+    G = tok_grad_kept(P.kept[r], P.d_logp[static_cast<unsigned>(r) / static_cast<unsigned>(P.d_rows)], P.inv_T);
+  } else if (x >= 0) {
     const uint32_t zx = load_bits<ELT>(row, min(x, P.V - 1));
     G = tok_grad_from(value_of<ELT>(zx), x < P.V ? P.logp[r] : NAN, P.lse[r], ENT ? P.entropy[r] : 0.f,
-                      P.d_logp[P.d_rows > 1 ? static_cast<unsigned>(r) / static_cast<unsigned>(P.d_rows) : r],
-                      ENT ? P.d_entropy[r] : 0.f, P.inv_T);
+                      P.d_logp[r], ENT ? P.d_entropy[r] : 0.f, P.inv_T);
   }
   if (P.in_place) {
     if (parts > 1) cluster_sync();
@@ -923,24 +926,33 @@ bool rows_ok(int n_seq, int t_len, int V, sv_dtype dtype, const void* logits, co
 }
 
 cudaError_t launch_token_logp(int rows, int V, sv_dtype dtype, const void* logits, const int32_t* tokens,
-                              float temperature, float* logp, float* entropy, float* lse, float* logp_rest, bool followed, cudaStream_t s) {
+                              float temperature, float* logp, float* entropy, float* lse, float4* kept, bool followed, cudaStream_t s) {
   RowParams p = row_params(1, V, logits, tokens, temperature, nullptr);
   p.logp = logp;
   p.entropy = entropy;
   p.lse = lse;
-  p.logp_rest = logp_rest;
+  p.kept = kept;
   p.followed = followed;
   return dtype == SV_BF16 ? launch_rows<2>(p, rows, entropy != nullptr, s) : launch_rows<4>(p, rows, entropy != nullptr, s);
 }
 
 cudaError_t launch_token_grad(int rows, int V, sv_dtype dtype, const void* logits, const int32_t* tokens,
-                              const float* logp, const float* lse, const float* entropy, const float* d_logp, int d_rows,
-                              const float* d_entropy, float temperature, void* grad, bool dependent, cudaStream_t s) {
+                              const float* logp, const float* lse, const float* entropy, const float* d_logp,
+                              const float* d_entropy, float temperature, void* grad, cudaStream_t s) {
   const RowParams q = row_params(1, V, logits, tokens, temperature, grad);
-  const GradParams p{q.logits, tokens, logp, lse, entropy, d_logp, d_entropy, q.grad, V, q.same_shift, d_rows,
+  const GradParams p{q.logits, tokens, logp, lse, entropy, d_logp, d_entropy, nullptr, q.grad, V, q.same_shift, 1,
                      grad == logits, q.c2, q.inv_T};
-  if (dtype == SV_BF16) return entropy ? launch_grad<2, true>(p, rows, dependent, s) : launch_grad<2, false>(p, rows, dependent, s);
-  return entropy ? launch_grad<4, true>(p, rows, dependent, s) : launch_grad<4, false>(p, rows, dependent, s);
+  if (dtype == SV_BF16) return entropy ? launch_grad<2, true>(p, rows, false, s) : launch_grad<2, false>(p, rows, false, s);
+  return entropy ? launch_grad<4, true>(p, rows, false, s) : launch_grad<4, false>(p, rows, false, s);
+}
+
+cudaError_t launch_kept_grad(int rows, int V, sv_dtype dtype, const void* logits, const int32_t* tokens,
+                             const float4* kept, const float* d_logp, int d_rows, float temperature, void* grad,
+                             cudaStream_t s) {
+  const RowParams q = row_params(1, V, logits, tokens, temperature, grad);
+  const GradParams p{q.logits, tokens, nullptr, nullptr, nullptr, d_logp, nullptr, kept, q.grad, V, q.same_shift, d_rows,
+                     0, q.c2, q.inv_T};
+  return dtype == SV_BF16 ? launch_grad<2, false>(p, rows, true, s) : launch_grad<4, false>(p, rows, true, s);
 }
 
 }  // namespace sv
@@ -965,8 +977,8 @@ extern "C" sv_status sv_token_logp_grad(int n_seq, int t_len, int V, sv_dtype dt
     return SV_ERR_INVALID_ARG;
   if (!entropy != !d_entropy) return SV_ERR_INVALID_ARG;
   NvtxRange range("sv_token_logp_grad");
-  return launch_token_grad(n_seq * t_len, V, dtype, logits, tokens, logp, lse, entropy, d_logp, 1, d_entropy, temperature,
-                           grad, false, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+  return launch_token_grad(n_seq * t_len, V, dtype, logits, tokens, logp, lse, entropy, d_logp, d_entropy, temperature,
+                           grad, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? SV_OK : SV_ERR_CUDA;
 }
 
 extern "C" sv_status sv_policy_loss(int n_seq, int t_len, int V, sv_dtype dtype, const void* logits,

@@ -31,7 +31,8 @@ namespace {
 
 struct PairParams {
   const int* tokens;           // [2 n_pair, t_len]
-  const float *logp, *rest;    // [2 n_pair, t_len]: the log-probabilities, and what their rounding left
+  const float* logp;           // [2 n_pair, t_len]
+  const float4* kept;          // [2 n_pair, t_len]: .w is what the rounding of logp left
   const float* ref;            // [2 n_pair]
   const float* weights;        // [n_pair]
   float *margin, *loss;        // [n_pair]
@@ -59,7 +60,7 @@ __global__ void __launch_bounds__(kPairThreads) pair_kernel(const __grid_constan
     double s = 0.0;
     int n = 0;
     for (int t = tid; t < P.t_len; t += kPairThreads) {
-      s += static_cast<double>(P.logp[at + t]) + static_cast<double>(P.rest[at + t]);
+      s += static_cast<double>(P.logp[at + t]) + static_cast<double>(P.kept[at + t].w);
       n += P.tokens[at + t] >= 0;
     }
     s = warp_sum(s);
@@ -109,8 +110,8 @@ __global__ void __launch_bounds__(kPairThreads) pair_kernel(const __grid_constan
 }  // namespace sv
 
 extern "C" size_t sv_preference_work(int n_pair, int t_len) {
-  // each row's log-sum-exp and what the rounding of its log-probability left, each sequence's derivative
-  return n_pair < 1 || t_len < 1 ? 0 : static_cast<size_t>(n_pair) * 2 * (2 * static_cast<size_t>(t_len) + 1);
+  // four floats of each row and each sequence's derivative
+  return n_pair < 1 || t_len < 1 ? 0 : static_cast<size_t>(n_pair) * 2 * (4 * static_cast<size_t>(t_len) + 1);
 }
 
 extern "C" sv_status sv_preference_loss(int n_pair, int t_len, int V, sv_dtype dtype, const void* logits,
@@ -131,10 +132,11 @@ extern "C" sv_status sv_preference_loss(int n_pair, int t_len, int V, sv_dtype d
   NvtxRange range("sv_preference_loss");
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const int rows = n_seq * t_len;
-  float *lse = work, *rest = work + rows, *d_logp = grad ? work + 2 * static_cast<size_t>(rows) : nullptr;
-  if (launch_token_logp(rows, V, dtype, logits, tokens, temperature, logp, nullptr, lse, rest, true, s) != cudaSuccess)
+  float4* kept = reinterpret_cast<float4*>(work);
+  float* d_logp = grad ? work + 4 * static_cast<size_t>(rows) : nullptr;
+  if (launch_token_logp(rows, V, dtype, logits, tokens, temperature, logp, nullptr, nullptr, kept, true, s) != cudaSuccess)
     return SV_ERR_CUDA;
-  const PairParams p{tokens, logp, rest, ref_logp, weights, margin, loss, d_logp, t_len, kind, average, beta, smoothing};
+  const PairParams p{tokens, logp, kept, ref_logp, weights, margin, loss, d_logp, t_len, kind, average, beta, smoothing};
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
@@ -145,8 +147,7 @@ extern "C" sv_status sv_preference_loss(int n_pair, int t_len, int V, sv_dtype d
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   if (cudaLaunchKernelEx(&cfg, pair_kernel, p) != cudaSuccess) return SV_ERR_CUDA;
-  if (grad && launch_token_grad(rows, V, dtype, logits, tokens, logp, lse, nullptr, d_logp, t_len, nullptr, temperature,
-                                grad, true, s) != cudaSuccess)
+  if (grad && launch_kept_grad(rows, V, dtype, logits, tokens, kept, d_logp, t_len, temperature, grad, s) != cudaSuccess)
     return SV_ERR_CUDA;
   return SV_OK;
 }

@@ -240,6 +240,21 @@ __device__ __forceinline__ TokGrad tok_grad(const TokRow& R, float g, float h, f
   return G;
 }
 
+// What a gradient of log p(x) takes of a row later, and what the rounding of log
+// p(x) left: no value of it is rounded at the level of the logits.
+__device__ __forceinline__ float4 tok_kept(const TokRow& R) {
+  return make_float4(R.M, R.valid ? R.rZ : NAN, R.rest, R.logp_rest);
+}
+__device__ __forceinline__ TokGrad tok_grad_kept(const float4& row, float g, float inv_T) {
+  TokGrad G;
+  G.base = row.x;
+  G.k = G.gamma = 0.f;
+  G.alpha = -g * __fmul_rn(inv_T, row.y);
+  G.at_token = __fmul_rn(inv_T, g * row.z);
+  tok_check(G, row.y == row.y);
+  return G;
+}
+
 // The same from what token_logp gave for the row.
 __device__ __forceinline__ TokGrad tok_grad_from(float zx, float logp, float lse, float H, float g, float h, float inv_T) {
   TokGrad G;
