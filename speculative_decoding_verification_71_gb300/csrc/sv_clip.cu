@@ -6,8 +6,8 @@
 //
 // Bound by memory: one read for the norm, one more and a write for the scaling.
 // Every tensor is cut into pieces of 32 KB at most on 16-byte boundaries of its
-// memory, and piece b + i 608 of them all goes to CTA b (four an SM), eight
-// 16-byte loads a thread in flight.  The CTAs' sums go to `work` and every CTA of
+// memory, and piece b + i 608 of them all goes to CTA b (four an SM, fewer for few
+// pieces), eight 16-byte loads a thread in flight.  The CTAs' sums go to `work` and every CTA of
 // the second launch joins them again for itself, so there is no counter to reset
 // and no order that changes.  The second launch takes the pieces backwards: the
 // last ones are still in L2 then.
@@ -190,7 +190,7 @@ __global__ void __launch_bounds__(kClipThreads, 4) clip_norm_kernel(const __grid
   ClipPart part{0.0, 0.f, 0.f, 0u};
   const int pieces = T.first[T.n];
   if (static_cast<int>(blockIdx.x) < pieces)
-    for (int piece = blockIdx.x, k = clip_find(T, piece); piece < pieces; piece += kClipGrid) {
+    for (int piece = blockIdx.x, k = clip_find(T, piece); piece < pieces; piece += gridDim.x) {
       while (piece >= T.first[k + 1]) ++k;
       if (T.wide[k] & 1) clip_add<4>(T, k, piece, part);
       else clip_add<2>(T, k, piece, part);
@@ -205,9 +205,9 @@ __global__ void __launch_bounds__(kClipThreads, 4) clip_norm_kernel(const __grid
 }
 
 // The norm, the same in every CTA.
-__device__ __forceinline__ float clip_total(const double* work, int kind) {
+__device__ __forceinline__ float clip_total(const double* work, int ctas, int kind) {
   ClipPart part{0.0, 0.f, 0.f, 0u};
-  for (int i = threadIdx.x; i < kClipGrid; i += kClipThreads) {
+  for (int i = threadIdx.x; i < ctas; i += kClipThreads) {
     const double v = __ldcg(work + i);
     if (kind == SV_NORM_L2) part.s += v;
     else part.top = max(part.top, __float_as_uint(static_cast<float>(v)) & 0x7fffffffu);
@@ -216,9 +216,9 @@ __device__ __forceinline__ float clip_total(const double* work, int kind) {
   return kind == SV_NORM_L2 ? static_cast<float>(sqrt(part.s)) : __uint_as_float(part.top);
 }
 
-__global__ void __launch_bounds__(kClipThreads) clip_total_kernel(const double* work, int kind, float* norm) {
+__global__ void __launch_bounds__(kClipThreads) clip_total_kernel(const double* work, int ctas, int kind, float* norm) {
   grid_dependency_wait();
-  const float v = clip_total(work, kind);
+  const float v = clip_total(work, ctas, kind);
   if (threadIdx.x == 0) *norm = v;
 }
 
@@ -294,7 +294,7 @@ __global__ void __launch_bounds__(kClipThreads, 4) clip_scale_kernel(const __gri
     clip_fetch(T, k, piece, w);
   }
   grid_dependency_wait();
-  const float total = clip_total(work, T.kind);
+  const float total = clip_total(work, static_cast<int>(gridDim.x), T.kind);
   if (blockIdx.x == 0 && threadIdx.x == 0) *norm = total;
   const float scale = total < INFINITY ? fminf(__fdiv_rn(max_norm, __fadd_rn(total, 1e-6f)), 1.f) : 1.f;
   if (piece < 0 || (in_place && scale == 1.f)) return;
@@ -304,7 +304,7 @@ __global__ void __launch_bounds__(kClipThreads, 4) clip_scale_kernel(const __gri
   }
   while (true) {
     clip_scale(T, k, piece, w, scale);
-    piece -= kClipGrid;
+    piece -= static_cast<int>(gridDim.x);
     if (piece < 0) break;
     while (piece < T.first[k]) --k;
     clip_fetch(T, k, piece, w);
@@ -349,14 +349,15 @@ long long clip_pieces(const ClipCall& c, int i, int per) {
 
 // How many vectors of a piece each thread takes: what makes the CTA with the
 // most pieces move the least, a piece's start counted as half a vector (48 MB of
-// bf16, 3 pieces of 8 or 4 of 5: 12.2 and 11.8 us for the norm).
+// bf16, 3 pieces of 8 or 4 of 5: 12.2 and 11.8 us for the norm), and 64 CTAs as a
+// vector (0.6 MB in five tensors: 6.4 us with a CTA a piece, 12.8 with 608).
 int clip_per(const ClipCall& c, int first, int tensors) {
   int best = kClipPerThread;
   long long least = 0;
   for (int per = kClipPerThread; per >= 1; --per) {
     long long pieces = 0;
     for (int i = first; i < c.n && i < first + tensors; ++i) pieces += clip_pieces(c, i, per);
-    const long long cost = (pieces + kClipGrid - 1) / kClipGrid * (2 * per + 1);
+    const long long cost = (pieces + kClipGrid - 1) / kClipGrid * (2 * per + 1) + std::min<long long>(pieces, kClipGrid) / 32;
     if (per == kClipPerThread || cost < least) best = per, least = cost;
     if (pieces > 16LL * kClipGrid) break;     // nothing to win
   }
@@ -367,6 +368,7 @@ template <int N>
 cudaError_t clip_run_call(const ClipCall& c) {
   const bool scales = c.outs || c.max_norm < INFINITY;
   static thread_local ClipTable<N> t;
+  int ctas = kClipGrid;
   for (int pass = 0; pass < (scales ? 2 : 1); ++pass)
     for (int first = 0; first < c.n || first == 0; first += N) {
       t.n = 0;
@@ -388,18 +390,19 @@ cudaError_t clip_run_call(const ClipCall& c) {
         t.wide[0] = 0;
         t.first[1] = 0;
       }
+      if (c.n <= N) ctas = std::max(1, std::min(kClipGrid, t.first[t.n]));
       cudaError_t e;
       if (pass == 0) {
-        clip_norm_kernel<N><<<kClipGrid, kClipThreads, 0, c.stream>>>(t, c.work, first == 0);
+        clip_norm_kernel<N><<<ctas, kClipThreads, 0, c.stream>>>(t, c.work, first == 0);
         e = cudaGetLastError();
       } else {
-        e = clip_launch(clip_scale_kernel<N>, kClipGrid, c.stream, t, static_cast<const double*>(c.work), c.norm,
+        e = clip_launch(clip_scale_kernel<N>, ctas, c.stream, t, static_cast<const double*>(c.work), c.norm,
                         c.max_norm, c.outs == nullptr ? 1 : 0);
       }
       if (e != cudaSuccess) return e;
     }
   if (scales) return cudaSuccess;
-  return clip_launch(clip_total_kernel, 1, c.stream, static_cast<const double*>(c.work), c.kind, c.norm);
+  return clip_launch(clip_total_kernel, 1, c.stream, static_cast<const double*>(c.work), ctas, c.kind, c.norm);
 }
 
 // Memory that a call reads or writes.
