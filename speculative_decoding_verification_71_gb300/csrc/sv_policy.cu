@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(kShThreads, kShPerSm) token_short_kernel(const
   const int stride = static_cast<int>(gridDim.x) * kGroups;
   int par = 0, r = static_cast<int>(blockIdx.x) * kGroups + group;
   int x_next = r < rows ? P.tokens[r] : -1;
-  for (; r < rows; r += stride, par ^= 1) {
+  for (; r < rows; r += stride) {
     const int x_row = x_next;
     x_next = r + stride < rows ? P.tokens[r + stride] : -1;
     const unsigned long long at_row = static_cast<unsigned long long>(r) * (static_cast<unsigned>(P.V) * ELT);
@@ -188,6 +188,7 @@ __global__ void __launch_bounds__(kShThreads, kShPerSm) token_short_kernel(const
       if (lane == 0) parts[par][warp] = part;
       named_barrier_sync(1 + group, G * 32);
       part = tok_join<ENT>(lane < G ? parts[par][group * G + lane] : tok_none(), P.c2);
+      par ^= 1;   // only here: the next row's barrier lies between these reads and the writes to the same place
     }
     const TokRow R = tok_row<ENT>(part, zx, P.inv_T);
     float loss = 0.f, slope = 0.f;
