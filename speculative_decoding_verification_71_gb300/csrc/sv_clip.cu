@@ -35,8 +35,12 @@ constexpr int kClipGrid = SV_CLIP_WORK;    // CTAs, and their parts of the sum
 constexpr int kClipFew = 64, kClipMany = 512;                 // tensors of a launch: its table is a kernel argument
 
 // A sum of squares of 64 values in float32 outside these has lost or may lose
-// some of them, and is taken again in 64 bits.
-constexpr float kClipLow = 0x1p-100f, kClipHigh = 0x1p120f;
+// some of them, and is taken again in 64 bits.  A thread joins the sums of all its
+// pieces of a launch in float32: fewer than 2^21 of them (2^30 pieces over
+// SV_CLIP_WORK CTAs), so below 2^117.
+constexpr float kClipLow = 0x1p-100f, kClipHigh = 0x1p96f;
+constexpr long long kClipMaxPieces = 1LL << 30;
+static_assert(kClipMaxPieces / SV_CLIP_WORK < 1 << 21, "a thread's pieces");
 
 template <int N>
 struct ClipTable {
@@ -457,7 +461,7 @@ extern "C" sv_status sv_clip_gradients(int n, const void* const* grads, const lo
     range_of(grads[i], sizes[i], dtypes[i] == SV_F32 ? 4 : 2, outs ? same : scales);
     if (outs && !same) range_of(outs[i], sizes[i], out_dtypes[i] == SV_F32 ? 4 : 2, true);
   }
-  ok = ok && pieces < (1LL << 30) && !clip_overlaps(ranges, used);
+  ok = ok && pieces < kClipMaxPieces && !clip_overlaps(ranges, used);
   delete[] ranges;
   if (!ok) return SV_ERR_INVALID_ARG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
