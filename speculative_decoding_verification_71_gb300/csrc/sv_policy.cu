@@ -83,9 +83,15 @@ template <bool ENT>
 __device__ __forceinline__ void policy_row(const PolicyArgs& P, const PolicyRow& row, const TokRow& R, float& loss,
                                            float& slope) {
   const float A = row.A;
-  const float r = P.old_logp ? expf(__fadd_rn(__fsub_rn(R.logp, row.old_logp), R.logp_rest)) : 1.f;
+  const float up_old = P.old_logp ? __fadd_rn(__fsub_rn(R.logp, row.old_logp), R.logp_rest) : 0.f;
+  const float r = P.old_logp ? expf(up_old) : 1.f;
   const float low = 1.f - P.low, high = 1.f + P.high;
-  const float gained = r * A, held = (r < low ? low : r > high ? high : r) * A;
+  float gained = r * A;
+  if (r == INFINITY && up_old < INFINITY) {   // past the range where the product need not be
+    const float half = expf(0.5f * up_old);
+    gained = A == 0.f ? A : half * A * half;
+  }
+  const float held = (r < low ? low : r > high ? high : r) * A;
   float gain = gained <= held ? gained : held;
   slope = gained <= held ? -gained : 0.f;
   if (!(gained == gained)) gain = slope = NAN;
