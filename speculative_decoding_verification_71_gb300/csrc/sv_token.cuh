@@ -146,6 +146,26 @@ __device__ __forceinline__ TokPart tok_join(const TokPart& p, float c2) {
   return r;
 }
 
+// log(Z + Z_rest) as a float and what its rounding leaves, for Z >= 1 and Z_rest
+// within Z's rounding.  Of Z = 2^k f, f in [3/4, 3/2), log f is at most 0.41 and off
+// by a step of 2^-25 at most, and k log 2 is taken as two numbers, so a sum of many
+// logarithms does not gather their roundings (2^-22 each where Z is some thousands).
+// Near Z = 1 the logarithm keeps the digits of Z - 1, which Z_rest completes (what
+// Z_rest's square would add is below 2e-15): a nearly sure token's -log p.
+__device__ __forceinline__ float tok_log(float Z, float Z_rest, float rZ, float& rest) {
+  constexpr float kLn2Rest = static_cast<float>(0.69314718055994530942 - static_cast<double>(kLn2));
+  const int at = __float_as_int(Z) - 0x3f400000;      // 3/4's bits
+  const float k = static_cast<float>(at >> 23);
+  const float f = __int_as_float(__float_as_int(Z) - (at & static_cast<int>(0xff800000)));
+  const float hi = __fmul_rn(k, kLn2), lo = __fmaf_rn(k, kLn2Rest, __fmaf_rn(k, kLn2, -hi));
+  float y, e;
+  two_sum(hi, logf(f), y, e);
+  e = __fadd_rn(e, __fmaf_rn(Z_rest, rZ, lo));
+  const float whole = __fadd_rn(y, e);
+  rest = __fadd_rn(__fsub_rn(y, whole), e);
+  return whole;
+}
+
 // (z - m) / T for z <= m and what its roundings left, also where z - m passes the
 // range and the quotient does not.
 __device__ __forceinline__ float tok_below(float z, float m, float inv_T, float& rest) {
@@ -181,17 +201,21 @@ __device__ __forceinline__ TokRow tok_row(const TokPart& part, float zx, float i
   float e = expf(d);
   e = __fmaf_rn(e, d_rest, e);
   const float rest = top ? __fmul_rn(part.s, e) : part.s, ex = top ? 1.f : e;
-  R.Z = __fadd_rn(rest, ex);
+  float Z_rest, log_rest = 0.f;
+  two_sum(rest, ex, R.Z, Z_rest);
   R.rZ = __fdiv_rn(1.f, R.Z);
-  R.log_Z = top ? log1pf(rest) : logf(R.Z);
+  R.log_Z = tok_log(R.Z, Z_rest, R.rZ, log_rest);
   R.rest = __fmul_rn(rest, R.rZ);
   R.px = __fmul_rn(ex, R.rZ);
   float lp, lp_rest = 0.f;
-  if (top || !(d > -INFINITY)) {
-    lp = __fsub_rn(top ? 0.f : d, R.log_Z);
+  if (top) {
+    lp = __fsub_rn(0.f, R.log_Z);
+    lp_rest = -log_rest;
+  } else if (!(d > -INFINITY)) {
+    lp = d;
   } else {
     two_sum(d, -R.log_Z, lp, lp_rest);
-    lp_rest = __fadd_rn(lp_rest, d_rest);
+    lp_rest = __fadd_rn(lp_rest, __fsub_rn(d_rest, log_rest));
     const float whole = __fadd_rn(lp, lp_rest);
     lp_rest = __fadd_rn(__fsub_rn(lp, whole), lp_rest);
     lp = whole;
