@@ -52,6 +52,7 @@ struct RowParams {
   int same_shift;              // logits and grad lie alike: 16-byte stores
   int followed;                // by a kernel that waits for this one: it may take its place on an SM early
   float c2, inv_T;             // log2(e) / T, 1 / T
+  float inv_T_rest;            // what 1 / T's rounding left
   long long wait_limit_ns;     // of a wait for staged logits
   PolicyArgs policy;
 };
@@ -196,7 +197,7 @@ __global__ void __launch_bounds__(kShThreads, kShPerSm) token_short_kernel(const
       part = tok_join<ENT>(lane < G ? parts[par][group * G + lane] : tok_none(), P.c2);
       par ^= 1;   // only here: the next row's barrier lies between these reads and the writes to the same place
     }
-    const TokRow R = tok_row<ENT>(part, zx, P.inv_T);
+    const TokRow R = tok_row<ENT>(part, zx, TokTemp{P.inv_T, P.inv_T_rest});
     float loss = 0.f, slope = 0.f;
     if (P.row_loss) policy_row<ENT>(P.policy, mine, R, loss, slope);
     if (tid == 0) {
@@ -525,7 +526,7 @@ __global__ void __launch_bounds__(Rg<GRAD>::kThreads, Rg<GRAD>::kPerSm)
           part.s = NAN;
           if (lane == 0) atomicMin(&sh.failed, static_cast<int>(r));
         }
-        const TokRow row = tok_row<ENT>(part, zx, P.inv_T);
+        const TokRow row = tok_row<ENT>(part, zx, TokTemp{P.inv_T, P.inv_T_rest});
         float loss = 0.f, slope = 0.f;
         if (P.row_loss) policy_row<ENT>(P.policy, mine_row, row, loss, slope);
         if (GRAD) {
@@ -913,6 +914,7 @@ RowParams row_params(int t_len, int V, const void* logits, const int32_t* tokens
   p.same_shift = reinterpret_cast<uintptr_t>(logits) % 16 == reinterpret_cast<uintptr_t>(grad) % 16;
   p.c2 = static_cast<float>(1.4426950408889634 / static_cast<double>(temperature));
   p.inv_T = 1.f / temperature;
+  p.inv_T_rest = static_cast<float>(1.0 / static_cast<double>(temperature) - static_cast<double>(p.inv_T));
   p.wait_limit_ns = kd_wait_limit_ns();
   return p;
 }

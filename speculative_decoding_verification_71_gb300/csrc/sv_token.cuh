@@ -166,13 +166,20 @@ __device__ __forceinline__ float tok_log(float Z, float Z_rest, float rZ, float&
   return whole;
 }
 
+// 1 / T, and what its rounding left: a common factor of all that is divided by T,
+// which a sum over tokens would gather.
+struct TokTemp {
+  float inv, inv_rest;
+};
+
 // (z - m) / T for z <= m and what its roundings left, also where z - m passes the
 // range and the quotient does not.
-__device__ __forceinline__ float tok_below(float z, float m, float inv_T, float& rest) {
+__device__ __forceinline__ float tok_below(float z, float m, TokTemp T, float& rest) {
+  const float inv_T = T.inv;
   float d, e;
   two_sum(z, -m, d, e);
   const float q = __fmul_rn(d, inv_T);
-  rest = __fmaf_rn(e, inv_T, __fmaf_rn(d, inv_T, -q));
+  rest = __fmaf_rn(d, T.inv_rest, __fmaf_rn(e, inv_T, __fmaf_rn(d, inv_T, -q)));
   if (!(fabsf(rest) < 1.f)) rest = 0.f;    // (far below anything that counts)
   if (d > -INFINITY || !(z > -INFINITY)) return q;
   return __fsub_rn(__fmul_rn(z, inv_T), __fmul_rn(m, inv_T));
@@ -190,14 +197,14 @@ struct TokRow {
 };
 
 template <bool ENT>
-__device__ __forceinline__ TokRow tok_row(const TokPart& part, float zx, float inv_T) {
+__device__ __forceinline__ TokRow tok_row(const TokPart& part, float zx, TokTemp T) {
   TokRow R;
   const bool top = zx >= part.m;           // the token's logit is the base
   R.M = top ? zx : part.m;
   R.valid = part.s == part.s && zx == zx && R.M > -INFINITY && R.M < INFINITY;
   const float low = top ? part.m : zx;
   float d_rest = 0.f;
-  const float d = low > -INFINITY ? tok_below(low, R.M, inv_T, d_rest) : -INFINITY;
+  const float d = low > -INFINITY ? tok_below(low, R.M, T, d_rest) : -INFINITY;
   float e = expf(d);
   e = __fmaf_rn(e, d_rest, e);
   const float rest = top ? __fmul_rn(part.s, e) : part.s, ex = top ? 1.f : e;

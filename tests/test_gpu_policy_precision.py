@@ -39,7 +39,7 @@ def pair_of_alike_rows(V, k, low, dtype, n):
     return z, x
 
 
-@pytest.mark.parametrize("T", [1.0])
+@pytest.mark.parametrize("T", [1.0, 0.6, 1.3])
 @pytest.mark.parametrize("low", [0.0, -3.0, -40.0])
 @pytest.mark.parametrize("V,dtype", [(2900, F32), (6000, BF16), (40008, BF16), (21001, F32)])
 def test_a_margin_does_not_gather_roundings(V, dtype, low, T):
