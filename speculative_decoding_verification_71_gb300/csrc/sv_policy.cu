@@ -724,7 +724,7 @@ struct GradParams {
   int V, same_shift;
   int d_rows;                  // rows that share a d_logp
   int in_place;                // and the token's logit is read
-  float c2, inv_T;
+  float c2, inv_T, T;
 };
 constexpr int kGrThreads = 256, kGrPerThread = 8, kGrVecs = kGrThreads * kGrPerThread;
 constexpr int kGrMaxParts = 8;
@@ -749,7 +749,7 @@ __global__ void __launch_bounds__(kGrThreads, 4) token_grad_kernel(const __grid_
   } else if (x >= 0) {
     const uint32_t zx = load_bits<ELT>(row, min(x, P.V - 1));
     G = tok_grad_from(value_of<ELT>(zx), x < P.V ? P.logp[r] : NAN, P.lse[r], ENT ? P.entropy[r] : 0.f,
-                      P.d_logp[r], ENT ? P.d_entropy[r] : 0.f, P.inv_T);
+                      P.d_logp[r], ENT ? P.d_entropy[r] : 0.f, P.T, P.inv_T, P.c2);
   }
   if (P.in_place) {
     if (parts > 1) cluster_sync();
@@ -950,7 +950,7 @@ cudaError_t launch_token_grad(int rows, int V, sv_dtype dtype, const void* logit
                               const float* d_entropy, float temperature, void* grad, cudaStream_t s) {
   const RowParams q = row_params(1, V, logits, tokens, temperature, grad);
   const GradParams p{q.logits, tokens, logp, lse, entropy, d_logp, d_entropy, nullptr, q.grad, V, q.same_shift, 1,
-                     grad == logits, q.c2, q.inv_T};
+                     grad == logits, q.c2, q.inv_T, temperature};
   if (dtype == SV_BF16) return entropy ? launch_grad<2, true>(p, rows, false, s) : launch_grad<2, false>(p, rows, false, s);
   return entropy ? launch_grad<4, true>(p, rows, false, s) : launch_grad<4, false>(p, rows, false, s);
 }
@@ -960,7 +960,7 @@ cudaError_t launch_kept_grad(int rows, int V, sv_dtype dtype, const void* logits
                              cudaStream_t s) {
   const RowParams q = row_params(1, V, logits, tokens, temperature, grad);
   const GradParams p{q.logits, tokens, nullptr, nullptr, nullptr, d_logp, nullptr, kept, q.grad, V, q.same_shift, d_rows,
-                     0, q.c2, q.inv_T};
+                     0, q.c2, q.inv_T, temperature};
   return dtype == SV_BF16 ? launch_grad<2, false>(p, rows, true, s) : launch_grad<4, false>(p, rows, true, s);
 }
 

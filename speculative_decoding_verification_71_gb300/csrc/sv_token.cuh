@@ -286,14 +286,24 @@ __device__ __forceinline__ TokGrad tok_grad_kept(const float4& row, float g, flo
   return G;
 }
 
-// The same from what token_logp gave for the row.
-__device__ __forceinline__ TokGrad tok_grad_from(float zx, float logp, float lse, float H, float g, float h, float inv_T) {
+// The same from what token_logp gave for the row.  p(v) = e^((z(v) - b) / T) with b
+// = z(x) - T log p(x), whose difference from the logits that count keeps its digits
+// at any level, or b = T lse where the token is far below them.  b is a float and
+// what that leaves, which k takes: an exponent near 0 has no rounding but those of
+// log p(x) or lse themselves.
+__device__ __forceinline__ TokGrad tok_grad_from(float zx, float logp, float lse, float H, float g, float h, float T,
+                                                 float inv_T, float c2) {
   TokGrad G;
-  // about the token's own logit, whose difference from the others keeps its
-  // digits at any level; about lse where the token is far below them
   const bool near_token = logp > -32.f;
-  G.base = near_token ? zx : 0.f;
-  G.k = __fmul_rn(near_token ? logp : -lse, kLog2e);
+  const float from = near_token ? zx : 0.f, y = near_token ? -logp : lse;
+  const float up = __fmul_rn(y, T);
+  float rest;
+  two_sum(from, up, G.base, rest);
+  G.k = -__fmul_rn(__fadd_rn(rest, __fmaf_rn(y, T, -up)), c2);
+  if (!(fabsf(G.base) < INFINITY)) {      // T times it passes the range
+    G.base = from;
+    G.k = -__fmul_rn(y, kLog2e);
+  }
   G.alpha = __fmul_rn(inv_T, __fmaf_rn(-h, H, -g));
   G.gamma = -h * kLn2 * inv_T;
   const float px = expf(logp);

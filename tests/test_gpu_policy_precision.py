@@ -60,6 +60,57 @@ def test_a_margin_does_not_gather_roundings(V, dtype, low, T):
         assert abs(margin.item() - want) <= n * 2.0 ** -25 * 1.01 + HALF * abs(want), (k, margin.item(), want)
 
 
+@pytest.mark.parametrize("T", [1.0, 0.6, 1.3])
+@pytest.mark.parametrize("base,low", [(0.0, -20.0), (0.0, -29.0), (3.3, -14.0), (50.0, 15.0), (-7.0, -60.0)])
+@pytest.mark.parametrize("V", [64, 9001])
+def test_gradients_from_kept_numbers(V, base, low, T):
+    """Rows of one likely token and their own, unlikely one: the likely token's
+    probability is e^((z - z(x)) / T + log p), or e^(z / T - lse) for log p <= -32,
+    with log p and lse as they were given.  That exponent is near 0, so it has no
+    rounding of its own: 2^-22 of ex2.approx and four steps of products remain."""
+    n, T = 400, level(T)
+    g = torch.Generator().manual_seed(int(V + 10 * base + low))
+    z = torch.full((n, 1, V), -INF)
+    z[:, 0, 5] = base + torch.rand(n, generator=g)
+    z[:, 0, 40] = low + torch.rand(n, generator=g)
+    x = torch.full((n, 1), 40, dtype=torch.int32)
+    z64 = z.double().numpy()[:, 0, [5, 40]] / T
+    lse = np.logaddexp(z64[:, 0], z64[:, 1])
+    logp32, lse32 = (z64[:, 1] - lse).astype(np.float32), lse.astype(np.float32)
+    to = lambda a: torch.from_numpy(a)[:, None].to(DEV)
+    d = torch.full((n, 1), -1.0, device=DEV)
+    got = svp.token_logp_grad(z.to(DEV), x.to(DEV), to(logp32), to(lse32), d, temperature=T)[:, 0, 5].double().cpu().numpy()
+    near = logp32 > -32
+    want = np.exp(np.where(near, z64[:, 0] - z64[:, 1] + logp32.astype(np.float64), z64[:, 0] - lse32.astype(np.float64))) / T
+    off = np.abs(got / want - 1)
+    assert off.max() <= 2.0 ** -22 + 4 * HALF, (off.max(), np.median(off))
+
+
+@pytest.mark.parametrize("T", [1.0, 0.6])
+def test_gradients_of_entropies_from_kept_numbers(T):
+    """The same rows with a derivative in the entropy: p (log p + H) at the likely
+    token, whose log p is known to an absolute 2^-24 of the numbers it comes of."""
+    n, T, V = 200, level(T), 64
+    g = torch.Generator().manual_seed(3)
+    z = torch.full((n, 1, V), -INF)
+    z[:, 0, 5] = torch.rand(n, generator=g)
+    z[:, 0, 9] = torch.rand(n, generator=g) - 1
+    z[:, 0, 40] = torch.rand(n, generator=g) - 12
+    x = torch.full((n, 1), 40, dtype=torch.int32)
+    lp = torch.log_softmax(z[:, 0, [5, 9, 40]].double() / T, 1)
+    lse = torch.logsumexp(z[:, 0].double() / T, 1)
+    H = -(lp.exp() * lp).sum(1)
+    f = lambda t: t.float()[:, None].to(DEV)
+    one = torch.ones(n, 1, device=DEV)
+    got = svp.token_logp_grad(z.to(DEV), x.to(DEV), f(lp[:, 2]), f(lse), 0 * one, entropy=f(H), d_entropy=one,
+                              temperature=T)[:, 0, [5, 9, 40]].double().cpu()
+    want = -lp.exp() * (lp + H[:, None]) / T
+    # log p(x) of up to 32 comes rounded (2^-20), and is part of every exponent; t of up to 2 is
+    # rounded three times, ex2.approx 2^-22
+    size = lp.exp() * ((lp + H[:, None]).abs() + 1) / T
+    assert ((got - want).abs() <= size * (2.0 ** -20 + 2.0 ** -21 + 2.0 ** -22)).all()
+
+
 @pytest.mark.parametrize("V,dtype", [(17000, BF16), (9001, F32), (3000, F32)])
 def test_sums_of_long_padded_rollouts(V, dtype):
     """The log-sum-exps of rows without a token are -inf, all others numbers; a
