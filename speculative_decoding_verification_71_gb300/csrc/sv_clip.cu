@@ -208,8 +208,15 @@ __global__ void __launch_bounds__(kClipThreads, 4) clip_norm_kernel(const __grid
   }
 }
 
-// The norm, the same in every CTA.
-__device__ __forceinline__ float clip_total(const double* work, int ctas, int kind) {
+// The norm, the same in every CTA, and the factor that `max_norm` makes of it, which
+// is rounded to float32 once: three roundings in turn would be common to all
+// gradients.  By one thread (64-bit roots and divisions by all of them are
+// microseconds); the others get it through shared memory.
+struct ClipTotal {
+  float norm, scale;
+};
+__device__ __forceinline__ ClipTotal clip_total(const double* work, int ctas, int kind, float max_norm) {
+  __shared__ ClipTotal total;
   ClipPart part{0.0, 0.f, 0.f, 0u};
   for (int i = threadIdx.x; i < ctas; i += kClipThreads) {
     const double v = __ldcg(work + i);
@@ -217,13 +224,19 @@ __device__ __forceinline__ float clip_total(const double* work, int ctas, int ki
     else part.top = max(part.top, __float_as_uint(static_cast<float>(v)) & 0x7fffffffu);
   }
   part = clip_block(part);
-  return kind == SV_NORM_L2 ? static_cast<float>(sqrt(part.s)) : __uint_as_float(part.top);
+  if (threadIdx.x == 0) {
+    const double norm = kind == SV_NORM_L2 ? sqrt(part.s) : static_cast<double>(__uint_as_float(part.top));
+    total.norm = static_cast<float>(norm);
+    total.scale = total.norm < INFINITY ? fminf(static_cast<float>(static_cast<double>(max_norm) / (norm + 1e-6)), 1.f) : 1.f;
+  }
+  __syncthreads();
+  return total;
 }
 
 __global__ void __launch_bounds__(kClipThreads) clip_total_kernel(const double* work, int ctas, int kind, float* norm) {
   grid_dependency_wait();
-  const float v = clip_total(work, ctas, kind);
-  if (threadIdx.x == 0) *norm = v;
+  const ClipTotal total = clip_total(work, ctas, kind, INFINITY);
+  if (threadIdx.x == 0) *norm = total.norm;
 }
 
 // Stores a vector as bfloat16 or as float32, whole.
@@ -298,9 +311,9 @@ __global__ void __launch_bounds__(kClipThreads, 4) clip_scale_kernel(const __gri
     clip_fetch(T, k, piece, w);
   }
   grid_dependency_wait();
-  const float total = clip_total(work, static_cast<int>(gridDim.x), T.kind);
-  if (blockIdx.x == 0 && threadIdx.x == 0) *norm = total;
-  const float scale = total < INFINITY ? fminf(__fdiv_rn(max_norm, __fadd_rn(total, 1e-6f)), 1.f) : 1.f;
+  const ClipTotal total = clip_total(work, static_cast<int>(gridDim.x), T.kind, max_norm);
+  if (blockIdx.x == 0 && threadIdx.x == 0) *norm = total.norm;
+  const float scale = total.scale;
   if (piece < 0 || (in_place && scale == 1.f)) return;
   if (in_place) {
     k = clip_find(T, piece);

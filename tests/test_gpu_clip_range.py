@@ -36,3 +36,23 @@ def test_many_squares_past_the_range_together(dtype, n, value):
     low, high = t.min().item(), t.max().item()
     half = 2.0 ** -8 if dtype == BF16 else 2.0 ** -24
     assert low == high and abs(low - value / 2) <= value / 2 * (1e-6 + 4 * 2.0 ** -24 + half)
+
+
+@pytest.mark.parametrize("kind", ["l2", "max"])
+@pytest.mark.parametrize("place", [False, True])
+def test_the_factor_is_rounded_once(kind, place):
+    """Gradients of one power of two: their squares' sum is exact, so the factor
+    max_norm / (norm + 1e-6) is known, and the scaled gradients show it.  To float32 it
+    is off by half a step, and a product with a power of two is exact."""
+    for n in (1, 3, 7, 1000, 4099, 100003, 5_000_001):
+        for e in (-11, 0, 3):
+            norm = 2.0 ** e * (math.sqrt(n) if kind == "l2" else 1.0)
+            for share in (0.001, 0.3, 0.77, 0.9999):
+                most = torch.tensor(norm * share).item()          # as float32
+                t = torch.full((n,), 2.0 ** e, device=DEV)
+                out = None if place else [torch.empty_like(t)]
+                got = svp.clip_gradients([t], most, kind=kind, out=out).item()
+                assert abs(got - norm) <= 2.0 ** -24 * norm
+                scaled = (t if place else out[0]) / 2.0 ** e
+                want = most / (norm + 1e-6)
+                assert (scaled.double() - want).abs().max().item() <= 2.0 ** -24 * want * (1 + 1e-6), (n, e, share)
