@@ -227,7 +227,9 @@ __device__ __forceinline__ ClipTotal clip_total(const double* work, int ctas, in
   if (threadIdx.x == 0) {
     const double norm = kind == SV_NORM_L2 ? sqrt(part.s) : static_cast<double>(__uint_as_float(part.top));
     total.norm = static_cast<float>(norm);
-    total.scale = total.norm < INFINITY ? fminf(static_cast<float>(static_cast<double>(max_norm) / (norm + 1e-6)), 1.f) : 1.f;
+    total.scale = 1.f;
+    if (max_norm < INFINITY && total.norm < INFINITY)
+      total.scale = fminf(static_cast<float>(static_cast<double>(max_norm) / (norm + 1e-6)), 1.f);
   }
   __syncthreads();
   return total;

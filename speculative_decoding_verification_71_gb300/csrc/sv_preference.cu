@@ -44,7 +44,9 @@ struct PairParams {
 constexpr int kPairThreads = 256, kPairWarps = kPairThreads / 32;
 
 // log(1 + e^x) and 1 / (1 + e^-x).  The sums and h are taken in 64 bits, what
-// follows in 32: with 64-bit exponentials in every thread a pair took 14 us.
+// follows, a few float32 steps of a float32 output, in 32: with 64-bit exponentials
+// in every thread a pair took 14 us, in one thread the whole call 2 us more (23.6 for
+// 21.7, which brought the loss from 2e-7 to 6e-8 of itself).
 __device__ __forceinline__ float softplus(float x) { return fmaxf(x, 0.f) + log1pf(expf(-fabsf(x))); }
 __device__ __forceinline__ float sigmoid(float x) { return __fdiv_rn(1.f, 1.f + expf(-x)); }
 
