@@ -455,7 +455,7 @@ extern "C" sv_status sv_clip_gradients(int n, const void* const* grads, const lo
   const bool scales = outs || max_norm < INFINITY;
   long long pieces = 0;
   ClipRange* ranges = new (std::nothrow) ClipRange[2 * static_cast<size_t>(n) + 2];
-  if (!ranges) return SV_ERR_INVALID_ARG;
+  if (!ranges) return SV_ERR_CUDA;
   int used = 0;
   bool ok = true;
   auto range_of = [&](const void* p, long long size, int bytes, bool written) {
