@@ -832,7 +832,7 @@ def preference_loss(logits, tokens, ref_logp, weights, beta=0.1, temperature=1.0
         logp = torch.empty(per, dtype=f32, device=dev)
         margin = torch.empty((n,), dtype=f32, device=dev)
         loss = torch.empty_like(margin)
-        work = torch.empty((n_seq * (4 * t_len + 1),), dtype=f32, device=dev)   # sv_preference_work
+        work = torch.empty((lib.sv_preference_work(n, t_len),), dtype=f32, device=dev)
         g = _gradient_of(logits, grad, out)
         st = lib.sv_preference_loss(n, t_len, V, code, logits.data_ptr(), tokens_at, ref_at, weights_at, temperature, beta,
                                     _PREFERENCES[kind], smoothing, int(bool(average)), logp.data_ptr(),

@@ -95,3 +95,14 @@ def test_the_same_bits_without_the_rows_in_between(V, dtype):
     part = svp.preference_loss(z[rows].contiguous(), x[rows], torch.zeros(len(rows), device=DEV), w[:len(keep)], beta=0.3)
     for a, b, at in zip(pairs, part, (rows, keep, keep, rows)):
         assert torch.equal(a[at], b)
+
+
+def test_the_workspace_is_what_the_library_asks_for(monkeypatch):
+    """No formula of its own in the binding."""
+    lib, asked = svp.load_library(), []
+    real = lib.sv_preference_work
+    monkeypatch.setattr(lib, "sv_preference_work", lambda n, t: asked.append((n, t)) or real(n, t))
+    z = torch.zeros(6, 5, 40, device=DEV)
+    x, w = torch.zeros(6, 5, dtype=torch.int32, device=DEV), torch.zeros(6, device=DEV)
+    svp.preference_loss(z, x, w, w[:3])
+    assert asked == [(3, 5)]
