@@ -459,10 +459,12 @@ sv_status spec_kd_top_loss(int n_seq, int t_len, int V, sv_dtype dtype, int K, c
  * enters.  So does a derivative past float32's range in the gradient.  A token at
  * logit -inf has log-probability -inf.  At most 2^28 rows, V * sizeof(dtype) <=
  * 1 MiB, temperature as for spec_kd_loss.  Asynchronous on `stream`; no context,
- * no allocation; every sum is taken in a fixed order.  Host-checkable errors
- * return SV_ERR_INVALID_ARG and launch nothing.
- * Rows longer than 32 KB are staged; a wait for staged logits that lasts longer
- * than 1 s is given up.  There is no status for it: the row and every later row
+ * no allocation; every sum is taken in a fixed order, which depends on the sizes and
+ * on the rows' addresses modulo 16.  A weight of 0 takes finite losses and gradients
+ * out, not those that are NaN or infinite (0 times them is NaN): there negative
+ * tokens do.  Host-checkable errors return SV_ERR_INVALID_ARG and launch nothing.
+ * Rows of up to 32736 bytes stay in registers, longer ones may be staged; a wait
+ * for staged logits that lasts longer than 1 s is given up.  There is no status for it: the row and every later row
  * (with a token) of the CTAs concerned come out as NaN, and so do the losses that
  * they enter; no copy is left in flight and the next call is not affected.
  * ------------------------------------------------------------------------ */
@@ -562,7 +564,9 @@ sv_status sv_preference_loss(int n_pair, int t_len, int V, sv_dtype dtype, const
  * not overlap anything else that is read or written, outs[i] = grads[i] with
  * one type apart.  Squares are summed in fp32 by threads where that loses
  * nothing, else in fp64, and joined in fp64, in a fixed order that depends on
- * the sizes alone.  The host arrays are read during the call. */
+ * the sizes, the types and the addresses modulo 16 alone.  The factor is taken in
+ * fp64 and rounded to fp32 once.  The host arrays are read during the call; where
+ * the host has no memory for a table of them the answer is SV_ERR_CUDA. */
 typedef enum { SV_NORM_L2 = 0, SV_NORM_MAX = 1 } sv_norm_kind;
 #define SV_CLIP_WORK 608
 
@@ -573,9 +577,9 @@ sv_status sv_clip_gradients(int n, const void *const *grads, const long long *si
 /* Test hook: the limit, in nanoseconds, of spec_kd_loss's and
  * spec_kd_top_loss's waits for staged logits, and of sv_token_logp's,
  * sv_policy_loss's and sv_preference_loss's, in the calls of the whole process
- * from here on (default 1 s).  0 makes every such wait report expiry; rows that
- * stay in registers (32 KB; spec_kd_loss has none) wait for nothing.  Negative
- * restores the default. */
+ * from here on (default 1 s).  0 makes every such wait report expiry; rows of up
+ * to 32736 bytes stay in registers and wait for nothing (spec_kd_loss stages every
+ * row).  Negative restores the default. */
 sv_status spec_kd_set_wait_limit_ns(long long ns);
 
 /* Test hook: the limit, in nanoseconds, of each bounded wait for staged logits

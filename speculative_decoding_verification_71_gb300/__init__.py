@@ -711,7 +711,8 @@ def token_logp(logits, tokens, temperature=1.0, entropy=False, stream=None):
     the reference.  logits [n_seq, t_len, V] float32 or bfloat16; tokens
     [n_seq, t_len] int32, negative where a row has none (``verify``'s
     out_tokens will do).  Returns (logp, entropy or None, lse), each [n_seq,
-    t_len] float32; 0, 0 and -inf where there is no token."""
+    t_len] float32; 0, 0 and -inf where there is no token.  Nothing is recorded
+    for automatic differentiation: ``token_logp_grad`` is the gradient."""
     lib = load_library()
     (n_seq, t_len, V), dev, code = _logit_rows("logits", logits)
     tokens_at = _address("tokens", tokens, torch.int32, (n_seq, t_len), dev)
@@ -769,7 +770,8 @@ def policy_loss(logits, tokens, advantages, weights, old_logp=None, ref_logp=Non
     ratio is 1).  ``out=logits`` overwrites the logits with the gradient.
     Returns (logp [n_seq, t_len], entropy [n_seq, t_len] or None, row_loss
     [n_seq, t_len], loss [n_seq], grad [n_seq, t_len, V] or None); the entropy
-    is there where it is asked for or has a coefficient."""
+    is there where it is asked for or has a coefficient.  Nothing is recorded for
+    automatic differentiation: ``logits.backward(grad)`` goes on from there."""
     lib = load_library()
     (n_seq, t_len, V), dev, code = _logit_rows("logits", logits)
     f32, per = torch.float32, (n_seq, t_len)
@@ -814,7 +816,9 @@ def preference_loss(logits, tokens, ref_logp, weights, beta=0.1, temperature=1.0
     reference (``token_logp(...)[0].sum(1)``, their mean over the tokens with
     ``average``); weights [n] float32; kind "sigmoid", "hinge" or "ipo".
     ``out=logits`` overwrites the logits with the gradient.  Returns (logp
-    [2 n, t_len], margin [n], loss [n], grad [2 n, t_len, V] or None)."""
+    [2 n, t_len], margin [n], loss [n], grad [2 n, t_len, V] or None).  Nothing is
+    recorded for automatic differentiation: ``logits.backward(grad)`` goes on
+    from there."""
     lib = load_library()
     (n_seq, t_len, V), dev, code = _logit_rows("logits", logits)
     if n_seq % 2:
