@@ -13,7 +13,7 @@
 // last ones are still in L2 then.
 //
 // 2.5 GB of bf16: the norm 349 us, 7.1 TB/s.  0.7 GB into scaled copies: 345 us, 6.1
-// TB/s of two reads and a write.
+// TB/s of two reads and a write.  2.5 GB in place, the norm exceeded: 1146 us, 6.6.
 
 #include <cuda_runtime.h>
 

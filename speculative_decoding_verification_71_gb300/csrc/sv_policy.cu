@@ -122,7 +122,7 @@ __device__ __forceinline__ void zero_row(unsigned char* grad, int V, int tid, in
 // sixteen warps an SM keep 128 KB on their way.  A row is read once, its warps meet
 // at one barrier, and no CTA waits for another.  Bound by instructions: what a row's
 // numbers take beside its logits, by every warp of its own.  50000 rows of 4000 bf16
-// logits with the policy loss's gradient: 162 us, 4.9 TB/s; 200000 of 1000: 334 us, 2.4
+// logits with the policy loss's gradient: 153 us, 5.2 TB/s; 200000 of 1000: 325 us, 2.5
 // TB/s (a CTA to a row, read twice: 385 and 1253 us).
 constexpr int kShThreads = 128, kShWarps = kShThreads / 32, kShPerLane = 16, kShChunk = 4;
 constexpr int kShPerSm = 4;                                 // CTAs
@@ -248,8 +248,8 @@ __global__ void __launch_bounds__(kShThreads, kShPerSm) token_short_kernel(const
 // longer at work): every CTA counts the tokens of a window of rows and lists its
 // own.  Rows without one are zero-filled by single CTAs in between.
 //
-// 4096 rows of 151936 bf16 logits: log-probabilities 188 us, 6.6 TB/s; with the policy
-// loss's gradient 420 us, 5.9 TB/s of each logit read and each gradient written once.
+// 4096 rows of 151936 bf16 logits: log-probabilities 186 us, 6.7 TB/s; with the policy
+// loss's gradient 418 us, 6.0 TB/s of each logit read and each gradient written once.
 // Bound there by instructions (17 a logit over both passes, half of them beside the
 // arithmetic) and by eight SMs that clusters of four leave idle.
 //
@@ -714,7 +714,8 @@ __global__ void __launch_bounds__(Rg<GRAD>::kThreads, Rg<GRAD>::kPerSm)
 // row's numbers, then its token's logit).  In place the token's logit may be
 // overwritten by another piece's CTA, so there the row's CTAs are a cluster, which
 // goes on when all of them have it (what the preference loss keeps of a row has no
-// need of that logit).  4096 rows of 151936 bf16: 387 us, 6.4 TB/s.
+// need of that logit).  4096 rows of 151936 bf16: 384 us, 6.5 TB/s;
+// 50000 of 4000 259 us, 3.1 TB/s.
 struct GradParams {
   const unsigned char* logits;
   const int* tokens;
@@ -850,7 +851,8 @@ cudaError_t launch_ring(const RowParams& p, int rows, cudaStream_t s) {
   // busy as the memory, the smallest of them that fits two parts, so that one row is
   // summed while the other's gradient is written (1024 rows of 151936: 115 us, of
   // 128256 102 us; with one part 124 and 108); in float32 the smallest that fits one
-  // (1024 rows of 50001: 81 us, with two parts 85).
+  // (1024 rows of 50001: 83 us, with two parts 86; 4096 of 100003 552 and 616; 512 of
+  // 50001 the other way, 51 and 48).
   const int slots = static_cast<int>((row_bytes + kRgSlotBytes - 1) / kRgSlotBytes), kept = Rg<GRAD>::kSlots - 1;
   auto fits = [&](int ctas, int most) { return (slots + ctas - 1) / ctas <= most; };
   int ctas = 1;
