@@ -103,8 +103,14 @@ __device__ __forceinline__ void policy_row(const PolicyArgs& P, const PolicyRow&
   loss = R.valid ? -gain : NAN;
   if (P.ref_logp) {
     const float d = __fsub_rn(__fsub_rn(row.ref_logp, R.logp), R.logp_rest), up = expm1f(d);
-    loss = __fmaf_rn(P.kl, kl_term(d, up), loss);
-    slope = __fmaf_rn(-P.kl, up, slope);
+    if (up == INFINITY && d < INFINITY) {     // likewise
+      const float half = expf(0.5f * d), pull = P.kl * half * half;
+      loss += pull;
+      slope -= pull;
+    } else {
+      loss = __fmaf_rn(P.kl, kl_term(d, up), loss);
+      slope = __fmaf_rn(-P.kl, up, slope);
+    }
   }
   if (ENT) loss = __fmaf_rn(-P.entropy, R.entropy(), loss);
 }

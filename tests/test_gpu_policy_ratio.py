@@ -46,3 +46,21 @@ def test_ratios_past_the_range(V, per_token):
     # with the other clip such a row is held
     _, _, row, _, grad = svp.policy_loss(z, x, A, w, old_logp=old, dual_clip=3.0)
     assert row[3, 0].item() == pytest.approx(3e-12, rel=1e-6) and (grad == 0).all()
+
+
+@pytest.mark.parametrize("V", [100, 40008])
+def test_divergences_past_the_range(V):
+    """e^d with d = ref - log p above 88: where kl_coef times it is in range, so are
+    the loss and the gradient.  d is rounded twice (2 x 2^-24 x 95 of the product)."""
+    z = torch.full((3, 1, V), -math.inf, device=DEV)
+    z[:, :, 0] = 0.0
+    z[:, :, 1] = torch.tensor([-90.0, -95.0, -300.0], device=DEV)[:, None]
+    x = torch.ones(3, 1, dtype=torch.int32, device=DEV)
+    ref = torch.zeros(3, 1, device=DEV)
+    w = torch.ones(3, device=DEV)
+    _, _, row, loss, grad = svp.policy_loss(z, x, 0 * w, w, ref_logp=ref, kl_coef=1e-3)
+    for i, d in enumerate((90.0, 95.0)):
+        big = 1e-3 * math.exp(d)
+        assert row[i, 0].item() == pytest.approx(big, rel=2e-5) and loss[i].item() == pytest.approx(big, rel=2e-5)
+        assert grad[i, 0, 1].item() == pytest.approx(-big, rel=2e-5) and grad[i, 0, 0].item() == pytest.approx(big, rel=2e-5)
+    assert row[2, 0].item() == math.inf and grad[2].isnan().all()       # past the range: as documented
